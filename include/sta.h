@@ -370,6 +370,174 @@ STA_API sta_status sta_forward_noalloc(const sta_geom* g, int32_t batch, int32_t
                                        const void* v, void* o, float* lse, int32_t head_dim,
                                        float softmax_scale, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The prompt side: attention of packed sequences of different lengths, and
+ * attention over a cache held in 8 bits.
+ *
+ * A video model that runs the calls above conditions on text: prompts go
+ * through a causal language model with grouped heads, several of different
+ * lengths packed one after another, are continued token by token over a
+ * cache, and the video's tokens attend to the text's keys.  These calls are
+ * the attention of that part.  They need no plan: the sequences' bounds are
+ * device arrays which the kernels read, so one CUDA graph serves any lengths.
+ * Nothing is kept between calls: all scratch is in the caller's workspace,
+ * which calls running at the same time must not share (nor may two captured
+ * graphs that are replayed at the same time).  Work is deterministic: the same
+ * inputs give the same bits.
+ *
+ * Tensors are token-major, [tokens, heads, head_dim] with free strides: */
+typedef struct {
+    void* data;           /* device bf16, 16-byte aligned */
+    int64_t token_stride; /* elements from a token to the next */
+    int64_t head_stride;  /* elements from a head to the next; the last dimension is contiguous */
+} sta_rows;               /* both strides positive multiples of 8 (so the parts of one fused projection do) */
+
+/* The problem.  Sequence b's queries are rows cu_q[b] .. cu_q[b+1] - 1 of the
+ * query-like tensors, its keys rows cu_k[b] .. cu_k[b+1] - 1 of the key-like
+ * ones; both arrays start at 0 and do not decrease.  Query head h uses key head
+ * h / (heads / kv_heads).  Query i of a sequence of nq queries and nk keys sees
+ * all nk keys, or with `causal` the first nk - nq + i + 1 (the last query sees
+ * every key); a query that sees none gives O = 0, LSE = -inf and no gradient.
+ * Bounds that decrease or reach past the tensors are cut to them on the device
+ * (nothing is read or written outside) and reported by
+ * sta_operator_status as BOUNDS. */
+typedef struct {
+    int32_t batch;            /* sequences, >= 0 */
+    int32_t heads, kv_heads;  /* heads a multiple of kv_heads, at most 128 query heads to a key head */
+    int32_t head_dim;         /* 64 or 128 */
+    int64_t tokens_q;         /* rows of q, o, dout, dq; columns of lse */
+    int64_t tokens_k;         /* rows of k, v, dk, dv */
+    const int32_t* cu_q;      /* device [batch + 1] */
+    const int32_t* cu_k;      /* device [batch + 1]; may be cu_q itself */
+    int32_t causal;           /* 0 or 1 */
+    int32_t clear_tail;       /* output rows behind the last sequence: 0 left as they were, 1 zeros (lse: -inf) */
+    float softmax_scale;      /* finite and > 0 */
+} sta_packed;
+
+/* Bytes of workspace that sta_packed_forward (backward = 0) or
+ * sta_packed_backward (1) needs for this problem (its pointers are not read).
+ * Host only.  INVALID_ARG / UNSUPPORTED as the calls themselves. */
+STA_API sta_status sta_packed_workspace(const sta_packed* p, int32_t backward, int64_t* bytes);
+
+/* O = softmax(scale Q K^T) V per sequence and head, and the natural-log
+ * log-sum-exp of the scaled scores.
+ *   q, o    : [tokens_q, heads, d]     k, v : [tokens_k, kv_heads, d]
+ *   lse     : device fp32 [heads, tokens_q], contiguous (written)
+ *   workspace, workspace_bytes: device, 256-byte aligned, at least
+ *             sta_packed_workspace bytes; need not be initialised
+ * Scores, softmax statistics and O accumulate in fp32; P enters P V as bf16.
+ * A masked key's score never counts, whatever it holds, and the rows of other
+ * sequences and behind the last one are never mixed in; only a non-finite V
+ * row can reach the other queries of its own sequence's 128-key block (0 x
+ * inf).  Every sequence being empty, or batch 0, is not an error.
+ * Errors: INVALID_ARG (null, misaligned or short buffers, bad sizes, strides
+ * or scale), UNSUPPORTED (head_dim, more than 128 query heads to a key head,
+ * sizes past 2^31 - 1 rows of work), CUDA. */
+STA_API sta_status sta_packed_forward(const sta_packed* p, const sta_rows* q, const sta_rows* k, const sta_rows* v,
+                                      const sta_rows* o, float* lse, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
+
+/* Gradients of sta_packed_forward (formulas as sta_backward; the gradients of
+ * a key head are summed over its query heads in fp32).  o and lse as written
+ * by the forward for the same problem; dout, dq like q, dk, dv like k; the
+ * outputs are distinct from every input.  Every row of every sequence is
+ * written, a key that no query sees with zeros.  P and dS enter the products as
+ * bf16 with fp32 accumulation.  No atomics on results. */
+STA_API sta_status sta_packed_backward(const sta_packed* p, const sta_rows* q, const sta_rows* k, const sta_rows* v,
+                                       const sta_rows* o, const sta_rows* dout, const float* lse, const sta_rows* dq,
+                                       const sta_rows* dk, const sta_rows* dv, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+
+/* A paged cache of keys and values in e4m3 (4 exponent, 3 mantissa bits), one
+ * fp32 scale for each block of tokens and head: value = code * scale. */
+typedef struct {
+    int32_t blocks;       /* blocks in the pool, >= 1 */
+    int32_t block_tokens; /* 16, 32, 64 or 128 */
+    int32_t kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    void* k_codes;        /* device [blocks, kv_heads, block_tokens, head_dim] e4m3, contiguous, 16-byte aligned */
+    void* v_codes;
+    float* k_scales;      /* device [blocks, kv_heads]; finite and > 0 in blocks that hold tokens */
+    float* v_scales;
+} sta_cache;
+
+/* Write new tokens' keys and values into the cache.
+ *   k, v  : [tokens, kv_heads, d]
+ *   slots : device int64 [tokens]: block * block_tokens + offset of each token;
+ *           negative: the token is not written
+ * A block's scale is the smallest power of two 2^e, -60 <= e <= 120, with
+ * |x| <= 448 * 2^e for what the block holds, so scaling is exact and the
+ * only rounding is e4m3's (to nearest, ties to even).  When a token raises it,
+ * the codes already in the block are scaled down and rounded again; it never
+ * falls, except that writing offset 0 starts the block anew (its old scale and
+ * codes no longer count).  NaN stays NaN; an infinity sets e = 120.
+ * The tokens of one block stand next to each other in `slots`, in rising order
+ * (as sta_cache_extend writes them), and the caller lets no two blocks' runs
+ * name the same block.  A slot outside the pool is skipped and reported by
+ * sta_operator_status as BOUNDS.  One kernel, no workspace. */
+STA_API sta_status sta_cache_append(const sta_cache* c, const sta_rows* k, const sta_rows* v, int64_t tokens,
+                                    const int64_t* slots, void* stream);
+
+/* Attention over the cache, causal: the serving form of sta_packed_forward,
+ * for one or a few queries of each sequence.
+ *   p            : batch, heads, kv_heads, head_dim, tokens_q, cu_q (NULL: one
+ *                  query for each sequence, tokens_q = batch), clear_tail and
+ *                  softmax_scale as above; cu_k, tokens_k, causal are not read
+ *   lengths      : device int32 [batch]: tokens of each sequence in the cache,
+ *                  its queries' own among them
+ *   block_tables : device int32 [batch, table_stride]: the blocks of each
+ *                  sequence in order; the first table_width of a row count
+ *   q, o, lse    : as sta_packed_forward
+ * Query i of nq sees the first lengths[b] - nq + i + 1 tokens.  Products with
+ * K and V are of fp16 operands (the codes exactly, Q scaled by a power of two
+ * for each row, P rounded) with fp32 accumulation.  What a block holds behind
+ * its sequence's last token is never mixed in.  Tokens of a block whose id is
+ * outside the pool are not seen, nor are tokens past table_width blocks; both
+ * are reported by sta_operator_status as BOUNDS.  The keys are split over the
+ * GPU and joined in a fixed order.  Workspace: sta_cache_workspace bytes,
+ * 256-byte aligned, need not be initialised. */
+STA_API sta_status sta_cache_workspace(const sta_cache* c, const sta_packed* p, int64_t* bytes);
+STA_API sta_status sta_cache_attention(const sta_cache* c, const sta_packed* p, const int32_t* lengths,
+                                       const int32_t* block_tables, int32_t table_width, int64_t table_stride,
+                                       const sta_rows* q, const sta_rows* o, float* lse, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+
+/* Block tables and slot maps for the next step, built on the GPU: gives each
+ * request the blocks that its new tokens need and takes back those of requests
+ * that ended.
+ *   new_tokens   : device int32 [batch]: tokens to add (>= 0), or negative: the
+ *                  request has ended, its blocks return to the free stack
+ *   lengths      : device int32 [batch]: tokens held now
+ *   lengths_out  : device int32 [batch] (written; may be `lengths`): after the
+ *                  step; 0 for ended requests, whose table rows stay as they were
+ *   block_tables : device int32 [batch, table_stride], table_width entries
+ *                  count: read for held blocks, written for new ones
+ *   free_blocks  : device int32 [pool]: the free stack's first free_count[0]
+ *                  entries are free block ids (read; returned ids are pushed)
+ *   free_count, free_count_out: device int32 [1] (may be the same)
+ *   slots        : device int64 [max_slots] (written): the new tokens' slots,
+ *                  request by request, then -1
+ *   cu_new       : device int32 [batch + 1] (written): bounds of each request's
+ *                  new tokens
+ *   shortage     : device int32 [1] (written): 0 done; n > 0: n blocks are
+ *                  missing; -1: a request outgrows its table, `max_slots`, the
+ *                  pool or 2^31 - 1 tokens, or a length or count is out of
+ *                  range.  Unless 0, nothing changed: the lengths and the count
+ *                  out are those in, no request has new tokens, slots are -1.
+ * Blocks are returned first, request by request in table order; then request
+ * by request each new block is taken from the top of the stack.  One kernel. */
+STA_API sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* new_tokens,
+                                    const int32_t* lengths, int32_t* lengths_out, int32_t* block_tables,
+                                    int32_t table_width, int64_t table_stride, int32_t* free_blocks, int32_t pool,
+                                    const int32_t* free_count, int32_t* free_count_out, int64_t* slots,
+                                    int64_t max_slots, int32_t* cu_new, int32_t* shortage, void* stream);
+
+/* Synchronise `stream`, then report (and clear) the first asynchronous error of
+ * the calls of this part on the current device: CUDA, BOUNDS (bounds, block ids
+ * or slots out of range, cut as described) or TIMEOUT.  The device has one
+ * status word for these calls, whichever stream they ran on. */
+STA_API sta_status sta_operator_status(void* stream);
+
 /* Synchronise `stream`, then report (and clear) the first asynchronous error
  * of work enqueued with this plan: CUDA for a launch or execution fault,
  * BOUNDS when a kernel of the debug build found a plan index out of range

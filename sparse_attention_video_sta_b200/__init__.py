@@ -19,6 +19,11 @@ The functions carry the C names:
 tensors, and ``StaAttention`` wraps both as a ``torch.autograd.Function``.
 ``sta_window_stats`` / ``sta_window_search`` profile candidate windows per head
 (attention recall and output error against full attention).
+
+The prompt side (``_prompt.py``): ``sta_packed_attention`` / ``..._backward`` and
+``StaPackedAttention`` for packed sequences of different lengths with grouped
+heads, ``sta_cache_extend`` / ``sta_cache_append`` / ``sta_cache_attention`` for
+serving over a paged 8-bit cache.
 """
 from __future__ import annotations
 
@@ -28,12 +33,17 @@ import os
 
 import torch
 
+from . import _prompt
+
 __all__ = [
     "StaError", "Plan", "sta_plan", "sta_plan_host", "sta_tile_reorder", "sta_tile_unreorder",
     "sta_forward", "sta_forward_raster", "sta_forward_noalloc", "sta_last_device_status",
     "sta_status_string", "sta_debug_inject_timeout", "sta_attention", "raster_supported", "library_path", "EXPORTED_SYMBOLS",
     "sta_backward", "sta_attention_backward", "StaAttention", "sta_window_stats", "sta_window_search",
     "Pipe", "sta_pipe_create", "sta_backward_raster", "sta_window_pick",
+    "sta_packed_forward", "sta_packed_backward", "sta_packed_attention", "sta_packed_attention_backward",
+    "StaPackedAttention", "sta_cache_append", "sta_cache_attention", "sta_cache_extend", "CacheStep",
+    "sta_operator_status",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -57,7 +67,7 @@ EXPORTED_SYMBOLS = (
     "sta_last_error_detail", "sta_plan_key_query", "sta_backward", "sta_window_stats",
     "sta_pipe_create", "sta_pipe_submit", "sta_pipe_wait", "sta_pipe_destroy", "sta_backward_raster",
     "sta_plan_backward_items", "sta_plan_validate", "sta_debug_plan_poke", "sta_window_pick",
-)
+) + _prompt.SYMBOLS
 
 
 class _Geom(ctypes.Structure):
@@ -139,6 +149,12 @@ class StaError(RuntimeError):
 def _check(status: int, what: str) -> None:
     if status != STA_OK:
         raise StaError(status, what)
+
+
+_prompt.bind(_lib, _check)
+from ._prompt import (  # noqa: E402  (after the library is loaded)
+    CacheStep, StaPackedAttention, sta_cache_append, sta_cache_attention, sta_cache_extend, sta_operator_status,
+    sta_packed_attention, sta_packed_attention_backward, sta_packed_backward, sta_packed_forward)
 
 
 def _geom(latent, tile) -> _Geom:

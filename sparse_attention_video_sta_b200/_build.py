@@ -14,8 +14,10 @@ LIB_PATH = os.path.join(PKG_DIR, "libsta.so")
 # (STA_DEBUG_BOUNDS; see csrc/sta_bounds.cuh).
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libsta_debug.so")
 
-SOURCES = ["sta_api.cu", "sta_permute.cu", "sta_forward.cu", "sta_backward.cu", "sta_search.cu", "sta_pipe.cu", "sta_noalloc.cu"]
-HEADERS = ["sta_internal.h", "sta_ptx.cuh", "sta_raster.cuh", "sta_wait.cuh", "sta_bounds.cuh"]
+SOURCES = ["sta_api.cu", "sta_permute.cu", "sta_forward.cu", "sta_backward.cu", "sta_search.cu", "sta_pipe.cu", "sta_noalloc.cu",
+           "sta_packed.cu", "sta_packed_backward.cu", "sta_cache.cu", "sta_cache_attention.cu"]
+HEADERS = ["sta_internal.h", "sta_ptx.cuh", "sta_raster.cuh", "sta_wait.cuh", "sta_bounds.cuh",
+           "sta_ops.h", "sta_ops.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -41,7 +43,7 @@ def up_to_date(path: str = LIB_PATH) -> bool:
 def _compile(path: str, extra, verbose: bool):
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = path + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC,
+    cmd = [nvcc, "--threads", "0", *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC,
            *[os.path.join(CSRC, f) for f in SOURCES], "-o", tmp]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)

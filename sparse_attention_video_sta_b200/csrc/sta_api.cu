@@ -21,6 +21,7 @@
 
 #include "sta.h"
 #include "sta_internal.h"
+#include "sta_ops.h"
 
 namespace {
 
@@ -476,6 +477,20 @@ sta_status backward_common(sta_plan_t p, const void* q, const void* k, const voi
 }
 
 }  // namespace
+
+namespace sta {
+
+sta_status op_cuda_status(cudaError_t e) { return cuda_status(e); }
+
+cudaError_t op_begin() {
+    int dev = -1;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (cudaError_t e = make_context_current(dev); e != cudaSuccess) return e;
+    clear_stale_error();
+    return cudaSuccess;
+}
+
+}  // namespace sta
 
 extern "C" {
 

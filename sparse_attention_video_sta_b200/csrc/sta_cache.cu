@@ -1,0 +1,392 @@
+// sta_cache.cu -- the 8-bit paged cache: writing tokens into it, and the block
+// tables and slot maps of a serving step.  (Attention over it: sta_cache_attention.cu.)
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sta_ops.h"
+#include "sta_ops.cuh"
+
+namespace sta {
+
+bool cache_ok(const sta_cache* c) {
+    if (c == nullptr || c->blocks < 1 || c->kv_heads < 1) return false;
+    for (const void* p : {(const void*)c->k_codes, (const void*)c->v_codes})
+        if (p == nullptr || reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+    for (const void* p : {(const void*)c->k_scales, (const void*)c->v_scales})
+        if (p == nullptr || reinterpret_cast<uintptr_t>(p) % 4 != 0) return false;
+    return true;
+}
+
+bool cache_supported(const sta_cache* c) {
+    const int bt = c->block_tokens;
+    return (bt == 16 || bt == 32 || bt == 64 || bt == 128) && (c->head_dim == 64 || c->head_dim == 128) &&
+           c->kv_heads <= 65535;
+}
+
+namespace {
+
+// ---------------------------------------------------------------- append
+constexpr int kAppendThreads = 128;
+
+// Exponent e of the smallest power of two 2^e, -60 <= e <= 120, with
+// amax <= 448 * 2^e = 1.75 * 2^(e + 8).
+__device__ int scale_exponent(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int e = int(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, -60), 120);
+}
+
+// Codes of 8 values, already divided by their scale.
+__device__ uint2 codes8(const float (&x)[8]) {
+    return make_uint2(uint32_t(ops::e4m3x2(x[0], x[1])) | uint32_t(ops::e4m3x2(x[2], x[3])) << 16,
+                      uint32_t(ops::e4m3x2(x[4], x[5])) | uint32_t(ops::e4m3x2(x[6], x[7])) << 16);
+}
+
+// One CTA takes the runs (tokens of one block, next to each other) that begin
+// among its `range` tokens, for one head of K or V.  A run's values stay in
+// registers between the reduction of their maximum and their rounding, so each
+// is read once: 128 threads hold a block of 128 tokens x 128 in 64 registers.
+// Bound by HBM: 2 bytes read and 1 written for each value.
+template <int D, int BT>
+__global__ void __launch_bounds__(kAppendThreads)
+cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* __restrict__ slots, int range,
+                    uint32_t* status) {
+    constexpr int kPer = D / 8;                          // threads for one token
+    constexpr int kStep = kAppendThreads / kPer;         // tokens in one pass
+    constexpr int kPasses = BT / kStep > 0 ? BT / kStep : 1;
+    __shared__ int sh_n;
+    __shared__ int sh_off[BT + 1];
+    __shared__ float sh_max[kAppendThreads / 32];
+    const int tid = threadIdx.x, h = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+    const Rows x = is_v ? v : k;
+    uint8_t* codes = static_cast<uint8_t*>(is_v ? c.v_codes : c.k_codes);
+    float* scales = is_v ? c.v_scales : c.k_scales;
+    const int64_t n_slots = int64_t(c.blocks) * BT;
+    const int64_t t0 = int64_t(blockIdx.x) * range, t1 = min(t0 + range, tokens);
+    for (int64_t t = t0; t < t1; ++t) {
+        const int64_t s = slots[t];
+        if (s >= n_slots && tid == 0) atomicOr(status, kDevBounds);
+        if (s < 0 || s >= n_slots) continue;
+        const int64_t blk = s / BT;
+        if (t > 0) {
+            const int64_t before = slots[t - 1];
+            if (before >= 0 && before / BT == blk) continue;  // inside a run that began earlier
+        }
+        // ---- the run's length and offsets
+        if (tid == 0) sh_n = BT;
+        __syncthreads();
+        for (int i = tid; i < BT + 1; i += kAppendThreads) {
+            const int64_t si = t + i < tokens ? slots[t + i] : -1;
+            const bool in = si >= 0 && si / BT == blk;
+            sh_off[i] = in ? int(si % BT) : -1;
+            if (!in) atomicMin(&sh_n, i);
+        }
+        __syncthreads();
+        const int n = sh_n;
+        const int col = (tid % kPer) * 8;
+        uint4 raw[kPasses];
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int j = i * kStep + tid / kPer;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (j < n) raw[i] = __ldg(reinterpret_cast<const uint4*>(x.p + (t + j) * x.ts + h * x.hs + col));
+        }
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // fmaxf leaves NaN out
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+        }
+        for (int i = 16; i > 0; i >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, i));
+        if (tid % 32 == 0) sh_max[tid / 32] = amax;
+        __syncthreads();
+        amax = fmaxf(fmaxf(sh_max[0], sh_max[1]), fmaxf(sh_max[2], sh_max[3]));
+        // ---- the block's scale
+        const int64_t at = blk * c.kv_heads + h;
+        float scale = ldexpf(1.0f, scale_exponent(amax));
+        uint8_t* page = codes + at * (BT * D);
+        if (sh_off[0] != 0) {  // the block holds tokens already
+            float old = scales[at];
+            if (!(old > 0.0f) || isinf(old)) old = ldexpf(1.0f, -60);
+            if (scale > old) {
+                const float ratio = old / scale;
+                for (int i = tid; i < BT * D / 8; i += kAppendThreads) {
+                    uint2 u = reinterpret_cast<uint2*>(page)[i];
+                    float y[8];
+                    ops::e4m3_floats(u.x, y[0], y[1], y[2], y[3]);
+                    ops::e4m3_floats(u.y, y[4], y[5], y[6], y[7]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] *= ratio;
+                    reinterpret_cast<uint2*>(page)[i] = codes8(y);
+                }
+            } else {
+                scale = old;
+            }
+        }
+        __syncthreads();  // every thread has read the old scale, and the old codes are rewritten
+        if (tid == 0) scales[at] = scale;
+        const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0u;
+        const float inv = 1.0f / scale;  // exact for a power of two
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int j = i * kStep + tid / kPer;
+            // a slot named twice in a row keeps the later token
+            if (j >= n || (j + 1 < n && sh_off[j + 1] == sh_off[j])) continue;
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[2 * e] = __uint_as_float(w[e] << 16);
+                y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = pow2 ? y[e] * inv : y[e] / scale;
+            *reinterpret_cast<uint2*>(page + sh_off[j] * D + col) = codes8(y);
+        }
+        __syncthreads();  // sh_off and sh_n are used again
+    }
+}
+
+template <int D, int BT>
+cudaError_t launch_append(const sta_cache& c, const Rows& k, const Rows& v, int64_t tokens, const int64_t* slots,
+                          uint32_t* status, cudaStream_t stream) {
+    // One token for each CTA while that is at most some 16 CTAs to an SM: a serving step's
+    // tokens are all in blocks of their own.  Else 16 tokens, which hold the beginning of
+    // one or two runs of a prompt.
+    const int range = tokens * c.kv_heads * 2 <= 4096 ? 1 : 16;
+    const int64_t gx = (tokens + range - 1) / range;
+    if (gx > INT32_MAX) return cudaErrorInvalidValue;
+    cache_append_kernel<D, BT><<<dim3(unsigned(gx), unsigned(c.kv_heads), 2), kAppendThreads, 0, stream>>>(
+        c, k, v, tokens, slots, range, status);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- extend
+constexpr int kExtendThreads = 1024;
+constexpr int kExtendCluster = 8;
+constexpr int kMaxRequests = 8192;
+
+struct ExtendParams {
+    int32_t batch, bt, width, pool;
+    int64_t stride, max_slots;
+    const int32_t* add;
+    const int32_t* len;
+    int32_t* len_out;
+    int32_t* tables;
+    int32_t* free_blocks;
+    const int32_t* count;
+    int32_t* count_out;
+    int64_t* slots;
+    int32_t* cu;
+    int32_t* shortage;
+};
+
+// Sums of `v` over the threads before this one; `total`: over all.
+__device__ int64_t block_scan(int64_t v, int64_t* sh, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+    for (int i = 1; i < 32; i <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, x, i);
+        if (lane >= i) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = sh[lane];
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, s, i);
+            if (lane >= i) s += y;
+        }
+        sh[lane] = s;
+    }
+    __syncthreads();
+    const int64_t before = (warp > 0 ? sh[warp - 1] : 0) + x - v;
+    total = sh[31];
+    __syncthreads();
+    return before;
+}
+
+// One cluster.  Every CTA sums the requests for itself (new tokens, blocks
+// returned, blocks needed) into its own shared memory; then all share the
+// pushes, meet, and share the tables and slots.  The reads of `len` and `count`
+// come before the cluster's meeting and their writes after it, so the outputs
+// may be the inputs.  Latency-bound: one launch in place of a chain of scans.
+__global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const ExtendParams p) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ int32_t sh[];
+    __shared__ int64_t sh_scan[32];
+    const int B = p.batch, per = (B + kExtendThreads - 1) / kExtendThreads;
+    int32_t* s_len = sh;           // tokens held
+    int32_t* s_cu = s_len + B;     // new tokens before this request; [B]: all
+    int32_t* s_back = s_cu + B + 1;  // blocks returned before it; [B]: all
+    int32_t* s_need = s_back + B + 1;  // blocks needed before it; [B]: all
+    const int tid = threadIdx.x, first = tid * per, last = min(first + per, B);
+    const int64_t row = int64_t(p.width) * p.bt;  // tokens that a table holds
+    const int32_t count = *p.count;
+    bool bad = count < 0 || count > p.pool;
+    int64_t add = 0, back = 0, need = 0;
+    for (int b = first; b < last; ++b) {
+        const int64_t n = p.len[b], a = p.add[b];
+        if (n < 0 || n > row || n + (a > 0 ? a : 0) > row || n + (a > 0 ? a : 0) > INT32_MAX) bad = true;
+        const int64_t held = (n + p.bt - 1) / p.bt;
+        s_len[b] = int32_t(n);
+        if (a < 0) {
+            back += held;
+        } else {
+            add += a;
+            need += (n + a + p.bt - 1) / p.bt - held;
+        }
+    }
+    int64_t all_add, all_back, all_need;
+    int64_t at_add = block_scan(add, sh_scan, all_add);
+    int64_t at_back = block_scan(back, sh_scan, all_back);
+    int64_t at_need = block_scan(need, sh_scan, all_need);
+    bad = __syncthreads_or(bad) || all_add > p.max_slots || all_add > INT32_MAX || count + all_back > p.pool;
+    const int64_t there = count + all_back;
+    const int64_t lack = all_need > there ? all_need - there : 0;
+    const bool fine = !bad && lack == 0;
+    // (sums that do not fit are only read where `fine`)
+    for (int b = first; b < last; ++b) {
+        const int64_t n = s_len[b], a = p.add[b], held = (n + p.bt - 1) / p.bt;
+        s_cu[b] = int32_t(at_add);
+        s_back[b] = int32_t(at_back);
+        s_need[b] = int32_t(at_need);
+        if (a < 0) {
+            at_back += held;
+        } else {
+            at_add += a;
+            at_need += (n + a + p.bt - 1) / p.bt - held;
+        }
+    }
+    if (tid == 0) {
+        s_cu[B] = int32_t(all_add);
+        s_back[B] = int32_t(all_back);
+        s_need[B] = int32_t(all_need);
+    }
+    __syncthreads();
+    const int rank = int(cluster.block_rank()), size = int(cluster.num_blocks());
+    const int warp = tid / 32, lane = tid % 32, n_warps = kExtendThreads / 32;
+    if (fine && all_back > 0)
+        for (int b = rank * n_warps + warp; b < B; b += size * n_warps)
+            for (int j = lane; j < s_back[b + 1] - s_back[b]; j += 32)
+                p.free_blocks[count + s_back[b] + j] = p.tables[b * p.stride + j];
+    cluster.sync();  // the stack is whole, and every CTA has read the lengths and the count
+    if (fine)
+        for (int b = rank * n_warps + warp; b < B; b += size * n_warps) {
+            const int held = (s_len[b] + p.bt - 1) / p.bt;
+            for (int j = lane; j < s_need[b + 1] - s_need[b]; j += 32)
+                p.tables[b * p.stride + held + j] = p.free_blocks[there - 1 - s_need[b] - j];
+        }
+    const int32_t n_new = fine ? s_cu[B] : 0;
+    for (int64_t t = rank * kExtendThreads + tid; t < p.max_slots; t += size * kExtendThreads) {
+        int64_t slot = -1;
+        if (t < n_new) {
+            int lo = 0, hi = B - 1;  // the last request whose tokens begin at or before t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (s_cu[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int held = (s_len[lo] + p.bt - 1) / p.bt, pos = s_len[lo] + int(t - s_cu[lo]), j = pos / p.bt;
+            const int32_t blk = j < held ? p.tables[lo * p.stride + j]
+                                         : p.free_blocks[there - 1 - s_need[lo] - (j - held)];
+            if (blk >= 0 && blk < p.pool) slot = int64_t(blk) * p.bt + pos % p.bt;
+        }
+        p.slots[t] = slot;
+    }
+    if (rank == 0) {
+        for (int b = tid; b <= B; b += kExtendThreads) p.cu[b] = fine ? s_cu[b] : 0;
+        for (int b = tid; b < B; b += kExtendThreads) {
+            const bool ended = s_back[b + 1] > s_back[b] || p.add[b] < 0;
+            const int32_t n = s_len[b];
+            p.len_out[b] = !fine ? n : ended ? 0 : n + (s_cu[b + 1] - s_cu[b]);
+        }
+        if (tid == 0) {
+            *p.count_out = fine ? int32_t(there - all_need) : count;
+            *p.shortage = bad ? -1 : int32_t(lack > INT32_MAX ? INT32_MAX : lack);
+        }
+    }
+}
+
+}  // namespace
+}  // namespace sta
+
+using namespace sta;
+
+extern "C" {
+
+sta_status sta_cache_append(const sta_cache* c, const sta_rows* k, const sta_rows* v, int64_t tokens,
+                            const int64_t* slots, void* stream) {
+    if (!cache_ok(c) || tokens < 0) return STA_ERR_INVALID_ARG;
+    if (!cache_supported(c)) return STA_ERR_UNSUPPORTED;
+    if (tokens == 0) return STA_OK;
+    if (!rows_ok(k, tokens) || !rows_ok(v, tokens) || slots == nullptr || reinterpret_cast<uintptr_t>(slots) % 8 != 0)
+        return STA_ERR_INVALID_ARG;
+    if (cudaError_t e = op_begin(); e != cudaSuccess) return op_cuda_status(e);
+    uint32_t* status = nullptr;
+    if (cudaError_t e = op_status_word(&status); e != cudaSuccess) return op_cuda_status(e);
+    const Rows kr = rows_of(k), vr = rows_of(v);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaErrorInvalidValue;
+#define STA_APPEND(D, BT) \
+    if (c->head_dim == D && c->block_tokens == BT) e = launch_append<D, BT>(*c, kr, vr, tokens, slots, status, s)
+    STA_APPEND(64, 16);
+    STA_APPEND(64, 32);
+    STA_APPEND(64, 64);
+    STA_APPEND(64, 128);
+    STA_APPEND(128, 16);
+    STA_APPEND(128, 32);
+    STA_APPEND(128, 64);
+    STA_APPEND(128, 128);
+#undef STA_APPEND
+    return op_cuda_status(e);
+}
+
+sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* new_tokens, const int32_t* lengths,
+                            int32_t* lengths_out, int32_t* block_tables, int32_t table_width, int64_t table_stride,
+                            int32_t* free_blocks, int32_t pool, const int32_t* free_count, int32_t* free_count_out,
+                            int64_t* slots, int64_t max_slots, int32_t* cu_new, int32_t* shortage, void* stream) {
+    if (batch < 1 || table_width < 1 || table_stride < table_width || pool < 1 || max_slots < 0 || block_tokens < 1)
+        return STA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)new_tokens, (const void*)lengths, (const void*)lengths_out,
+                          (const void*)block_tables, (const void*)free_blocks, (const void*)free_count,
+                          (const void*)free_count_out, (const void*)cu_new, (const void*)shortage})
+        if (p == nullptr || reinterpret_cast<uintptr_t>(p) % 4 != 0) return STA_ERR_INVALID_ARG;
+    if (max_slots > 0 && (slots == nullptr || reinterpret_cast<uintptr_t>(slots) % 8 != 0)) return STA_ERR_INVALID_ARG;
+    if (batch > kMaxRequests || (block_tokens != 16 && block_tokens != 32 && block_tokens != 64 && block_tokens != 128))
+        return STA_ERR_UNSUPPORTED;
+    if (cudaError_t e = op_begin(); e != cudaSuccess) return op_cuda_status(e);
+    ExtendParams p{batch, block_tokens, table_width, pool, table_stride, max_slots, new_tokens, lengths, lengths_out,
+                   block_tables, free_blocks, free_count, free_count_out, slots, cu_new, shortage};
+    const size_t smem = size_t(4 * batch + 3) * sizeof(int32_t);
+    if (smem > 48 * 1024)
+        if (cudaError_t e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 int(smem));
+            e != cudaSuccess)
+            return op_cuda_status(e);
+    // a serving step's few slots and tables need no second CTA
+    const unsigned ctas = max_slots > 4 * kExtendThreads || batch > 4 * kExtendThreads / 32 ? kExtendCluster : 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kExtendThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return op_cuda_status(cudaLaunchKernelEx(&cfg, cache_extend_kernel, p));
+}
+
+}  // extern "C"

@@ -1,0 +1,302 @@
+"""Packed attention (forward, backward, autograd) against a 64-bit reference with bounds derived from the
+roundings that the kernels make (prompt_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import prompt_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sta():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    import sparse_attention_video_sta_b200 as s
+    return s
+
+
+def make(lens_q, lens_k, heads, kv_heads, d, seed=0, tail=0, gain=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def randn(t, h):
+        return (gain * torch.randn(t + tail, h, d, generator=g, device="cuda")).bfloat16()
+    q, k, v = randn(sum(lens_q), heads), randn(sum(lens_k), kv_heads), randn(sum(lens_k), kv_heads)
+    return q, k, v, randn(sum(lens_q), heads)
+
+
+# (query lengths, key lengths or None for the same)
+LENGTHS = [
+    ([1], None), ([2], None), ([127, 128, 129], None), ([0, 5, 0, 300, 1], None), ([64], [513]),
+    ([1, 1, 1], [7, 200, 1025]), ([50, 200, 10], [20, 60, 0]), ([0, 3], [9, 0]), ([700], None), ([33, 1, 385, 77], None),
+    ([3, 260], [400, 129]),
+]
+HEADS = [(2, 2, 64), (6, 2, 128), (8, 1, 64), (10, 2, 128), (3, 3, 128)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,kv_heads,d", HEADS)
+@pytest.mark.parametrize("lens_q,lens_k", LENGTHS)
+def test_forward_and_backward(sta, lens_q, lens_k, heads, kv_heads, d, causal):
+    lens_k = lens_k or lens_q
+    q, k, v, do = make(lens_q, lens_k, heads, kv_heads, d, seed=len(lens_q) + heads)
+    cq, ck, scale = ref.cu_of(lens_q), ref.cu_of(lens_k), 1.0 / math.sqrt(d)
+    want = ref.packed(q, k, v, lens_q, lens_k, causal, scale, do)
+    o, lse = sta.sta_packed_attention(q, k, v, cq, ck, causal=causal)
+    dq, dk, dv = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cq, ck, causal=causal)
+    assert sta.sta_operator_status() == 0
+    for name, t in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.check(t, want, name)
+
+
+@pytest.mark.parametrize("heads,kv_heads,d,n", [(128, 1, 64, 70), (100, 1, 128, 33), (40, 2, 64, 150), (14, 2, 128, 400),
+                                                 (24, 8, 128, 2100)])
+def test_many_heads_to_a_key_head(sta, heads, kv_heads, d, n):
+    q, k, v, do = make([n, 3], [n, 3], heads, kv_heads, d, seed=5)
+    cu = ref.cu_of([n, 3])
+    want = ref.packed(q, k, v, [n, 3], [n, 3], True, 0.1, do)
+    o, lse = sta.sta_packed_attention(q, k, v, cu, softmax_scale=0.1)
+    grads = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu, softmax_scale=0.1)
+    for name, t in zip(("o", "lse", "dq", "dk", "dv"), (o, lse) + grads):
+        ref.check(t, want, name)
+
+
+def test_many_sequences(sta):
+    """More sequences than one pass of the bounds' scan takes, most of them tiny."""
+    lens = [(i * 7) % 5 for i in range(2500)] + [260]
+    q, k, v, do = make(lens, lens, 2, 1, 64, seed=8)
+    cu = ref.cu_of(lens)
+    o, lse = sta.sta_packed_attention(q, k, v, cu)
+    dq, dk, dv = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu)
+    assert sta.sta_operator_status() == 0
+    want = ref.packed(q, k, v, lens, lens, True, 0.125, do)
+    for name, t in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.check(t, want, name)
+
+
+@pytest.mark.parametrize("gain,scale", [(6.0, 0.4), (0.01, 1.0), (3.0, 0.02)])
+def test_large_and_small_scores(sta, gain, scale):
+    """Scores of hundreds (rows dominated by one key, maxima that keep rising) and of nearly nothing."""
+    lens = [400, 129]
+    q, k, v, do = make(lens, lens, 4, 2, 64, seed=11, gain=gain)
+    k[::7] *= 3
+    cu = ref.cu_of(lens)
+    o, lse = sta.sta_packed_attention(q, k, v, cu, softmax_scale=scale)
+    grads = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu, softmax_scale=scale)
+    want = ref.packed(q, k, v, lens, lens, True, scale, do)
+    for name, t in zip(("o", "lse", "dq", "dk", "dv"), (o, lse) + grads):
+        ref.check(t, want, name)
+
+
+def test_rising_scores_rescale(sta):
+    """Every key's score above all before it, far past the first chunk's maximum."""
+    n, d = 600, 64
+    q, k, v, do = make([n], [n], 2, 1, d, seed=12)
+    q[:] = 1.0
+    k[:] = (torch.arange(n, device="cuda") * 0.05)[:, None, None].bfloat16()
+    cu = ref.cu_of([n])
+    want = ref.packed(q, k, v, [n], [n], False, 0.5, do)
+    o, lse = sta.sta_packed_attention(q, k, v, cu, causal=False, softmax_scale=0.5)
+    grads = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu, causal=False, softmax_scale=0.5)
+    for name, t in zip(("o", "lse", "dq", "dk", "dv"), (o, lse) + grads):
+        ref.check(t, want, name)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_nothing_of_other_sequences_or_the_tail_is_mixed_in(sta, bad):
+    """Non-finite values in another sequence and behind the last one reach no row of the others."""
+    lens = [100, 60, 171]
+    q, k, v, do = make(lens, lens, 6, 2, 128, seed=3, tail=40)
+    want = ref.packed(q, k, v, lens, lens, True, 0.1, do)
+    for t in (q, k, v, do):
+        t[100:160] = bad
+        t[331:] = bad
+    cu = ref.cu_of(lens)
+    o, lse = sta.sta_packed_attention(q, k, v, cu, softmax_scale=0.1)
+    dq, dk, dv = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu, softmax_scale=0.1)
+    assert sta.sta_operator_status() == 0
+    for name, t in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+        for rows in (slice(0, 100), slice(160, None)):
+            assert bool(((t[rows].double() - want[name][rows]).abs() <= want[name + "_tol"][rows]).all()), name
+    for rows in (slice(0, 100), slice(160, None)):
+        ref.check(lse, want, "lse", rows)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_masked_scores_never_count(sta, bad):
+    """A non-finite key is masked for the queries before it: those rows are as if it were not there."""
+    n = 300
+    q, k, v, do = make([n], [n], 2, 1, 64, seed=4)
+    want = ref.packed(q, k, v, [n], [n], True, 0.125)
+    k[200] = bad
+    o, lse = sta.sta_packed_attention(q, k, v, ref.cu_of([n]))
+    assert bool(((o[:200].double() - want["o"][:200]).abs() <= want["o_tol"][:200]).all())
+    ref.check(lse, want, "lse", slice(0, 200))
+
+
+def test_rows_behind_the_last_sequence_stay(sta):
+    lens_q, lens_k = [40, 90], [77, 130]
+    q, k, v, do = make(lens_q, lens_k, 4, 2, 64, seed=6, tail=29)
+    cq, ck = ref.cu_of(lens_q), ref.cu_of(lens_k)
+    o, dq, dk, dv = (torch.full_like(t, 7.0) for t in (q, q, k, v))
+    lse = torch.full((4, q.shape[0]), 7.0, device="cuda")
+    sta.sta_packed_forward(q, k, v, o, lse, cq, ck)
+    sta.sta_packed_backward(q, k, v, o, lse, do, dq, dk, dv, cq, ck)
+    for t, n in ((o, 130), (dq, 130), (dk, 207), (dv, 207)):
+        assert bool((t[n:] == 7.0).all()) and not bool((t[:n] == 7.0).all(2).any())
+    assert bool((lse[:, 130:] == 7.0).all())
+    o2, lse2 = sta.sta_packed_attention(q, k, v, cq, ck)
+    grads = sta.sta_packed_attention_backward(q, k, v, o2, lse2, do, cq, ck)
+    assert torch.equal(o2[:130], o[:130]) and not bool(o2[130:].any()) and bool((lse2[:, 130:] == -math.inf).all())
+    for t, u, n in zip(grads, (dq, dk, dv), (130, 207, 207)):
+        assert torch.equal(t[:n], u[:n]) and not bool(t[n:].any())
+
+
+def test_strides(sta):
+    """Parts of a fused projection, head-major storage, and strided outputs give the bits of contiguous tensors."""
+    lens, H, K, d = [65, 200, 7], 6, 2, 64
+    T, cu = sum(lens), ref.cu_of([65, 200, 7])
+    qkv = torch.randn(T, H + 2 * K, d, generator=torch.Generator("cuda").manual_seed(1), device="cuda").bfloat16()
+    q, k, v = qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:]
+    do = torch.randn(H, T, d, device="cuda").bfloat16().transpose(0, 1)
+    o0, lse0 = sta.sta_packed_attention(q.contiguous(), k.contiguous(), v.contiguous(), cu)
+    g0 = sta.sta_packed_attention_backward(q.contiguous(), k.contiguous(), v.contiguous(), o0, lse0, do.contiguous(), cu)
+    o = torch.zeros(H, T + 3, d, dtype=torch.bfloat16, device="cuda").transpose(0, 1)[:T]
+    dqkv = torch.zeros(T, H + 2 * K, d + 8, dtype=torch.bfloat16, device="cuda")[..., :d]
+    lse = torch.empty_like(lse0)
+    sta.sta_packed_forward(q, k, v, o, lse, cu)
+    sta.sta_packed_backward(q, k, v, o, lse, do, dqkv[:, :H], dqkv[:, H:H + K], dqkv[:, H + K:], cu)
+    assert torch.equal(o, o0) and torch.equal(lse, lse0)
+    for a, b in zip(g0, (dqkv[:, :H], dqkv[:, H:H + K], dqkv[:, H + K:])):
+        assert torch.equal(a, b)
+
+
+def test_same_bits_again_and_on_another_stream(sta):
+    lens = [1000, 13, 400]
+    q, k, v, do = make(lens, lens, 12, 4, 128, seed=9)
+    cu = ref.cu_of(lens)
+
+    def both(stream=None):
+        o, lse = sta.sta_packed_attention(q, k, v, cu, stream=stream)
+        return (o, lse) + sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu, stream=stream)
+    first = both()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    runs = [both(s) for s in streams * 3]
+    torch.cuda.synchronize()
+    for r in runs + [both()]:
+        assert all(torch.equal(a, b) for a, b in zip(first, r))
+
+
+def test_graphs_follow_new_bounds(sta):
+    """One capture of forward and backward; replayed with other lengths in the same bounds array.  Two graphs
+    replayed at the same time do not disturb each other."""
+    T, H, K, d = 700, 4, 2, 64
+    q, k, v, do = make([T], [T], H, K, d, seed=10)
+    cus = [torch.tensor(c, dtype=torch.int32, device="cuda") for c in ([0, 700, 700, 700], [0, 0, 300, 700], [0, 129, 130, 700])]
+    want = []
+    for cu in cus:
+        o, lse = sta.sta_packed_attention(q, k, v, cu)
+        want.append((o, lse) + sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu))
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        cu = cus[0].clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o, lse = sta.sta_packed_attention(q, k, v, cu)
+            out = (o, lse) + sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu)
+        graphs.append((g, cu, out))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, j in ((0, 1), (1, 2), (2, 0)):
+        for n, s, (g, cu, _) in zip((i, j), streams, graphs):
+            cu.copy_(cus[n])
+        torch.cuda.synchronize()
+        for s, (g, _, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for n, (_, _, out) in zip((i, j), graphs):
+            assert all(torch.equal(a, b) for a, b in zip(out, want[n]))
+    del graphs
+
+
+def test_autograd_against_the_formula_and_differences(sta):
+    """StaPackedAttention on broadcast and transposed inputs: gradients summed into the leaves, and the
+    directional derivative of the 64-bit forward."""
+    lens, H, K, d = [37, 140], 4, 2, 64
+    T, cu = 177, ref.cu_of(lens)
+    g = torch.Generator("cuda").manual_seed(2)
+    q = torch.randn(H, T, d, generator=g, device="cuda").bfloat16().requires_grad_()
+    kv = torch.randn(T, 1, 2 * d, generator=g, device="cuda").bfloat16().requires_grad_()  # one head for both key heads
+    do = torch.randn(T, H, d, generator=g, device="cuda").bfloat16()
+    o = sta.StaPackedAttention.apply(q.transpose(0, 1), kv[..., :d].expand(T, K, d), kv[..., d:].expand(T, K, d), cu)
+    o.backward(do)
+    kx, vx = kv.detach()[..., :d].expand(T, K, d), kv.detach()[..., d:].expand(T, K, d)
+    r = ref.packed(q.detach().transpose(0, 1), kx, vx, lens, lens, True, 1 / math.sqrt(d), do)
+    assert bool(((q.grad.transpose(0, 1).double() - r["dq"]).abs() <= r["dq_tol"]).all())
+    for part, name in ((kv.grad[..., :d], "dk"), (kv.grad[..., d:], "dv")):
+        want, tol = r[name].sum(1, keepdim=True), r[name + "_tol"].sum(1, keepdim=True)
+        # the two heads' gradients are summed in bf16 by autograd: one more rounding
+        assert bool(((part.double() - want).abs() <= tol + 2 * ref.U * (want.abs() + tol)).all())
+    # central differences of the 64-bit loss along a random direction
+    step = 1e-4
+    u = [torch.randn(t.shape, generator=g, device="cuda").double() for t in (r["dq"], r["dk"], r["dv"])]
+
+    def loss(s):
+        x = [a.double() + s * b for a, b in zip((q.detach().transpose(0, 1), kx, vx), u)]
+        return float((ref.packed(*x, lens, lens, True, 1 / math.sqrt(d))["o"] * do.double()).sum())
+    slope = (loss(step) - loss(-step)) / (2 * step)
+    o1, lse1 = sta.sta_packed_attention(q.detach().transpose(0, 1), kx.contiguous(), vx.contiguous(), cu)
+    grads = sta.sta_packed_attention_backward(q.detach().transpose(0, 1), kx.contiguous(), vx.contiguous(), o1, lse1, do, cu)
+    got = sum(float((a.double() * b).sum()) for a, b in zip(grads, u))
+    bound = sum(float((r[n + "_tol"] * b.abs()).sum()) for n, b in zip(("dq", "dk", "dv"), u))
+    assert abs(got - slope) <= bound + 1e-4 * (1 + abs(slope))
+
+
+def test_backward_captured_while_an_eager_graph_lives(sta):
+    """Autograd forward and backward captured into a CUDA graph on their own stream, on leaves of their own that
+    share the storage of an eager graph still alive: the replay gives the eager gradients."""
+    lens = [60, 200]
+    q, k, v, do = make(lens, lens, 4, 2, 64, seed=13)
+    cu = ref.cu_of(lens)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    eager = sta.StaPackedAttention.apply(*leaves, cu)
+    want = torch.autograd.grad(eager, leaves, do, retain_graph=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fresh = [t.detach().requires_grad_() for t in leaves]
+        torch.autograd.grad(sta.StaPackedAttention.apply(*fresh, cu), fresh, do)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = torch.autograd.grad(sta.StaPackedAttention.apply(*fresh, cu), fresh, do)
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    again = torch.autograd.grad(eager, leaves, do)
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+    del g
+
+
+def test_empty_problems(sta):
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = sta.sta_packed_attention(q, k, k, cu)
+    assert o.shape == q.shape and lse.shape == (4, 0)
+    sta.sta_packed_attention_backward(q, k, k, o, lse, q, cu)
+    # keys but no queries: zero gradients; queries but no keys: zeros and -inf
+    k9 = torch.ones(9, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu0, cu9 = ref.cu_of([0, 0]), ref.cu_of([4, 5])
+    _, dk, dv = sta.sta_packed_attention_backward(q, k9, k9, q, lse, q, cu0, cu9)
+    assert not bool(dk.any()) and not bool(dv.any())
+    q9 = torch.ones(9, 4, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = sta.sta_packed_attention(q9, k, k, cu9, cu0, causal=False)
+    assert not bool(o.any()) and bool((lse == -math.inf).all())
+    dq, _, _ = sta.sta_packed_attention_backward(q9, k, k, o, lse, q9, cu9, cu0, causal=False)
+    assert not bool(dq.any())
+    assert sta.sta_operator_status() == 0
