@@ -1,11 +1,28 @@
-// sta_ops.cuh -- device helpers of the plan-less operators: e4m3 conversions.
+// sta_ops.cuh -- device helpers of the plan-less operators: e4m3 conversions,
+// dependent launches, 3D tensor loads.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
 namespace sta {
 namespace ops {
+
+// Wait until the grid that this one depends on (a launch with programmatic
+// serialization) has ended and its writes are visible; let dependents start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// 3D tiled bulk tensor load (coordinates innermost first), completion on an mbarrier.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 
 // Two floats to e4m3, `lo` in bits 0-7: to nearest even, magnitudes above 448 to 448, NaN kept.
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {

@@ -1,5 +1,9 @@
 // sta_packed.cu -- attention of packed sequences of different lengths, causal
 // or not, with grouped heads: the C entry points and the forward kernel.
+//
+// Two launches: the work lists from the bounds (sta_packed_lists.cu), and a
+// persistent tcgen05 kernel that starts beside it.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -7,63 +11,628 @@
 #include <cmath>
 #include <mutex>
 
+#include "sta_ops.cuh"
 #include "sta_ops.h"
+#include "sta_packed.cuh"
+#include "sta_ptx.cuh"
+#include "sta_wait.cuh"
 
 namespace sta {
 namespace {
+
+using packed::QBlock;
 
 constexpr int kMaxDevices = 64;
 __device__ uint32_t g_op_status;  // one word per device: kDevTimeout | kDevBounds
 std::mutex g_status_mutex;
 uint32_t* g_status_ptr[kMaxDevices] = {};
 
-// Sequence of row t, or -1: the last b with cu[b] <= t, if t is before cu[b + 1].
-__device__ int find_sequence(const int32_t* cu, int batch, int t) {
-    int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi], if any
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (cu[mid + 1] <= t)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo < batch && cu[lo] <= t ? lo : -1;
+constexpr int kThreads = 384;  // 3 warpgroups: softmax half A, softmax half B, producers
+constexpr int kLoadWarp = 8;
+constexpr int kPvWarp = 9;    // PV issuer; also allocates TMEM
+constexpr int kSWarp = 10;    // S issuer
+constexpr int kTailWarp = 11; // clears V rows behind a sequence's last key
+// Registers as in the video kernel: 384 threads launched at 168, the producers
+// give theirs to the softmax warpgroups; 128 * (208 + 208 + 88) <= 384 * 168.
+constexpr uint32_t kRegsSoftmax = 208;
+constexpr uint32_t kRegsProducer = 88;
+static_assert(128 * (2 * kRegsSoftmax + kRegsProducer) <= kThreads * 168, "register split exceeds the launch");
+constexpr uint32_t kTmemCols = 512;
+constexpr int kItemQ = 4;               // entries of the item queue in shared memory
+constexpr int kItemConsumers = 3 + 8;   // the issuing threads, the tail warp and the eight softmax warps
+constexpr int kSBufs = 3;               // S buffers in TMEM
+// A half-row sum above this takes the slow path (the running maximum is raised).
+constexpr float kRescaleRowSum = 65536.0f;
+constexpr int kBoxBytes = 128 * 128;    // 128 rows x 128 bytes
+
+struct FwdParams {
+    packed::View v;
+    int32_t kv_heads, group, causal, tokens_q;
+    Rows o;
+    float* lse;
+    float scale, scale_log2;
+    uint32_t q_box_bytes;  // bytes of one box of a query block: group * (128 / group) rows of 128 bytes
+    uint32_t* status;
+    uint64_t timeout_ns;
+};
+
+// Scores of the 64 keys of a half row from index `n` on to -inf.
+__device__ __forceinline__ void mask_from(uint32_t (&sr)[64], int n) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+        if (j >= n) sr[j] = 0xff800000u;
 }
 
-// One warp for each (query, head): keys one after another, D / 32 elements of
-// the head in each lane, running maximum and sum.
+// P = exp2(S * c - m * c) for one 64-score half row, packed to bf16 pairs; returns
+// the fp32 sum of the unrounded values: LSE is their logarithm, to fp32 accuracy.
+// (P's rounding to bf16, at most 2^-8 relative, is the operand type of P V.)
+__device__ __forceinline__ float softmax_exp64(const uint32_t (&sr)[64], float c, float m, uint32_t (&pk)[32]) {
+    const uint64_t c2 = ptx::f2(c, c);
+    const uint64_t nmc2 = ptx::f2(-m * c, -m * c);
+    uint64_t acc0 = ptx::f2(0.0f, 0.0f), acc1 = acc0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float x0, x1;
+        ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), c2, nmc2), x0, x1);
+        const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+        pk[j] = ptx::pack_bf16x2(p0, p1);
+        if (j & 1)
+            acc1 = ptx::f2_add(acc1, ptx::f2(p0, p1));
+        else
+            acc0 = ptx::f2_add(acc0, ptx::f2(p0, p1));
+    }
+    float r0, r1, r2, r3;
+    ptx::f2_split(acc0, r0, r1);
+    ptx::f2_split(acc1, r2, r3);
+    return (r0 + r1) + (r2 + r3);
+}
+
+__device__ __forceinline__ float row_max64(const uint32_t (&sr)[64]) {
+    float a0 = __uint_as_float(sr[0]), a1 = __uint_as_float(sr[1]);
+    float a2 = __uint_as_float(sr[2]), a3 = __uint_as_float(sr[3]);
+#pragma unroll
+    for (int j = 4; j < 60; j += 8) {
+        a0 = ptx::max3(a0, __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
+        a1 = ptx::max3(a1, __uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3]));
+        a2 = ptx::max3(a2, __uint_as_float(sr[j + 4]), __uint_as_float(sr[j + 5]));
+        a3 = ptx::max3(a3, __uint_as_float(sr[j + 6]), __uint_as_float(sr[j + 7]));
+    }
+    a0 = ptx::max3(a0, __uint_as_float(sr[60]), __uint_as_float(sr[61]));
+    a1 = ptx::max3(a1, __uint_as_float(sr[62]), __uint_as_float(sr[63]));
+    return ptx::max3(a0, a1, fmaxf(a2, a3));
+}
+
+// The forward kernel.  One item is one query block (128 rows: tokens x the query
+// heads of one key head, sta_packed.cuh) of one key head; the pipeline is the
+// video forward's key-split one: every 128-key chunk is split between two
+// softmax warpgroups (keys 0-63 and 64-127) that share a running maximum for
+// each row and accumulate into one O, S is triple buffered in TMEM.
+//
+//   warp 8  (load): TMA of the query block (two buffers) and K(0), K(1), K(2), then
+//                   V(i), K(i + 3) into the ring
+//   warp 9  (PV)  : O += P_A V_A, then O += P_B V_B as each half's P lands in TMEM
+//   warp 10 (S)   : S(c) = Q K(c)^T into buffer c % 3, once the PVs of chunk c - 3 are done
+//   warp 11 (tail): a sequence's last chunk may end inside its 128 rows; what lies
+//                   behind (the next sequence, or anything) has P = 0, but 0 x inf is
+//                   not 0, so those V rows are overwritten with zeros in shared memory
+//   warps 0-7     : softmax halves and the epilogue
+//
+// Masks: a row sees keys [0, limit).  A chunk wholly below every row's limit
+// (warp-uniform test) runs without a mask; in the others scores from the limit
+// on become -inf before any arithmetic, so what they were (NaN, inf) is
+// forgotten.  Every row that sees a key sees key 0, in half A of chunk 0, so the
+// first chunk sets its maximum; a row without keys gets a stand-in of 0 and ends
+// with l = 0.  Rows past the block's tokens hold whatever the box brought: they
+// are never stored, and never start the slow path.
+// Bound like the video forward: MUFU exponentials and the tensor pipe nearly
+// level at d = 128; causal blocks lose the masked part of their last chunks.
 template <int D>
-__global__ void packed_forward_simple(PackedProblem p, Rows q, Rows k, Rows v, Rows o, float* lse) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-    if (w >= int64_t(p.tokens_q) * p.heads) return;
-    const int t = int(w / p.heads), h = int(w % p.heads), hk = h / p.group;
-    const int b = find_sequence(p.cu_q, p.batch, t);
-    float acc[E] = {}, m = -INFINITY, l = 0.0f;
-    if (b < 0 && !p.clear_tail) return;
-    if (b >= 0) {
-        const int q0 = p.cu_q[b], nq = p.cu_q[b + 1] - q0;
-        const int k0 = max(0, min(p.cu_k[b], p.tokens_k)), nk = max(0, min(p.cu_k[b + 1], p.tokens_k) - k0);
-        const int vis = p.causal ? min(nk, nk - nq + (t - q0) + 1) : nk;
-        float qv[E];
-        for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(q.p[t * q.ts + h * q.hs + lane * E + e]);
-        for (int j = 0; j < vis; ++j) {
-            float s = 0.0f;
-            for (int e = 0; e < E; ++e)
-                s += qv[e] * __bfloat162float(k.p[int64_t(k0 + j) * k.ts + hk * k.hs + lane * E + e]);
-            for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(~0u, s, i);
-            s *= p.scale;
-            const float mn = fmaxf(m, s), a = expf(m - mn), pr = expf(s - mn);
-            for (int e = 0; e < E; ++e)
-                acc[e] = acc[e] * a + pr * __bfloat162float(v.p[int64_t(k0 + j) * v.ts + hk * v.hs + lane * E + e]);
-            l = l * a + pr;
-            m = mn;
+struct Cfg {
+    static constexpr int kColBlocks = D / 64;
+    static constexpr int kQBytes = 128 * D * 2;
+    static constexpr int kKVBytes = 128 * D * 2;
+    static constexpr int kStages = (D == 128) ? 5 : 8;
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = 2 * kQBytes;
+    static constexpr int kBarOff = kRingOff + kStages * kKVBytes;
+    // full[S], empty[S], q_full[2], q_empty[2], s_full[3], p_full[2][3], pv_buf[3],
+    // o_full, o_empty, drain[2], item_full[Q], item_empty[Q], v_tail[S], v_clean[S]
+    static constexpr int kNumBars = 4 * kStages + 4 + kSBufs + 2 * kSBufs + kSBufs + 4 + 2 * kItemQ;
+    static constexpr int kXchOff = kBarOff + kNumBars * 8;   // [2 halves][128 rows] fp32 exchange
+    static constexpr int kMiscOff = kXchOff + 2 * 128 * 4;   // tmem base slot, abort flag, item queue
+    static constexpr int kSmemBytes = kMiscOff + 8 + 4 * kItemQ + 1024;
+    __host__ __device__ static constexpr uint32_t col_s(int buf) { return uint32_t(buf) * 128u; }
+    static constexpr uint32_t kColO = kSBufs * 128u;
+    static_assert(kSBufs * 128 + D <= int(kTmemCols), "TMEM budget");
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw_base);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const uint32_t bar0 = base + C::kBarOff;
+    constexpr int S = C::kStages;
+    constexpr int NB = kSBufs;
+    auto bar_full = [&](int r) { return bar0 + 8u * r; };
+    auto bar_empty = [&](int r) { return bar0 + 8u * (S + r); };
+    auto bar_q_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
+    auto bar_q_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+    auto bar_s_full = [&](int b) { return bar0 + 8u * (2 * S + 4 + b); };
+    auto bar_p_full = [&](int h, int b) { return bar0 + 8u * (2 * S + 4 + NB + NB * h + b); };
+    auto bar_pv_buf = [&](int b) { return bar0 + 8u * (2 * S + 4 + 3 * NB + b); };
+    const uint32_t xb = bar0 + 8u * (2 * S + 4 + 4 * NB);
+    const uint32_t bar_o_full = xb, bar_o_empty = xb + 8;
+    auto bar_drain = [&](int h) { return xb + 16 + 8u * h; };
+    auto bar_item_full = [&](int q) { return xb + 32 + 8u * q; };
+    auto bar_item_empty = [&](int q) { return xb + 32 + 8u * (kItemQ + q); };
+    // Hand-over of a V with rows to clear, one pair for each ring slot: the load thread arrives
+    // on v_tail once it has issued the copy (so the slot's `full` is in that copy's phase and
+    // the tail warp's wait means that copy), the tail warp on v_clean.  The slot is not filled
+    // again before PV has waited for v_clean, so neither side can be a phase ahead.
+    auto bar_v_tail = [&](int r) { return xb + 32 + 8u * (2 * kItemQ + r); };
+    auto bar_v_clean = [&](int r) { return xb + 32 + 8u * (2 * kItemQ + S + r); };
+    static_assert(4 * S + 4 + 4 * NB + 4 + 2 * kItemQ == C::kNumBars, "barrier count");
+    float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    volatile int32_t* item_q = reinterpret_cast<volatile int32_t*>(smem + C::kMiscOff + 8);
+    auto wait_bar = [&](uint32_t bar, uint32_t parity) {
+        return wait_bar_limited(bar, parity, abort_flag, p.status, p.timeout_ns);
+    };
+    auto take_item = [&](uint32_t k, int32_t& u) -> bool {
+        const int q = int(k % kItemQ);
+        if (!wait_bar(bar_item_full(q), (k / kItemQ) & 1u)) return false;
+        u = item_q[q];
+        return true;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int r = 0; r < S; ++r) {
+            ptx::mbar_init(bar_full(r), 1);
+            ptx::mbar_init(bar_empty(r), 1);
+            ptx::mbar_init(bar_v_tail(r), 1);
+            ptx::mbar_init(bar_v_clean(r), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(bar_q_full(b), 1);
+            ptx::mbar_init(bar_q_empty(b), 1);
+            ptx::mbar_init(bar_drain(b), 1);
+        }
+        for (int b = 0; b < NB; ++b) {
+            ptx::mbar_init(bar_s_full(b), 1);
+            ptx::mbar_init(bar_p_full(0, b), 4);  // one arrival for each softmax warp of the half
+            ptx::mbar_init(bar_p_full(1, b), 4);
+            ptx::mbar_init(bar_pv_buf(b), 1);
+        }
+        ptx::mbar_init(bar_o_full, 1);
+        ptx::mbar_init(bar_o_empty, 8);
+        for (int q = 0; q < kItemQ; ++q) {
+            ptx::mbar_init(bar_item_full(q), 1);
+            ptx::mbar_init(bar_item_empty(q), kItemConsumers);
+        }
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        ptx::prefetch_tensormap(&tm_q);
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    if (warp == kPvWarp) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ops::grid_wait();  // the lists
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int32_t K = p.kv_heads;
+    auto block_of = [&](int32_t u) { return p.v.qblocks + p.v.order_q[u / K]; };
+    // Ring entry of chunk c's K and V in a block of n chunks (the load order:
+    // K(0), K(1), K(2), then V(i), K(i + 3) for i = 0, 1, ...).
+    auto entry_k = [](uint32_t c) { return c < uint32_t(NB) ? c : 2u * c - uint32_t(NB - 1); };
+    auto entry_v = [](uint32_t i, uint32_t n) { return i + uint32_t(NB) <= n ? uint32_t(NB) + 2u * i : n + i; };
+    // Does the block's last chunk reach past the sequence's last key?
+    auto ragged = [](const QBlock& q) { return q.chunks * 128 > q.nkeys; };
+
+    if (warp == kLoadWarp) {
+        ptx::regs_dec<kRegsProducer>();
+        if (lane == 0) {
+            // ------------------------------------------------------------ load
+            const int32_t n_items = p.v.lists->n_q * K;
+            uint32_t ring = 0;
+            uint32_t q_loads[2] = {0u, 0u};
+            bool ok = true;
+            auto issue = [&](const CUtensorMap* m, int32_t head, int32_t row) -> bool {
+                const int r = int(ring % S);
+                if (ring >= uint32_t(S) && !wait_bar(bar_empty(r), ((ring / S) - 1) & 1u)) return false;
+                ptx::mbar_arrive_expect_tx(bar_full(r), C::kKVBytes);
+#pragma unroll
+                for (int cb = 0; cb < C::kColBlocks; ++cb)
+                    ops::tma_load_3d(base + C::kRingOff + r * C::kKVBytes + cb * kBoxBytes, m, bar_full(r), cb * 64, head,
+                                     row);
+                ++ring;
+                return true;
+            };
+            for (uint32_t k = 0; ok; ++k) {
+                int32_t u = atomicAdd(&p.v.lists->next_q, 1);
+                if (u >= n_items) u = -1;
+                const int qe = int(k % kItemQ);
+                if (k >= uint32_t(kItemQ) && !wait_bar(bar_item_empty(qe), ((k / kItemQ) - 1) & 1u)) break;
+                item_q[qe] = u;
+                ptx::mbar_arrive(bar_item_full(qe));
+                if (u < 0) break;
+                const QBlock q = *block_of(u);
+                const int32_t hk = u % K, n = q.chunks;
+                const int qb = int(k & 1u);
+                if (!wait_bar(bar_q_empty(qb), ((k >> 1) & 1u) ^ 1u)) break;
+                ptx::mbar_arrive_expect_tx(bar_q_full(qb), C::kColBlocks * p.q_box_bytes);
+#pragma unroll
+                for (int cb = 0; cb < C::kColBlocks; ++cb)
+                    ops::tma_load_3d(base + C::kQOff + qb * C::kQBytes + cb * kBoxBytes, &tm_q, bar_q_full(qb), cb * 64,
+                                     hk * p.group, q.tok0);
+                ++q_loads[qb];
+                for (int32_t c = 0; ok && c < n && c < NB; ++c) ok = issue(&tm_k, hk, q.key0 + c * 128);
+                for (int32_t i = 0; ok && i < n; ++i) {
+                    ok = issue(&tm_v, hk, q.key0 + i * 128);
+                    if (ok && i == n - 1 && ragged(q)) ptx::mbar_arrive(bar_v_tail(int((ring - 1) % S)));
+                    if (ok && i + NB < n) ok = issue(&tm_k, hk, q.key0 + (i + NB) * 128);
+                }
+            }
+            // Drain the copies that may still be in flight (after an abort).
+            const uint32_t first = ring > uint32_t(S) ? ring - S : 0u;
+            for (uint32_t it = first; it < ring; ++it) drain_bar(bar_full(int(it % S)), (it / S) & 1u, p.timeout_ns);
+            for (int b = 0; b < 2; ++b)
+                if (q_loads[b] > 0) drain_bar(bar_q_full(b), (q_loads[b] - 1u) & 1u, p.timeout_ns);
+        }
+    } else if (warp == kTailWarp) {
+        ptx::regs_dec<kRegsProducer>();
+        // ------------------------------------------------------------ V tails
+        uint32_t e0 = 0, tails = 0;  // tails, bit r: phase of slot r's v_tail
+        for (uint32_t kq = 0;; ++kq) {
+            int32_t u = -1;
+            if (!__all_sync(~0u, take_item(kq, u))) break;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_item_empty(int(kq % kItemQ)));
+            if (u < 0) break;
+            const QBlock q = *block_of(u);
+            const uint32_t n = uint32_t(q.chunks);
+            if (ragged(q)) {
+                const uint32_t e = e0 + entry_v(n - 1, n);
+                const int r = int(e % S);
+                if (!__all_sync(~0u, wait_bar(bar_v_tail(r), (tails >> r) & 1u))) break;
+                tails ^= 1u << r;
+                if (!__all_sync(~0u, wait_bar(bar_full(r), (e / S) & 1u))) break;
+                const int from = q.nkeys - int(n - 1) * 128;  // rows [from, 128) hold no key
+                uint8_t* v0 = smem + C::kRingOff + r * C::kKVBytes;
+                for (int i = from * 8 + lane; i < 128 * 8; i += 32)
+#pragma unroll
+                    for (int cb = 0; cb < C::kColBlocks; ++cb)
+                        *reinterpret_cast<uint4*>(v0 + cb * kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_v_clean(r));
+            }
+            e0 += 2u * n;
+        }
+    } else if (warp == kPvWarp || warp == kSWarp) {
+        ptx::regs_dec<kRegsProducer>();
+        if (lane == 0) {
+            // ------------------------------------------------------------- MMA
+            const bool pv_role = warp == kPvWarp;
+            constexpr uint32_t idesc_qk = ptx::idesc_bf16(128, 128, false);
+            constexpr uint32_t idesc_pv = ptx::idesc_bf16(128, D, true);
+            uint32_t e0 = 0, g = 0;
+            uint32_t cleaned = 0;  // bit r: phase of slot r's v_clean
+            bool ok = true;
+            auto wait_entry = [&](uint32_t e, uint32_t& addr) -> bool {
+                const int r = int(e % S);
+                if (!wait_bar(bar_full(r), (e / S) & 1u)) return false;
+                addr = base + C::kRingOff + r * C::kKVBytes;
+                return true;
+            };
+            for (uint32_t kq = 0; ok; ++kq) {
+                int32_t u;
+                if (!take_item(kq, u)) break;
+                ptx::mbar_arrive(bar_item_empty(int(kq % kItemQ)));
+                if (u < 0) break;
+                const QBlock q = *block_of(u);
+                const uint32_t n = uint32_t(q.chunks);
+                const uint32_t g0 = g;
+                if (pv_role) {
+                    const uint32_t tO = tmem + C::kColO;
+                    for (uint32_t i = 0; ok && i < n; ++i) {
+                        const uint32_t gi = g0 + i, bb = gi % uint32_t(NB), e = e0 + entry_v(i, n);
+                        uint32_t vaddr;
+                        if (!wait_entry(e, vaddr)) { ok = false; break; }
+                        if (i == n - 1 && ragged(q)) {
+                            const uint32_t r = e % S;
+                            if (!wait_bar(bar_v_clean(int(r)), (cleaned >> r) & 1u)) { ok = false; break; }
+                            cleaned ^= 1u << r;
+                        }
+                        if (i == 0 && !wait_bar(bar_o_empty, (kq & 1u) ^ 1u)) { ok = false; break; }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!wait_bar(bar_p_full(h, int(bb)), (gi / uint32_t(NB)) & 1u)) {
+                                ok = false;
+                                break;
+                            }
+                            ptx::tc_fence_after();
+                            const uint32_t tP = tmem + C::col_s(int(bb)) + uint32_t(h) * 64u;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                ptx::mma_ts(tO, tP + kk * 8,
+                                            ptx::desc_mn_sw128(vaddr + (h * 4 + kk) * 16 * 128, kBoxBytes), idesc_pv,
+                                            (i > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        if (!ok) break;
+                        ptx::mma_commit(bar_pv_buf(int(bb)));
+                        ptx::mma_commit(bar_empty(int(e % S)));
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit(bar_o_full);
+                } else {
+                    const int qb = int(kq & 1u);
+                    const uint32_t qaddr = base + C::kQOff + qb * C::kQBytes;
+                    if (!wait_bar(bar_q_full(qb), (kq >> 1) & 1u)) break;
+                    for (uint32_t c = 0; ok && c < n; ++c) {
+                        const uint32_t gc = g0 + c, bb = gc % uint32_t(NB), e = e0 + entry_k(c);
+                        if (gc >= uint32_t(NB) && !wait_bar(bar_pv_buf(int(bb)), ((gc / uint32_t(NB)) - 1u) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        uint32_t kaddr;
+                        if (!wait_entry(e, kaddr)) { ok = false; break; }
+                        ptx::tc_fence_after();
+                        const uint32_t tS = tmem + C::col_s(int(bb));
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t coff = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+                            ptx::mma_ss(tS, ptx::desc_k_sw128(qaddr + coff), ptx::desc_k_sw128(kaddr + coff), idesc_qk,
+                                        kk > 0 ? 1u : 0u);
+                        }
+                        ptx::mma_commit(bar_s_full(int(bb)));
+                        ptx::mma_commit(bar_empty(int(e % S)));
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit(bar_q_empty(qb));
+                }
+                g = g0 + n;
+                e0 += 2u * n;
+            }
+            const int dr = pv_role ? 0 : 1;
+            ptx::mma_commit(bar_drain(dr));
+            drain_bar(bar_drain(dr), 0, p.timeout_ns);
+        }
+    } else {
+        // ------------------------------------------------------------- softmax
+        ptx::regs_inc<kRegsSoftmax>();
+        const int half = warp >> 2;  // 0: keys 0-63 of every chunk, 1: keys 64-127
+        const int row = threadIdx.x & 127;
+        const uint32_t pair_bar = 1u + uint32_t(warp & 3);  // named barrier of warps w and w + 4
+        const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t tOh = tmem + lane_addr + C::kColO + uint32_t(half) * (D / 2);  // this half's O columns
+        float* x_mine = xch + half * 128 + row;
+        const float* x_other = xch + (1 - half) * 128 + row;
+        const float c = p.scale_log2;
+        const int r_tok = row / p.group, r_head = row - r_tok * p.group;
+        uint32_t g = 0;
+        bool ok = true;
+        for (uint32_t kq = 0; ok; ++kq) {
+            int32_t u = -1;
+            const bool took = __all_sync(~0u, take_item(kq, u));
+            __syncwarp();
+            if (took && lane == 0) ptx::mbar_arrive(bar_item_empty(int(kq % kItemQ)));
+            if (ptx::bar_red_or(pair_bar, 64, !took)) {  // leave together
+                ok = false;
+                break;
+            }
+            if (u < 0) break;
+            const QBlock q = *block_of(u);
+            const uint32_t n = uint32_t(q.chunks);
+            const bool real = r_tok < q.ntok;
+            const int limit = real ? min(q.nkeys, q.limit0 + (p.causal ? r_tok : 0)) : INT32_MAX;
+            const int warp_limit = __reduce_min_sync(~0u, limit);  // over the rows that are stored
+            float m_used = 0.0f, l = 0.0f;
+            uint32_t sr[64];
+            bool pre = false;  // sr already holds S(g)
+            for (uint32_t i = 0; i < n; ++i, ++g) {
+                const uint32_t b = g % uint32_t(NB), b1 = (g + 1u) % uint32_t(NB);
+                const uint32_t tS = tmem + lane_addr + C::col_s(int(b)) + uint32_t(half) * 64u;
+                const uint32_t tS1 = tmem + lane_addr + C::col_s(int(b1)) + uint32_t(half) * 64u;
+                bool wok = true;
+                if (!pre) {
+                    wok = __all_sync(~0u, wait_bar(bar_s_full(int(b)), (g / uint32_t(NB)) & 1u));
+                    if (wok) {
+                        ptx::tc_fence_after();
+                        ptx::tmem_ld64(tS, sr);
+                    }
+                }
+                pre = false;
+                const int kbeg = int(i) * 128 + half * 64;
+                const bool masked = kbeg + 64 > warp_limit;
+                if (wok && masked) mask_from(sr, limit - kbeg);
+                // Is S(g + 1) of this block complete?  If so, its load starts
+                // right after the exponentials and overlaps the P hand-over.
+                const bool can_pre = wok && i > 0 && i + 1 < n;
+                const bool t_next =
+                    can_pre && ptx::mbar_test_wait(bar_s_full(int(b1)), ((g + 1u) / uint32_t(NB)) & 1u);
+                uint32_t pk[32];
+                float rowsum = 0.0f;
+                bool need = false;
+                if (wok && i > 0) {
+                    rowsum = softmax_exp64(sr, c, m_used, pk);  // against the running max (no max pass)
+                    need = real && !(rowsum <= kRescaleRowSum);  // also catches inf
+                }
+                const bool nxt = can_pre && __all_sync(~0u, t_next);
+                if (nxt) {
+                    ptx::tc_fence_after();
+                    ptx::tmem_ld64_start(tS1, sr);
+                }
+                if (ptx::bar_red_or(pair_bar, 64, !wok || need || i == 0)) {
+                    // ---- slow path: the block's first chunk, a rescale, or an abort.
+                    // Both warps of the pair take it, exchange this chunk's
+                    // maxima of their rows and agree on the new running max.
+                    if (nxt) {
+                        ptx::tmem_wait_ld(sr);
+                        ptx::tmem_ld64(tS, sr);  // S(g) again: P(g) is not stored yet
+                        if (masked) mask_from(sr, limit - kbeg);
+                    }
+                    *x_mine = wok ? row_max64(sr) : -INFINITY;
+                    if (ptx::bar_red_or(pair_bar, 64, !wok)) {
+                        ok = false;
+                        break;
+                    }
+                    const float mx = fmaxf(*x_mine, *x_other);
+                    float alpha = 1.0f;
+                    if (i == 0) {
+                        m_used = mx == -INFINITY ? 0.0f : mx;  // no key yet: a finite stand-in
+                    } else if ((mx - m_used) * c > 0.0f) {
+                        alpha = ptx::ex2((m_used - mx) * c);
+                        m_used = mx;
+                    }
+                    rowsum = softmax_exp64(sr, c, m_used, pk);
+                    ptx::tmem_st32(tS, pk);
+                    l = l * alpha + rowsum;
+                    bool pv_ok = true;
+                    if (i > 0) {
+                        // O holds P(.. g - 1) V: wait for PV(g - 1), the one that
+                        // may still run, then rescale this half's columns of O.
+                        const uint32_t gp = g - 1u;
+                        pv_ok = __all_sync(~0u, wait_bar(bar_pv_buf(int(gp % uint32_t(NB))), (gp / uint32_t(NB)) & 1u));
+                        if (pv_ok && __any_sync(~0u, alpha != 1.0f)) {
+                            ptx::tc_fence_after();
+                            const uint64_t alpha2 = ptx::f2(alpha, alpha);
+#pragma unroll 1
+                            for (int cb = 0; cb < D / 64; ++cb) {
+                                uint32_t orr[32];
+                                ptx::tmem_ld32(tOh + cb * 32, orr);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    float o0, o1;
+                                    ptx::f2_split(ptx::f2_mul(ptx::f2(__uint_as_float(orr[2 * j]),
+                                                                      __uint_as_float(orr[2 * j + 1])), alpha2),
+                                                  o0, o1);
+                                    orr[2 * j] = __float_as_uint(o0);
+                                    orr[2 * j + 1] = __float_as_uint(o1);
+                                }
+                                ptx::tmem_st32(tOh + cb * 32, orr);
+                            }
+                        }
+                    }
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    // both halves' rescales of O are done before either half's P is signalled
+                    if (ptx::bar_red_or(pair_bar, 64, !pv_ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (nxt) ptx::tmem_ld64(tS1, sr);  // S(g + 1) again
+                } else {
+                    ptx::tmem_st32(tS, pk);
+                    l += rowsum;
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    if (nxt) ptx::tmem_wait_ld(sr);
+                }
+                pre = nxt;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_p_full(half, int(b)));
+            }
+            if (!ok) break;
+            // ---- epilogue: O / (l_A + l_B) -> bf16, LSE; each half stores its columns.
+            const bool ook = __all_sync(~0u, wait_bar(bar_o_full, kq & 1u));
+            *x_mine = l;
+            if (ptx::bar_red_or(pair_bar, 64, !ook)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const float l_sum = l + *x_other;
+            const bool none = l_sum == 0.0f;  // no visible key: O = 0, whatever TMEM holds
+            const float inv_l = 1.0f / l_sum;
+            const uint64_t f2inv = ptx::f2(inv_l, inv_l);
+            const int32_t head = (u % K) * p.group + r_head;
+            const int64_t tok = q.tok0 + r_tok;
+            uint4* dst = reinterpret_cast<uint4*>(p.o.p + tok * p.o.ts + head * p.o.hs + half * (D / 2));
+#pragma unroll 1
+            for (int cb = 0; cb < D / 64; ++cb) {
+                uint32_t orr[32];
+                ptx::tmem_ld32(tOh + cb * 32, orr);  // every lane loads: the access is warp-wide
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float o0, o1;
+                    ptx::f2_split(ptx::f2_mul(ptx::f2(__uint_as_float(orr[2 * j]), __uint_as_float(orr[2 * j + 1])),
+                                              f2inv),
+                                  o0, o1);
+                    pk[j] = none ? 0u : ptx::pack_bf16x2(o0, o1);
+                }
+                if (real) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[cb * 4 + j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                }
+            }
+            if (half == 0 && real)
+                p.lse[int64_t(head) * p.tokens_q + tok] = none ? -INFINITY : m_used * p.scale + logf(l_sum);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_o_empty);
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    for (int e = 0; e < E; ++e) o.p[t * o.ts + h * o.hs + lane * E + e] = __float2bfloat16(acc[e] * inv);
-    if (lane == 0) lse[int64_t(h) * p.tokens_q + t] = l == 0.0f ? -INFINITY : m + logf(l);
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kPvWarp) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// No keys at all: every row of every sequence is empty.
+__global__ void packed_no_keys_kernel(const PackedProblem p, const packed::View v, int head_dim, Rows o, float* lse) {
+    ops::grid_wait();
+    const int parts = head_dim / 8;
+    for (int e = blockIdx.x; e < v.lists->n_q; e += gridDim.x) {
+        const QBlock q = v.qblocks[e];
+        for (int i = threadIdx.x; i < q.ntok * p.heads * parts; i += blockDim.x) {
+            const int row = i / parts;
+            const int64_t tok = q.tok0 + row / p.heads;
+            const int h = row % p.heads;
+            *reinterpret_cast<uint4*>(o.p + tok * o.ts + h * o.hs + (i % parts) * 8) = make_uint4(0u, 0u, 0u, 0u);
+            if (lse != nullptr && i % parts == 0) lse[int64_t(h) * p.tokens_q + tok] = -INFINITY;
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, const Rows& v, const Rows& o, float* lse,
+                       const packed::View& view, int64_t max_items, int sms, cudaStream_t stream) {
+    const int tpb = 128 / p.group;
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = packed::rows_map(&mq, q, p.tokens_q, p.heads, D, p.group, tpb);
+    if (e == cudaSuccess) e = packed::rows_map(&mk, k, p.tokens_k, p.kv_heads, D, 1, 128);
+    if (e == cudaSuccess) e = packed::rows_map(&mv, v, p.tokens_k, p.kv_heads, D, 1, 128);
+    if (e != cudaSuccess) return e;
+    FwdParams fp{view, p.kv_heads, p.group, p.causal, p.tokens_q, o, lse, p.scale, p.scale * 1.4426950408889634f,
+                 uint32_t(p.group * tpb) * 128u, p.status, kOpTimeoutNs};
+    constexpr int kSmem = Cfg<D>::kSmemBytes;
+    e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = unsigned(max_items < sms ? max_items : sms);
+    return packed::launch(packed_fwd_kernel<D>, grid, kThreads, kSmem, stream, true, mq, mk, mv, fp);
 }
 
 }  // namespace
@@ -106,14 +675,24 @@ sta_status packed_problem(const sta_packed* p, bool pointers, PackedProblem* out
 }
 
 cudaError_t launch_packed_forward(const PackedProblem& p, int head_dim, const Rows& q, const Rows& k, const Rows& v,
-                                  const Rows& o, float* lse, void*, cudaStream_t stream) {
-    const int64_t warps = int64_t(p.tokens_q) * p.heads;
-    const unsigned grid = unsigned((warps + 3) / 4);
-    if (head_dim == 128)
-        packed_forward_simple<128><<<grid, 128, 0, stream>>>(p, q, k, v, o, lse);
-    else
-        packed_forward_simple<64><<<grid, 128, 0, stream>>>(p, q, k, v, o, lse);
-    return cudaGetLastError();
+                                  const Rows& o, float* lse, void* workspace, cudaStream_t stream) {
+    const packed::Layout w = packed::layout(p, false);
+    const packed::View view = packed::view(w, workspace);
+    packed::Tails tails{};
+    tails.r[0] = o;
+    tails.heads[0] = p.heads;
+    tails.is_q[0] = 1;
+    tails.n = 1;
+    tails.lse = lse;
+    int sms = 0;
+    cudaError_t e = packed::sm_count(&sms);
+    if (e == cudaSuccess) e = packed::launch_lists(p, view, false, head_dim, tails, stream);
+    if (e != cudaSuccess || p.batch == 0) return e;
+    if (p.tokens_k == 0)
+        return packed::launch(packed_no_keys_kernel, unsigned(sms), 256, 0, stream, true, p, view, head_dim, o, lse);
+    const int64_t items = w.max_q * p.kv_heads;
+    if (head_dim == 128) return launch_fwd<128>(p, q, k, v, o, lse, view, items, sms, stream);
+    return launch_fwd<64>(p, q, k, v, o, lse, view, items, sms, stream);
 }
 
 }  // namespace sta
@@ -126,7 +705,7 @@ sta_status sta_packed_workspace(const sta_packed* p, int32_t backward, int64_t* 
     PackedProblem pp;
     if (bytes == nullptr || (backward != 0 && backward != 1)) return STA_ERR_INVALID_ARG;
     if (sta_status st = packed_problem(p, false, &pp); st != STA_OK) return st;
-    *bytes = 256 + (backward ? int64_t(4) * pp.heads * pp.tokens_q : 0);
+    *bytes = packed::layout(pp, backward != 0).bytes;
     return STA_OK;
 }
 

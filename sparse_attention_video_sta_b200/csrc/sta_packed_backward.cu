@@ -104,7 +104,7 @@ __global__ void packed_dkdv_simple(PackedProblem p, Rows q, Rows k, Rows v, Rows
 cudaError_t launch_packed_backward(const PackedProblem& p, int head_dim, const Rows& q, const Rows& k, const Rows& v,
                                    const Rows& o, const Rows& dout, const float* lse, const Rows& dq, const Rows& dk,
                                    const Rows& dv, void* workspace, cudaStream_t stream) {
-    float* dsum = static_cast<float*>(workspace) + 64;
+    float* dsum = static_cast<float*>(workspace) + 64;  // within the workspace: heads * tokens_q floats
     const unsigned gq = unsigned((int64_t(p.tokens_q) * p.heads + 3) / 4),
                    gk = unsigned((int64_t(p.tokens_k) * p.kv_heads + 3) / 4);
     if (head_dim == 128) {
