@@ -358,7 +358,7 @@ class CacheStep(NamedTuple):
     cu_new: torch.Tensor      # int32 [batch + 1]: bounds of each request's new tokens
     lengths: torch.Tensor     # int32 [batch]: tokens held after the step
     free_count: torch.Tensor  # int32 [1]
-    shortage: torch.Tensor    # int32 [1]: 0 done, n > 0 blocks missing, -1 out of range; unless 0 nothing changed
+    short: torch.Tensor       # int32 [1]: 0 done, n > 0 blocks missing, -1 out of range; unless 0 nothing changed
 
 
 def sta_cache_extend(new_tokens: torch.Tensor, lengths: torch.Tensor, block_tables: torch.Tensor,

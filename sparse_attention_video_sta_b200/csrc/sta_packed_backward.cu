@@ -1,102 +1,891 @@
-// sta_packed_backward.cu -- gradients of the packed attention.
+// sta_packed_backward.cu -- gradients of the packed attention (sta_packed.cu).
+//
+//   P_ij = exp(scale q_i.k_j - LSE_i),  D_i = dO_i.O_i,  dS_ij = P_ij (dO_i.v_j - D_i),
+//   dQ_i = scale sum_j dS_ij k_j,  dK_j = scale sum_i dS_ij q_i,  dV_j = sum_i P_ij dO_i,
+// the sums over i running over the queries of every head that shares the key head.
+//
+// Four launches, no atomics on results: the work lists (sta_packed_lists.cu);
+// packed_prep_kernel, -D and -LSE log2(e) of every row of every query block;
+// packed_dq_kernel, one query block per item, walking key chunks; packed_dkdv_kernel,
+// one key block per item, walking the query blocks that see it.  Query blocks hold the
+// rows of all the query heads of a key head (sta_packed.cuh), so dK and dV of a shared
+// head are ordinary sums over a block's rows, in the tensor core's fp32 accumulator.
+// Both main kernels are the video backward's pipeline (one TMA warp, one tcgen05
+// issuing thread, two elementwise warpgroups) with masks.
+//
+// Masks and rows that are not there.  In a masked chunk P and dS are selected to 0,
+// whatever the products held.  Rows of an operand that a product sums over must be
+// finite as well, since 0 x inf is not 0: K rows behind the sequence's last key (dQ)
+// and Q, dO rows behind a block's last token (dK, dV) are overwritten with zeros in
+// shared memory by the elementwise warps, once the products that only need the other
+// rows have read them.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "sta_ops.cuh"
 #include "sta_ops.h"
+#include "sta_packed.cuh"
+#include "sta_ptx.cuh"
+#include "sta_wait.cuh"
 
 namespace sta {
 namespace {
 
-__device__ int sequence_of(const int32_t* cu, int batch, int t) {
-    int lo = 0, hi = batch;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (cu[mid + 1] <= t)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo < batch && cu[lo] <= t ? lo : -1;
+using packed::KBlock;
+using packed::QBlock;
+
+constexpr int kThreads = 320;  // warps 0-7 elementwise, 8 load, 9 MMA
+constexpr int kLoadWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kEwWarps = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kBoxBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16)
+constexpr int kItemQ = 4;
+constexpr int kItemConsumers = 1 + kEwWarps;
+// At least this much shared memory at launch, so that a CTA has its SM alone (a
+// second one would wait in tcgen05.alloc for the first one's 512 columns).
+constexpr int kMinSmem = 120 * 1024;
+constexpr int smem_launch(int bytes) { return bytes > kMinSmem ? bytes : kMinSmem; }
+
+struct BwdParams {
+    packed::View v;
+    int32_t kv_heads, group, causal;
+    const float* neg_l;  // [query blocks][kv_heads][128]: -LSE log2(e); -inf: no such row, or it sees no key
+    const float* neg_d;  // the same for -D
+    Rows out_a;          // dQ, or dK
+    Rows out_b;          // dV
+    float scale, scale_log2;
+    uint32_t q_box_bytes;
+    uint32_t* status;
+    uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ bool wait_bw(uint32_t bar, uint32_t parity, volatile int* abort_flag, const BwdParams& p) {
+    return wait_bar_limited(bar, parity, abort_flag, p.status, p.timeout_ns);
 }
 
-template <int E>
-__device__ float dot(const float* a, const __nv_bfloat16* b) {
-    float s = 0.0f;
-    for (int e = 0; e < E; ++e) s += a[e] * __bfloat162float(b[e]);
-    for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(~0u, s, i);
-    return s;
-}
-
-// One warp for each (query, head): D = dO.O, then dQ over the visible keys.
 template <int D>
-__global__ void packed_dq_simple(PackedProblem p, Rows q, Rows k, Rows v, Rows o, Rows dout, const float* lse, Rows dq,
-                                 float* dsum) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-    if (w >= int64_t(p.tokens_q) * p.heads) return;
-    const int t = int(w / p.heads), h = int(w % p.heads), hk = h / p.group;
-    const int b = sequence_of(p.cu_q, p.batch, t);
-    if (b < 0 && !p.clear_tail) return;
-    float acc[E] = {};
-    if (b >= 0) {
-        const int q0 = p.cu_q[b], nq = p.cu_q[b + 1] - q0;
-        const int k0 = max(0, min(p.cu_k[b], p.tokens_k)), nk = max(0, min(p.cu_k[b + 1], p.tokens_k) - k0);
-        const int vis = p.causal ? min(nk, nk - nq + (t - q0) + 1) : nk;
-        float qv[E], dov[E];
-        for (int e = 0; e < E; ++e) {
-            qv[e] = __bfloat162float(q.p[t * q.ts + h * q.hs + lane * E + e]);
-            dov[e] = __bfloat162float(dout.p[t * dout.ts + h * dout.hs + lane * E + e]);
-        }
-        const float d = dot<E>(dov, o.p + t * o.ts + h * o.hs + lane * E), ls = lse[int64_t(h) * p.tokens_q + t];
-        if (lane == 0) dsum[int64_t(h) * p.tokens_q + t] = d;
-        for (int j = 0; j < vis; ++j) {
-            const __nv_bfloat16* kj = k.p + int64_t(k0 + j) * k.ts + hk * k.hs + lane * E;
-            const __nv_bfloat16* vj = v.p + int64_t(k0 + j) * v.ts + hk * v.hs + lane * E;
-            const float ds = expf(p.scale * dot<E>(qv, kj) - ls) * (dot<E>(dov, vj) - d);
-            for (int e = 0; e < E; ++e) acc[e] += ds * __bfloat162float(kj[e]);
-        }
-    }
-    for (int e = 0; e < E; ++e) dq.p[t * dq.ts + h * dq.hs + lane * E + e] = __float2bfloat16(p.scale * acc[e]);
+__device__ __forceinline__ void load_block(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t head, int32_t tok) {
+#pragma unroll
+    for (int cb = 0; cb < D / 64; ++cb) ops::tma_load_3d(dst + cb * kBoxBytes, m, bar, cb * 64, head, tok);
 }
 
-// One warp for each (key, key head): dK and dV over the queries that see it.
-template <int D>
-__global__ void packed_dkdv_simple(PackedProblem p, Rows q, Rows k, Rows v, Rows dout, const float* lse,
-                                   const float* dsum, Rows dk, Rows dv) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-    if (w >= int64_t(p.tokens_k) * p.kv_heads) return;
-    const int t = int(w / p.kv_heads), hk = int(w % p.kv_heads);
-    const int b = sequence_of(p.cu_k, p.batch, t);
-    if (b < 0 && !p.clear_tail) return;
-    float ak[E] = {}, av[E] = {};
-    if (b >= 0) {
-        const int k0 = p.cu_k[b], nk = p.cu_k[b + 1] - k0;
-        const int q0 = max(0, min(p.cu_q[b], p.tokens_q)), nq = max(0, min(p.cu_q[b + 1], p.tokens_q) - q0);
-        float kv[E], vv[E];
-        for (int e = 0; e < E; ++e) {
-            kv[e] = __bfloat162float(k.p[t * k.ts + hk * k.hs + lane * E + e]);
-            vv[e] = __bfloat162float(v.p[t * v.ts + hk * v.hs + lane * E + e]);
+// Producer side of the item queue (one thread): publish this CTA's k-th item (-1: none left).
+// Returns it, or -2 when the CTA is aborting.
+__device__ __forceinline__ int32_t put_item(uint32_t k, int32_t* next, int32_t n_items, uint32_t full0, uint32_t empty0,
+                                            volatile int32_t* q, volatile int* abort_flag, const BwdParams& p) {
+    int32_t u = atomicAdd(next, 1);
+    if (u >= n_items) u = -1;
+    const uint32_t e = k % kItemQ;
+    if (k >= uint32_t(kItemQ) && !wait_bw(empty0 + 8u * e, ((k / kItemQ) - 1) & 1u, abort_flag, p)) return -2;
+    q[e] = u;
+    ptx::mbar_arrive(full0 + 8u * e);
+    return u;
+}
+__device__ __forceinline__ bool get_item(uint32_t k, uint32_t full0, volatile int32_t* q, volatile int* abort_flag,
+                                        const BwdParams& p, int32_t& u) {
+    if (!wait_bw(full0 + 8u * (k % kItemQ), (k / kItemQ) & 1u, abort_flag, p)) return false;
+    u = q[k % kItemQ];
+    return true;
+}
+
+__device__ __forceinline__ void pack64(const float (&x)[64], uint32_t (&pk)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) pk[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+
+// `kCols` fp32 TMEM columns of this thread's lane, times `mul`, as bf16 to dst; `zero`: zeros
+// instead.  Every lane loads (the access is warp-wide); lanes with `store` write.
+template <int kCols>
+__device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloat16* dst, bool store, bool zero) {
+    uint4* d4 = reinterpret_cast<uint4*>(dst);
+#pragma unroll 1
+    for (int cb = 0; cb < kCols / 32; ++cb) {
+        uint32_t r[32];
+        ptx::tmem_ld32(taddr + cb * 32, r);
+        if (!store) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 v;
+            v.x = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 0]) * mul, __uint_as_float(r[8 * j + 1]) * mul);
+            v.y = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 2]) * mul, __uint_as_float(r[8 * j + 3]) * mul);
+            v.z = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 4]) * mul, __uint_as_float(r[8 * j + 5]) * mul);
+            v.w = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 6]) * mul, __uint_as_float(r[8 * j + 7]) * mul);
+            d4[cb * 4 + j] = zero ? make_uint4(0u, 0u, 0u, 0u) : v;
         }
-        for (int i = p.causal ? max(0, (t - k0) - (nk - nq)) : 0; i < nq; ++i)
-            for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
-                const __nv_bfloat16* qi = q.p + int64_t(q0 + i) * q.ts + h * q.hs + lane * E;
-                const __nv_bfloat16* di = dout.p + int64_t(q0 + i) * dout.ts + h * dout.hs + lane * E;
-                const int64_t r = int64_t(h) * p.tokens_q + q0 + i;
-                const float pr = expf(p.scale * dot<E>(kv, qi) - lse[r]), ds = pr * (dot<E>(vv, di) - dsum[r]);
-                for (int e = 0; e < E; ++e) {
-                    av[e] += pr * __bfloat162float(di[e]);
-                    ak[e] += ds * __bfloat162float(qi[e]);
+    }
+}
+
+// A-operand column of K-step kk of a bf16 matrix that the two elementwise warpgroups wrote
+// into TMEM: warpgroup h packs its 64 columns into columns [64 h, 64 h + 32).
+__device__ __forceinline__ uint32_t a_col(int kk) { return uint32_t((kk >> 2) * 64 + (kk & 3) * 8); }
+
+// Rows [from, 128) of a 128-row block in shared memory to zero (128-byte rows in D / 64 boxes;
+// the swizzle permutes within rows), by the 256 elementwise threads, visible to tcgen05.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* blk, int from, int thread) {
+    for (int i = from * 8 + thread; i < 128 * 8; i += 256)
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb)
+            *reinterpret_cast<uint4*>(blk + cb * kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+}
+
+// ---------------------------------------------------------------- prep
+// -D and -LSE log2(e) of the rows of every (query block, key head): D / 8 threads for a
+// row, 16 bytes of O and dO each.  HBM-bound: O and dO once.
+template <int D>
+__global__ void __launch_bounds__(256) packed_prep_kernel(const PackedProblem p, const packed::View v, Rows o, Rows dout,
+                                                          const float* lse, float* neg_l, float* neg_d) {
+    constexpr int kTpr = D / 8;
+    ops::grid_wait();
+    ops::grid_launch_dependents();
+    const int part = threadIdx.x % kTpr;
+    const int64_t n = int64_t(v.lists->n_q) * p.kv_heads;
+    for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+        const QBlock q = v.qblocks[w / p.kv_heads];
+        const int hk = int(w % p.kv_heads);
+#pragma unroll
+        for (int r0 = 0; r0 < 128; r0 += 256 / kTpr) {
+            const int r = r0 + threadIdx.x / kTpr, t = r / p.group, h = hk * p.group + r - t * p.group;
+            const bool real = t < q.ntok;
+            float acc = 0.0f;
+            if (real) {
+                const int64_t tok = q.tok0 + t;
+                const uint4 a = __ldg(reinterpret_cast<const uint4*>(o.p + tok * o.ts + h * o.hs) + part);
+                const uint4 b = __ldg(reinterpret_cast<const uint4*>(dout.p + tok * dout.ts + h * dout.hs) + part);
+                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc = fmaf(__uint_as_float(aw[i] << 16), __uint_as_float(bw[i] << 16), acc);
+                    acc = fmaf(__uint_as_float(aw[i] & 0xffff0000u), __uint_as_float(bw[i] & 0xffff0000u), acc);
                 }
             }
+#pragma unroll
+            for (int s = kTpr / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(~0u, acc, s);
+            if (part == 0) {
+                const float l = real ? lse[int64_t(h) * p.tokens_q + q.tok0 + t] : -INFINITY;
+                neg_d[w * 128 + r] = real ? -acc : 0.0f;
+                neg_l[w * 128 + r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+            }
+        }
     }
-    for (int e = 0; e < E; ++e) {
-        dk.p[t * dk.ts + hk * dk.hs + lane * E + e] = __float2bfloat16(p.scale * ak[e]);
-        dv.p[t * dv.ts + hk * dv.hs + lane * E + e] = __float2bfloat16(av[e]);
+}
+
+// ---------------------------------------------------------------- dQ
+template <int D>
+struct DqCfg {
+    static constexpr int kBlk = 128 * D * 2;
+    static constexpr int kKStages = 3, kVStages = 2;
+    static constexpr int kQOff = 0, kDOOff = kBlk;
+    static constexpr int kKOff = 2 * kBlk;
+    static constexpr int kVOff = kKOff + kKStages * kBlk;
+    static constexpr int kBarOff = kVOff + kVStages * kBlk;
+    // k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], q_full, q_empty,
+    // s_full[2], dp_full, ds_full, dq_full, drain, item_full[Q], item_empty[Q]
+    static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 8 + 2 * kItemQ;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+    static constexpr int kSmemBytes = kMiscOff + 8 + 4 * kItemQ + 1024;
+    static constexpr uint32_t kColS0 = 0, kColDP = 256, kColDQ = 384;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+    static_assert(kColDQ + D <= kTmemCols, "TMEM budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                 const BwdParams p) {
+    using C = DqCfg<D>;
+    constexpr int KS = C::kKStages, VS = C::kVStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw_base);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const uint32_t bar0 = base + C::kBarOff;
+    auto k_full = [&](int r) { return bar0 + 8u * r; };
+    auto k_empty = [&](int r) { return bar0 + 8u * (KS + r); };
+    auto v_full = [&](int r) { return bar0 + 8u * (2 * KS + r); };
+    auto v_empty = [&](int r) { return bar0 + 8u * (2 * KS + VS + r); };
+    const uint32_t xb = bar0 + 8u * (2 * KS + 2 * VS);
+    const uint32_t q_full = xb, q_empty = xb + 8;
+    auto s_full = [&](int b) { return xb + 16 + 8u * b; };
+    const uint32_t dp_full = xb + 32, ds_full = xb + 40, dq_full = xb + 48, drain = xb + 56;
+    const uint32_t item_full0 = xb + 64, item_empty0 = xb + 64 + 8 * kItemQ;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    volatile int32_t* item_q = reinterpret_cast<volatile int32_t*>(smem + C::kMiscOff + 8);
+
+    if (threadIdx.x == 0) {
+        for (int r = 0; r < KS; ++r) {
+            ptx::mbar_init(k_full(r), 1);
+            ptx::mbar_init(k_empty(r), 1);
+        }
+        for (int r = 0; r < VS; ++r) {
+            ptx::mbar_init(v_full(r), 1);
+            ptx::mbar_init(v_empty(r), 1);
+        }
+        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(q_empty, 1);
+        ptx::mbar_init(s_full(0), 1);
+        ptx::mbar_init(s_full(1), 1);
+        ptx::mbar_init(dp_full, 1);
+        ptx::mbar_init(ds_full, kEwWarps);
+        ptx::mbar_init(dq_full, 1);
+        ptx::mbar_init(drain, 1);
+        for (int q = 0; q < kItemQ; ++q) {
+            ptx::mbar_init(item_full0 + 8u * q, 1);
+            ptx::mbar_init(item_empty0 + 8u * q, kItemConsumers);
+        }
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
     }
+    if (warp == kLoadWarp && lane == 0) {
+        ptx::prefetch_tensormap(&tm_q);
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+        ptx::prefetch_tensormap(&tm_do);
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ops::grid_wait();  // the lists and the rows' constants
+    ops::grid_launch_dependents();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int32_t K = p.kv_heads;
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ load
+            const int32_t n_items = p.v.lists->n_q * K;
+            uint32_t kit = 0, vit = 0, qc = 0;
+            bool ok = true;
+            for (uint32_t kq = 0; ok; ++kq) {
+                const int32_t u = put_item(kq, &p.v.lists->next_dq, n_items, item_full0, item_empty0, item_q, abort_flag, p);
+                if (u < 0) break;
+                const QBlock q = p.v.qblocks[p.v.order_q[u / K]];
+                const int32_t hk = u % K;
+                if (!wait_bw(q_empty, (qc & 1u) ^ 1u, abort_flag, p)) break;
+                ptx::mbar_arrive_expect_tx(q_full, 2 * (D / 64) * p.q_box_bytes);
+                load_block<D>(base + C::kQOff, &tm_q, q_full, hk * p.group, q.tok0);
+                load_block<D>(base + C::kDOOff, &tm_do, q_full, hk * p.group, q.tok0);
+                ++qc;
+                for (int32_t c = 0; c < q.chunks; ++c) {
+                    const int rk = int(kit % KS);
+                    if (kit >= uint32_t(KS) && !wait_bw(k_empty(rk), ((kit / KS) - 1) & 1u, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::mbar_arrive_expect_tx(k_full(rk), C::kBlk);
+                    load_block<D>(base + C::kKOff + rk * C::kBlk, &tm_k, k_full(rk), hk, q.key0 + c * 128);
+                    ++kit;
+                    const int rv = int(vit % VS);
+                    if (vit >= uint32_t(VS) && !wait_bw(v_empty(rv), ((vit / VS) - 1) & 1u, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::mbar_arrive_expect_tx(v_full(rv), C::kBlk);
+                    load_block<D>(base + C::kVOff + rv * C::kBlk, &tm_v, v_full(rv), hk, q.key0 + c * 128);
+                    ++vit;
+                }
+            }
+            // Drain the copies still in flight.
+            for (uint32_t it = kit > uint32_t(KS) ? kit - KS : 0u; it < kit; ++it)
+                drain_bar(k_full(int(it % KS)), (it / KS) & 1u, p.timeout_ns);
+            for (uint32_t it = vit > uint32_t(VS) ? vit - VS : 0u; it < vit; ++it)
+                drain_bar(v_full(int(it % VS)), (it / VS) & 1u, p.timeout_ns);
+            if (qc > 0) drain_bar(q_full, (qc - 1) & 1u, p.timeout_ns);
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            // ------------------------------------------------------------- MMA
+            constexpr uint32_t idesc_s = ptx::idesc_bf16(128, 128, false);
+            constexpr uint32_t idesc_dq = ptx::idesc_bf16(128, D, true);
+            const uint32_t qaddr = base + C::kQOff, doaddr = base + C::kDOOff;
+            uint32_t kbase = 0, gs = 0, qc = 0;
+            bool ok = true;
+            for (uint32_t kq = 0; ok; ++kq) {
+                int32_t u;
+                if (!get_item(kq, item_full0, item_q, abort_flag, p, u)) break;
+                ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
+                if (u < 0) break;
+                const int32_t n = p.v.qblocks[p.v.order_q[u / K]].chunks;
+                if (!wait_bw(q_full, qc & 1u, abort_flag, p)) break;
+                ++qc;
+                ptx::tc_fence_after();
+                // S_j = Q K_j^T into S buffer (gs + j) & 1
+                auto issue_s = [&](int32_t j) -> bool {
+                    const uint32_t it = kbase + uint32_t(j);
+                    if (!wait_bw(k_full(int(it % KS)), (it / KS) & 1u, abort_flag, p)) return false;
+                    ptx::tc_fence_after();
+                    const uint32_t kaddr = base + C::kKOff + (it % KS) * C::kBlk;
+                    const uint32_t tS = tmem + C::kColS0 + ((gs + uint32_t(j)) & 1u) * 128u;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t coff = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+                        ptx::mma_ss(tS, ptx::desc_k_sw128(qaddr + coff), ptx::desc_k_sw128(kaddr + coff), idesc_s,
+                                    kk > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit(s_full(int((gs + uint32_t(j)) & 1u)));
+                    return true;
+                };
+                // dP_j = dO V_j^T; V_j is then free
+                auto issue_dp = [&](int32_t j) -> bool {
+                    const uint32_t it = kbase + uint32_t(j);
+                    if (!wait_bw(v_full(int(it % VS)), (it / VS) & 1u, abort_flag, p)) return false;
+                    ptx::tc_fence_after();
+                    const uint32_t vaddr = base + C::kVOff + (it % VS) * C::kBlk;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t coff = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+                        ptx::mma_ss(tmem + C::kColDP, ptx::desc_k_sw128(doaddr + coff), ptx::desc_k_sw128(vaddr + coff),
+                                    idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit(dp_full);
+                    ptx::mma_commit(v_empty(int(it % VS)));
+                    return true;
+                };
+                ok = issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    if (!wait_bw(ds_full, (gs + uint32_t(j)) & 1u, abort_flag, p)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    // dQ += dS_j K_j (dS from TMEM over dP; K_j MN-major)
+                    const uint32_t it = kbase + uint32_t(j);
+                    const uint32_t kaddr = base + C::kKOff + (it % KS) * C::kBlk;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        ptx::mma_ts(tmem + C::kColDQ, tmem + C::kColDP + a_col(kk),
+                                    ptx::desc_mn_sw128(kaddr + kk * 16 * 128, kBoxBytes), idesc_dq,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit(k_empty(int(it % KS)));
+                    // in issue order after dQ_j, which reads the dS this dP overwrites
+                    if (j + 1 < n && !issue_dp(j + 1)) { ok = false; break; }
+                    if (j + 2 < n && !issue_s(j + 2)) { ok = false; break; }
+                }
+                if (!ok) break;
+                ptx::mma_commit(dq_full);
+                ptx::mma_commit(q_empty);
+                kbase += uint32_t(n);
+                gs += uint32_t(n);
+            }
+            ptx::mma_commit(drain);
+            drain_bar(drain, 0, p.timeout_ns);
+        }
+    } else {
+        // ------------------------------------------------------- elementwise
+        const int h = warp >> 2;  // column half
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
+        const uint64_t c2 = ptx::f2(p.scale_log2, p.scale_log2);
+        const int r_tok = row / p.group, r_head = row - r_tok * p.group;
+        uint32_t gs = 0, dqc = 0;
+        bool ok = true;
+        for (uint32_t kq = 0; ok; ++kq) {
+            int32_t u = -1;
+            if (!__all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, u))) break;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
+            if (u < 0) break;
+            const int32_t e = p.v.order_q[u / K], hk = u % K;
+            const QBlock q = p.v.qblocks[e];
+            const int32_t n = q.chunks;
+            const bool real = r_tok < q.ntok;
+            const int limit = real ? min(q.nkeys, q.limit0 + (p.causal ? r_tok : 0)) : INT32_MAX;
+            const int warp_limit = __reduce_min_sync(~0u, limit);
+            const int64_t grow = (int64_t(e) * K + hk) * 128 + row;
+            const float nl = p.neg_l[grow], nd = p.neg_d[grow];
+            const uint64_t nl2 = ptx::f2(nl, nl), nd2 = ptx::f2(nd, nd);
+            for (int32_t j = 0; j < n; ++j) {
+                const uint32_t step = gs + uint32_t(j);
+                if (!__all_sync(~0u, wait_bw(s_full(int(step & 1u)), (step >> 1) & 1u, abort_flag, p))) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const int seen = limit - (j * 128 + 64 * h);  // keys of this half that the row sees
+                const bool masked = warp_limit < j * 128 + 64 * h + 64;
+                if ((j + 1) * 128 > q.nkeys)  // the sequence's last chunk: S has read K, dQ has not
+                    zero_rows<D>(smem + C::kKOff + (step % KS) * C::kBlk, q.nkeys - j * 128, threadIdx.x);
+                float pr[64];
+                {
+                    uint32_t sr[64];
+                    ptx::tmem_ld64(tmem + lane_addr + C::kColS0 + (step & 1u) * 128u + 64u * h, sr);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float x0, x1;
+                        ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                                  c2, nl2),
+                                      x0, x1);
+                        pr[2 * i] = ptx::ex2(x0);
+                        pr[2 * i + 1] = ptx::ex2(x1);
+                    }
+                }
+                if (!__all_sync(~0u, wait_bw(dp_full, step & 1u, abort_flag, p))) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t tdp = tmem + lane_addr + C::kColDP + 64u * h;
+                uint32_t pk[32];
+                {
+                    uint32_t dr[64];
+                    ptx::tmem_ld64(tdp, dr);
+                    if (masked)
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i >= seen) {
+                                pr[i] = 0.0f;
+                                dr[i] = 0u;
+                            }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float t0, t1;
+                        ptx::f2_split(ptx::f2_mul(ptx::f2(pr[2 * i], pr[2 * i + 1]),
+                                                  ptx::f2_add(ptx::f2(__uint_as_float(dr[2 * i]),
+                                                                      __uint_as_float(dr[2 * i + 1])),
+                                                              nd2)),
+                                      t0, t1);
+                        pk[i] = ptx::pack_bf16x2(t0, t1);
+                    }
+                }
+                ptx::tmem_st32(tdp, pk);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ds_full);
+            }
+            if (!ok) break;
+            if (!__all_sync(~0u, wait_bw(dq_full, dqc & 1u, abort_flag, p))) break;
+            ++dqc;
+            ptx::tc_fence_after();
+            store_cols<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h, p.scale,
+                              p.out_a.p + int64_t(q.tok0 + r_tok) * p.out_a.ts + (hk * p.group + r_head) * p.out_a.hs +
+                                  (D / 2) * h,
+                              real, limit <= 0);
+            ptx::tc_fence_before();
+            gs += uint32_t(n);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- dK / dV
+template <int D>
+struct DkvCfg {
+    static constexpr int kBlk = 128 * D * 2;
+    static constexpr int kStages = 2;
+    static constexpr int kKOff = 0, kVOff = kBlk;
+    // stage: Q block, dO block, -LSE log2(e) [128], -D [128]
+    static constexpr int kStQ = 0, kStDO = kBlk, kStL = 2 * kBlk, kStD = 2 * kBlk + 512;
+    static constexpr int kStageBytes = 2 * kBlk + 1024;
+    static constexpr int kStageOff = 2 * kBlk;
+    static constexpr int kBarOff = kStageOff + kStages * kStageBytes;
+    // st_full[2], st_empty[2], kv_full, kv_empty, s_full, dp_full, p_full,
+    // ds_full, dkv_full, drain, item_full[Q], item_empty[Q]
+    static constexpr int kNumBars = 2 * kStages + 8 + 2 * kItemQ;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+    static constexpr int kSmemBytes = kMiscOff + 8 + 4 * kItemQ + 1024;
+    static constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 256 + D;
+    static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+    static_assert(kColDK + D <= kTmemCols, "TMEM budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                   const BwdParams p) {
+    using C = DkvCfg<D>;
+    constexpr int NS = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw_base);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const uint32_t bar0 = base + C::kBarOff;
+    auto st_full = [&](int r) { return bar0 + 8u * r; };
+    auto st_empty = [&](int r) { return bar0 + 8u * (NS + r); };
+    const uint32_t xb = bar0 + 8u * (2 * NS);
+    const uint32_t kv_full = xb, kv_empty = xb + 8, s_full = xb + 16, dp_full = xb + 24, p_full = xb + 32,
+                   ds_full = xb + 40, dkv_full = xb + 48, drain = xb + 56;
+    const uint32_t item_full0 = xb + 64, item_empty0 = xb + 64 + 8 * kItemQ;
+    auto stage_off = [&](int r) { return C::kStageOff + r * C::kStageBytes; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    volatile int32_t* item_q = reinterpret_cast<volatile int32_t*>(smem + C::kMiscOff + 8);
+    const int rows_used = (128 / p.group) * p.group;  // rows of a query block's box
+
+    if (threadIdx.x == 0) {
+        for (int r = 0; r < NS; ++r) {
+            ptx::mbar_init(st_full(r), 1);
+            ptx::mbar_init(st_empty(r), 1);
+        }
+        ptx::mbar_init(kv_full, 1);
+        ptx::mbar_init(kv_empty, 1);
+        ptx::mbar_init(s_full, 1);
+        ptx::mbar_init(dp_full, 1);
+        ptx::mbar_init(p_full, kEwWarps);
+        ptx::mbar_init(ds_full, kEwWarps);
+        ptx::mbar_init(dkv_full, 1);
+        ptx::mbar_init(drain, 1);
+        for (int q = 0; q < kItemQ; ++q) {
+            ptx::mbar_init(item_full0 + 8u * q, 1);
+            ptx::mbar_init(item_empty0 + 8u * q, kItemConsumers);
+        }
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        ptx::prefetch_tensormap(&tm_q);
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+        ptx::prefetch_tensormap(&tm_do);
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    // Rows that no box ever writes (128 is no multiple of the group): zeros for good.
+    if (warp < kEwWarps && rows_used < 128)
+        for (int r = 0; r < NS; ++r) {
+            zero_rows<D>(smem + stage_off(r) + C::kStQ, rows_used, threadIdx.x);
+            zero_rows<D>(smem + stage_off(r) + C::kStDO, rows_used, threadIdx.x);
+        }
+    ops::grid_wait();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int32_t K = p.kv_heads;
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ load
+            const int32_t n_items = p.v.lists->n_k * K;
+            uint32_t sit = 0, kvc = 0;
+            bool ok = true;
+            for (uint32_t kq = 0; ok; ++kq) {
+                const int32_t u = put_item(kq, &p.v.lists->next_k, n_items, item_full0, item_empty0, item_q, abort_flag, p);
+                if (u < 0) break;
+                const KBlock kb = p.v.kblocks[p.v.order_k[u / K]];
+                const int32_t hk = u % K;
+                if (!wait_bw(kv_empty, (kvc & 1u) ^ 1u, abort_flag, p)) break;
+                ptx::mbar_arrive_expect_tx(kv_full, 2 * C::kBlk);
+                load_block<D>(base + C::kKOff, &tm_k, kv_full, hk, kb.key0);
+                load_block<D>(base + C::kVOff, &tm_v, kv_full, hk, kb.key0);
+                ++kvc;
+                for (int32_t j = 0; j < kb.nq; ++j) {
+                    const int r = int(sit % NS);
+                    if (sit >= uint32_t(NS) && !wait_bw(st_empty(r), ((sit / NS) - 1) & 1u, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    const int32_t tok = p.v.qblocks[kb.q0 + j].tok0;
+                    const int64_t row = (int64_t(kb.q0 + j) * K + hk) * 128;
+                    const uint32_t st = base + stage_off(r);
+                    ptx::mbar_arrive_expect_tx(st_full(r), 2 * (D / 64) * p.q_box_bytes + 1024);
+                    load_block<D>(st + C::kStQ, &tm_q, st_full(r), hk * p.group, tok);
+                    load_block<D>(st + C::kStDO, &tm_do, st_full(r), hk * p.group, tok);
+                    ptx::bulk_load(st + C::kStL, p.neg_l + row, 512, st_full(r));
+                    ptx::bulk_load(st + C::kStD, p.neg_d + row, 512, st_full(r));
+                    ++sit;
+                }
+            }
+            for (uint32_t it = sit > uint32_t(NS) ? sit - NS : 0u; it < sit; ++it)
+                drain_bar(st_full(int(it % NS)), (it / NS) & 1u, p.timeout_ns);
+            if (kvc > 0) drain_bar(kv_full, (kvc - 1) & 1u, p.timeout_ns);
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            // ------------------------------------------------------------- MMA
+            constexpr uint32_t idesc_s = ptx::idesc_bf16(128, 128, false);
+            constexpr uint32_t idesc_acc = ptx::idesc_bf16(128, D, true);
+            const uint32_t kaddr = base + C::kKOff, vaddr = base + C::kVOff;
+            uint32_t gs = 0, kvc = 0;
+            bool ok = true;
+            for (uint32_t kq = 0; ok; ++kq) {
+                int32_t u;
+                if (!get_item(kq, item_full0, item_q, abort_flag, p, u)) break;
+                ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
+                if (u < 0) break;
+                const int32_t n = p.v.kblocks[p.v.order_k[u / K]].nq;
+                if (!wait_bw(kv_full, kvc & 1u, abort_flag, p)) break;
+                ++kvc;
+                ptx::tc_fence_after();
+                // S^T_j = K Q_j^T (waits for stage j)
+                auto issue_s = [&](int32_t j) -> bool {
+                    const uint32_t it = gs + uint32_t(j);
+                    if (!wait_bw(st_full(int(it % NS)), (it / NS) & 1u, abort_flag, p)) return false;
+                    ptx::tc_fence_after();
+                    const uint32_t qaddr = base + stage_off(int(it % NS)) + C::kStQ;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t coff = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+                        ptx::mma_ss(tmem + C::kColS, ptx::desc_k_sw128(kaddr + coff), ptx::desc_k_sw128(qaddr + coff),
+                                    idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit(s_full);
+                    return true;
+                };
+                // dP^T_j = V dO_j^T (stage j already waited for by issue_s)
+                auto issue_dp = [&](int32_t j) {
+                    const uint32_t it = gs + uint32_t(j);
+                    const uint32_t doaddr = base + stage_off(int(it % NS)) + C::kStDO;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t coff = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+                        ptx::mma_ss(tmem + C::kColDP, ptx::desc_k_sw128(vaddr + coff), ptx::desc_k_sw128(doaddr + coff),
+                                    idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit(dp_full);
+                };
+                if (n > 0) {
+                    ok = issue_s(0);
+                    if (ok) issue_dp(0);
+                }
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    const uint32_t it = gs + uint32_t(j);
+                    const uint32_t st = base + stage_off(int(it % NS));
+                    if (!wait_bw(p_full, it & 1u, abort_flag, p)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    // dV += P^T_j dO_j
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        ptx::mma_ts(tmem + C::kColDV, tmem + C::kColS + a_col(kk),
+                                    ptx::desc_mn_sw128(st + C::kStDO + kk * 16 * 128, kBoxBytes), idesc_acc,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+                    // in issue order after dV_j, which reads the P^T this S^T overwrites
+                    if (j + 1 < n && !issue_s(j + 1)) { ok = false; break; }
+                    if (!wait_bw(ds_full, it & 1u, abort_flag, p)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    // dK += dS^T_j Q_j
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        ptx::mma_ts(tmem + C::kColDK, tmem + C::kColDP + a_col(kk),
+                                    ptx::desc_mn_sw128(st + C::kStQ + kk * 16 * 128, kBoxBytes), idesc_acc,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit(st_empty(int(it % NS)));
+                    // after dK_j, which reads the dS^T this dP^T overwrites
+                    if (j + 1 < n) issue_dp(j + 1);
+                }
+                if (!ok) break;
+                ptx::mma_commit(dkv_full);
+                ptx::mma_commit(kv_empty);
+                gs += uint32_t(n);
+            }
+            ptx::mma_commit(drain);
+            drain_bar(drain, 0, p.timeout_ns);
+        }
+    } else {
+        // ------------------------------------------------------- elementwise
+        const int h = warp >> 2;  // query-column half
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
+        const uint64_t c2 = ptx::f2(p.scale_log2, p.scale_log2);
+        uint32_t gs = 0, kvc = 0;
+        bool ok = true;
+        for (uint32_t kq = 0; ok; ++kq) {
+            int32_t u = -1;
+            if (!__all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, u))) break;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
+            if (u < 0) break;
+            const KBlock kb = p.v.kblocks[p.v.order_k[u / K]];
+            const int32_t hk = u % K, n = kb.nq;
+            for (int32_t j = 0; j < n; ++j) {
+                const uint32_t step = gs + uint32_t(j);
+                const int r = int(step % NS);
+                // the stage's per-column constants (TMA-written) and the scores
+                if (!__all_sync(~0u, wait_bw(st_full(r), (step / NS) & 1u, abort_flag, p) &&
+                                         wait_bw(s_full, step & 1u, abort_flag, p))) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                uint8_t* st = smem + stage_off(r);
+                const int32_t limit0 = p.v.qblocks[kb.q0 + j].limit0, rows = p.v.qblocks[kb.q0 + j].ntok * p.group;
+                const bool ragged = rows < rows_used;
+                // query rows [from, to) of this half see this thread's key
+                const int from = (p.causal ? p.group * max(0, kb.pos + row - limit0 + 1) : 0) - 64 * h, to = rows - 64 * h;
+                const bool masked = ragged || (p.causal && kb.pos + 127 >= limit0);
+                if (ragged) zero_rows<D>(st + C::kStDO, rows, threadIdx.x);
+                // per-column constants, 16-byte broadcast loads
+                const float4* cl = reinterpret_cast<const float4*>(st + C::kStL) + 16 * h;
+                const float4* cd = reinterpret_cast<const float4*>(st + C::kStD) + 16 * h;
+                const uint32_t ts = tmem + lane_addr + C::kColS + 64u * h;
+                float pr[64];
+                uint32_t pk[32];
+                {
+                    uint32_t sr[64];
+                    ptx::tmem_ld64(ts, sr);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 l = cl[i];
+                        float x0, x1, x2, x3;
+                        ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1])),
+                                                  c2, ptx::f2(l.x, l.y)),
+                                      x0, x1);
+                        ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3])),
+                                                  c2, ptx::f2(l.z, l.w)),
+                                      x2, x3);
+                        pr[4 * i] = ptx::ex2(x0);
+                        pr[4 * i + 1] = ptx::ex2(x1);
+                        pr[4 * i + 2] = ptx::ex2(x2);
+                        pr[4 * i + 3] = ptx::ex2(x3);
+                    }
+                }
+                if (masked)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (i < from || i >= to) pr[i] = 0.0f;
+                pack64(pr, pk);
+                ptx::tmem_st32(ts, pk);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(p_full);
+                if (ragged) zero_rows<D>(st + C::kStQ, rows, threadIdx.x);
+                if (!__all_sync(~0u, wait_bw(dp_full, step & 1u, abort_flag, p))) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t tdp = tmem + lane_addr + C::kColDP + 64u * h;
+                {
+                    uint32_t dr[64];
+                    ptx::tmem_ld64(tdp, dr);
+                    if (masked)
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i < from || i >= to) dr[i] = 0u;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 dd = cd[i];
+                        float t0, t1, t2, t3;
+                        ptx::f2_split(ptx::f2_mul(ptx::f2(pr[4 * i], pr[4 * i + 1]),
+                                                  ptx::f2_add(ptx::f2(__uint_as_float(dr[4 * i]),
+                                                                      __uint_as_float(dr[4 * i + 1])),
+                                                              ptx::f2(dd.x, dd.y))),
+                                      t0, t1);
+                        ptx::f2_split(ptx::f2_mul(ptx::f2(pr[4 * i + 2], pr[4 * i + 3]),
+                                                  ptx::f2_add(ptx::f2(__uint_as_float(dr[4 * i + 2]),
+                                                                      __uint_as_float(dr[4 * i + 3])),
+                                                              ptx::f2(dd.z, dd.w))),
+                                      t2, t3);
+                        pk[2 * i] = ptx::pack_bf16x2(t0, t1);
+                        pk[2 * i + 1] = ptx::pack_bf16x2(t2, t3);
+                    }
+                }
+                ptx::tmem_st32(tdp, pk);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ds_full);
+            }
+            if (!ok) break;
+            if (!__all_sync(~0u, wait_bw(dkv_full, kvc & 1u, abort_flag, p))) break;
+            ++kvc;
+            ptx::tc_fence_after();
+            const bool real = row < kb.nkeys;
+            const int64_t tok = kb.key0 + row;
+            store_cols<D / 2>(tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h, 1.0f,
+                              p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + (D / 2) * h, real, n == 0);
+            store_cols<D / 2>(tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h, p.scale,
+                              p.out_a.p + tok * p.out_a.ts + hk * p.out_a.hs + (D / 2) * h, real, n == 0);
+            ptx::tc_fence_before();
+            gs += uint32_t(n);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- no queries, or no keys
+// Gradients of sequences whose other side is empty: zeros.
+__global__ void packed_zero_dq_kernel(const PackedProblem p, const packed::View v, int head_dim, Rows dq) {
+    ops::grid_wait();
+    const int parts = head_dim / 8;
+    for (int e = blockIdx.x; e < v.lists->n_q; e += gridDim.x) {
+        const QBlock q = v.qblocks[e];
+        for (int i = threadIdx.x; i < q.ntok * p.heads * parts; i += blockDim.x) {
+            const int row = i / parts;
+            *reinterpret_cast<uint4*>(dq.p + int64_t(q.tok0 + row / p.heads) * dq.ts + row % p.heads * dq.hs +
+                                      i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+__global__ void packed_zero_dkdv_kernel(const PackedProblem p, const packed::View v, int head_dim, Rows dk, Rows dv) {
+    ops::grid_wait();
+    const int parts = head_dim / 8;
+    for (int e = blockIdx.x; e < v.lists->n_k; e += gridDim.x) {
+        const KBlock k = v.kblocks[e];
+        for (int i = threadIdx.x; i < k.nkeys * p.kv_heads * parts; i += blockDim.x) {
+            const int row = i / parts, h = row % p.kv_heads;
+            const int64_t tok = k.key0 + row / p.kv_heads;
+            *reinterpret_cast<uint4*>(dk.p + tok * dk.ts + h * dk.hs + i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(dv.p + tok * dv.ts + h * dv.hs + i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch_bwd(const PackedProblem& p, const Rows& q, const Rows& k, const Rows& v, const Rows& o,
+                       const Rows& dout, const float* lse, const Rows& dq, const Rows& dk, const Rows& dv, char* ws,
+                       const packed::Layout& w, const packed::View& view, int sms, cudaStream_t stream) {
+    const int tpb = 128 / p.group;
+    CUtensorMap mq, mk, mv, md;
+    cudaError_t e = packed::rows_map(&mq, q, p.tokens_q, p.heads, D, p.group, tpb);
+    if (e == cudaSuccess) e = packed::rows_map(&md, dout, p.tokens_q, p.heads, D, p.group, tpb);
+    if (e == cudaSuccess) e = packed::rows_map(&mk, k, p.tokens_k, p.kv_heads, D, 1, 128);
+    if (e == cudaSuccess) e = packed::rows_map(&mv, v, p.tokens_k, p.kv_heads, D, 1, 128);
+    if (e != cudaSuccess) return e;
+    float* neg_l = reinterpret_cast<float*>(ws + w.neg_l);
+    float* neg_d = reinterpret_cast<float*>(ws + w.neg_d);
+    BwdParams bp{view, p.kv_heads, p.group, p.causal, neg_l, neg_d, dq, dq, p.scale, p.scale * kLog2e,
+                 uint32_t(p.group * tpb) * 128u, p.status, kOpTimeoutNs};
+    constexpr int kDq = smem_launch(DqCfg<D>::kSmemBytes), kDkv = smem_launch(DkvCfg<D>::kSmemBytes);
+    e = cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDq);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(packed_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkv);
+    const int64_t nq = w.max_q * p.kv_heads, nk = w.max_k * p.kv_heads;
+    if (e == cudaSuccess)
+        e = packed::launch(packed_prep_kernel<D>, unsigned(nq < 4 * sms ? nq : 4 * sms), 256, 0, stream, true, p, view, o,
+                           dout, lse, neg_l, neg_d);
+    if (e == cudaSuccess)
+        e = packed::launch(packed_dq_kernel<D>, unsigned(nq < sms ? nq : sms), kThreads, kDq, stream, true, mq, mk, mv, md,
+                           bp);
+    bp.out_a = dk;
+    bp.out_b = dv;
+    if (e == cudaSuccess)
+        e = packed::launch(packed_dkdv_kernel<D>, unsigned(nk < sms ? nk : sms), kThreads, kDkv, stream, true, mq, mk, mv,
+                           md, bp);
+    return e;
 }
 
 }  // namespace
@@ -104,17 +893,27 @@ __global__ void packed_dkdv_simple(PackedProblem p, Rows q, Rows k, Rows v, Rows
 cudaError_t launch_packed_backward(const PackedProblem& p, int head_dim, const Rows& q, const Rows& k, const Rows& v,
                                    const Rows& o, const Rows& dout, const float* lse, const Rows& dq, const Rows& dk,
                                    const Rows& dv, void* workspace, cudaStream_t stream) {
-    float* dsum = static_cast<float*>(workspace) + 64;  // within the workspace: heads * tokens_q floats
-    const unsigned gq = unsigned((int64_t(p.tokens_q) * p.heads + 3) / 4),
-                   gk = unsigned((int64_t(p.tokens_k) * p.kv_heads + 3) / 4);
-    if (head_dim == 128) {
-        if (gq) packed_dq_simple<128><<<gq, 128, 0, stream>>>(p, q, k, v, o, dout, lse, dq, dsum);
-        if (gk) packed_dkdv_simple<128><<<gk, 128, 0, stream>>>(p, q, k, v, dout, lse, dsum, dk, dv);
-    } else {
-        if (gq) packed_dq_simple<64><<<gq, 128, 0, stream>>>(p, q, k, v, o, dout, lse, dq, dsum);
-        if (gk) packed_dkdv_simple<64><<<gk, 128, 0, stream>>>(p, q, k, v, dout, lse, dsum, dk, dv);
-    }
-    return cudaGetLastError();
+    const packed::Layout w = packed::layout(p, true);
+    const packed::View view = packed::view(w, workspace);
+    packed::Tails tails{};
+    tails.r[0] = dq;
+    tails.r[1] = dk;
+    tails.r[2] = dv;
+    tails.heads[0] = p.heads;
+    tails.heads[1] = tails.heads[2] = p.kv_heads;
+    tails.is_q[0] = 1;
+    tails.n = 3;
+    int sms = 0;
+    cudaError_t e = packed::sm_count(&sms);
+    if (e == cudaSuccess) e = packed::launch_lists(p, view, true, head_dim, tails, stream);
+    if (e != cudaSuccess || p.batch == 0) return e;
+    if (p.tokens_k == 0)
+        return packed::launch(packed_zero_dq_kernel, unsigned(sms), 256, 0, stream, true, p, view, head_dim, dq);
+    if (p.tokens_q == 0)
+        return packed::launch(packed_zero_dkdv_kernel, unsigned(sms), 256, 0, stream, true, p, view, head_dim, dk, dv);
+    if (head_dim == 128)
+        return launch_bwd<128>(p, q, k, v, o, dout, lse, dq, dk, dv, static_cast<char*>(workspace), w, view, sms, stream);
+    return launch_bwd<64>(p, q, k, v, o, dout, lse, dq, dk, dv, static_cast<char*>(workspace), w, view, sms, stream);
 }
 
 }  // namespace sta

@@ -202,7 +202,7 @@ def test_extend(sta, batch, hi, new_hi, bt, short, in_place):
     t, f, n, c = dev(tables), dev(free), dev(lengths), dev([count])
     s = sta.sta_cache_extend(dev(new), n, t, f, c, bt, max_slots, in_place=in_place)
     torch.cuda.synchronize()
-    got = (t.tolist(), f.tolist(), s.slots.tolist(), s.cu_new.tolist(), s.lengths.tolist(), int(s.free_count), int(s.shortage))
+    got = (t.tolist(), f.tolist(), s.slots.tolist(), s.cu_new.tolist(), s.lengths.tolist(), int(s.free_count), int(s.short))
     for name, a, b in zip(("tables", "free", "slots", "cu", "lengths", "count", "short"), got, want):
         assert a == b, name
     assert (s.lengths is n) == in_place and (n.tolist() == lengths) == (not in_place or want[4] == lengths)
@@ -217,7 +217,7 @@ def test_extend_refuses_on_the_device(sta):
                                            ([2 ** 31 - 1, 2 ** 31 - 1], [5, 5], 3, 9), ([-1, 2], [17, 5], 3, 9)):
         t, f = dev([[0, 1, 2, 3], [0, 1, 2, 3]]), dev([9, 8, 7, 6])
         s = sta.sta_cache_extend(dev(new), dev(lengths), t, f, dev([count]), 16, max_slots)
-        assert int(s.shortage) == -1 and s.lengths.tolist() == lengths and int(s.free_count) == count
+        assert int(s.short) == -1 and s.lengths.tolist() == lengths and int(s.free_count) == count
         assert s.cu_new.tolist() == [0, 0, 0] and set(s.slots.tolist()) <= {-1}
         assert t.tolist() == [[0, 1, 2, 3]] * 2 and f.tolist() == [9, 8, 7, 6]
 
@@ -381,7 +381,7 @@ def test_serving_prompts_and_tokens(sta, H, K, d, bt):
     q, k, v = qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:]
     step = sta.sta_cache_extend(torch.tensor(prompt, dtype=torch.int32, device="cuda"), lengths, tables, free, count, bt,
                                 sum(prompt), in_place=True)
-    assert int(step.shortage) == 0
+    assert int(step.short) == 0
     o, lse = sta.sta_packed_attention(q, k, v, step.cu_new)
     want = ref.packed(q, k, v, prompt, prompt, True, 1 / math.sqrt(d))
     ref.check(o, want, "o")
@@ -414,7 +414,7 @@ def test_serving_prompts_and_tokens(sta, H, K, d, bt):
         torch.cuda.synchronize()
         now = new.tolist()
         held = [0 if a < 0 else n + a for n, a in zip(held, now)]
-        assert int(s.shortage) == 0 and lengths.tolist() == held
+        assert int(s.short) == 0 and lengths.tolist() == held
         blocks = sum(-(-n // bt) for n in held)
         assert int(count) == pool - blocks
         used = [int(tables[b, j]) for b in range(B) for j in range(-(-held[b] // bt))] + free[:int(count)].tolist()

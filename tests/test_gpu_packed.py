@@ -300,3 +300,29 @@ def test_empty_problems(sta):
     dq, _, _ = sta.sta_packed_attention_backward(q9, k, k, o, lse, q9, cu9, cu0, causal=False)
     assert not bool(dq.any())
     assert sta.sta_operator_status() == 0
+
+
+@pytest.mark.parametrize("cu_q,cu_k", [([0, 90, 40, 130], [0, 90, 40, 130]), ([0, 60, 500], [0, 60, 500]),
+                                       ([-5, 60, 130], [-5, 60, 130]), ([0, 130], [0, 2 ** 31 - 1]),
+                                       ([0, 60, 60, -1], [0, -7, 20, 130])])
+def test_bounds_that_do_not_fit_are_cut_and_reported(sta, cu_q, cu_k):
+    """Bounds that decrease or leave the tensors: the call is the one with the cut bounds, and says BOUNDS."""
+    T, H, K, d = 130, 4, 2, 64
+    q, k, v, do = make([T], [T], H, K, d, seed=14)
+
+    def cut(c):
+        out, top = [], 0
+        for x in c:
+            top = max(top, min(x, T))
+            out.append(top)
+        return torch.tensor(out, dtype=torch.int32, device="cuda")
+
+    def both(a, b):
+        o, lse = sta.sta_packed_attention(q, k, v, a, b)
+        return (o, lse) + sta.sta_packed_attention_backward(q, k, v, o, lse, do, a, b)
+    want = both(cut(cu_q), cut(cu_k))
+    assert sta.sta_operator_status() == 0
+    got = both(*(torch.tensor(c, dtype=torch.int32, device="cuda") for c in (cu_q, cu_k)))
+    assert sta.sta_operator_status() == sta.STA_ERR_BOUNDS
+    assert sta.sta_operator_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
