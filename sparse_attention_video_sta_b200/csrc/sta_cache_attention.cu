@@ -16,21 +16,29 @@
 namespace sta {
 namespace {
 
-// One warp streams tiles of 32 tokens through its own ring in shared memory; a CTA is 8
-// such warps and has its SM alone (192 KB of ring: 24 KB in flight for each warp, several
+// Each warp streams tiles of 16 tokens through its own ring in shared memory and waits for
+// another warp only at the end of its run.  A CTA has its SM alone (192 KB of rings: several
 // times what 1 us of HBM latency needs).
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 32;      // tokens of a tile
-constexpr int kRowTile = 16;   // query rows of a unit: one mma.m16n8k16 A operand
+constexpr int kTile = 16;      // tokens of a tile: in one block, whatever the block size
+constexpr int kPlanWarps = 8;  // warps that sum the sequences
+constexpr int kMinTiles = 4;   // a warp takes no fewer tiles, a CTA no fewer than two warps' worth
 constexpr int kMaxSms = 148;   // of a B200, for workspaces asked for without a device
-constexpr int kMinTiles = 8;   // a CTA takes no fewer tiles than it has warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -3.0e38f;  // running maximum of a row that has seen no key
+constexpr float kRise = 8.0f;      // log2 by which a score may pass the running maximum before it is raised
+
+// A unit, as its joins need it: its tiles, its first query token, the number of its rows, its
+// first row of (token, head) and its first query head.  unit0 < 0: none.
+struct Unit {
+    int64_t unit0, unit1;
+    int32_t q0, rows, row0, head;
+};
 
 struct CacheArgs {
     PackedProblem p;
-    int32_t blocks, bt;
+    int32_t blocks, bt, bt_log2;
+    int32_t row_tile;  // query rows of a unit
     const float* k_scales;
     const float* v_scales;
     const int32_t* lengths;
@@ -39,14 +47,18 @@ struct CacheArgs {
     int64_t stride;
     Rows q, o;
     float* lse;
-    float* parts;  // [2 * CTAs][16 rows][D + 4]: O, m, l, mw
+    float* warp_parts;  // [CTAs][warps][2][row_tile][D + 4]: O, m, l, mw
+    float* cta_parts;   // [CTAs][2][row_tile][D + 4]
+    Unit* begins;       // [CTAs]: the unit that a CTA's run begins inside of
+    int64_t* head;      // tiles of all units, CTAs that take part
     uint64_t timeout_ns;
 };
 
-// The work: units of (sequence, 16 query rows, key head), each of the sequence's tiles; all
-// units' tiles in one row, cut into equal runs, one for each CTA.  A unit that lies in one
-// run is finished there; the others' parts are joined by the second kernel, in the
-// order of the runs.
+// The work: units of (sequence, `row_tile` query rows, key head), each of the sequence's tiles; all
+// units' tiles in one row, cut into equal runs, one for each CTA, and those again, one for each
+// warp.  A unit that lies in one warp's run is finished there; the parts of the others are
+// joined by the CTA, and those of units that lie in several CTAs' runs by the second kernel,
+// always in the order of the runs.
 struct Sequence {
     int32_t q0, nq;      // its queries
     int32_t len, raw;    // tokens in the table; as given
@@ -68,57 +80,53 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b, bool* cu
     s.len = max(0, min(s.raw, a.width * a.bt));
     *cut |= s.raw != s.len;
     s.tiles = max(1, (s.len + kTile - 1) / kTile);
-    s.units = (s.nq * a.p.group + kRowTile - 1) / kRowTile * a.p.kv_heads;
+    s.units = (s.nq * a.p.group + a.row_tile - 1) / a.row_tile * a.p.kv_heads;
     return s;
 }
 
 struct PlanShared {
-    int64_t scan[kWarps];
-    int64_t total;
-    int64_t before;   // tiles of the sequences before `seq`
-    int32_t seq;
+    int64_t scan[kPlanWarps];
     int32_t last;     // end of the last sequence's queries
 };
 
-// Tiles of all units; the last query row.
+// Tiles of all units; the last query row.  (The first 8 warps sum; every thread calls.)
 __device__ int64_t plan_total(const CacheArgs& a, PlanShared& sh, bool report) {
     int64_t n = 0;
     int32_t last = 0;
     bool cut = false;
-    for (int b = threadIdx.x; b < a.p.batch; b += kThreads) {
-        const Sequence s = sequence(a, b, &cut);
-        n += int64_t(s.tiles) * s.units;
-        last = max(last, s.q0 + s.nq);
-    }
-    for (int i = 16; i > 0; i >>= 1) {
-        n += __shfl_xor_sync(~0u, n, i);
-        last = max(last, __shfl_xor_sync(~0u, last, i));
-    }
     if (threadIdx.x == 0) sh.last = 0;
     __syncthreads();
-    if (threadIdx.x % 32 == 0) {
-        sh.scan[threadIdx.x / 32] = n;
-        atomicMax(&sh.last, last);
+    if (threadIdx.x < kPlanWarps * 32) {
+        for (int b = threadIdx.x; b < a.p.batch; b += kPlanWarps * 32) {
+            const Sequence s = sequence(a, b, &cut);
+            n += int64_t(s.tiles) * s.units;
+            last = max(last, s.q0 + s.nq);
+        }
+        for (int i = 16; i > 0; i >>= 1) {
+            n += __shfl_xor_sync(~0u, n, i);
+            last = max(last, __shfl_xor_sync(~0u, last, i));
+        }
+        if (threadIdx.x % 32 == 0) {
+            sh.scan[threadIdx.x / 32] = n;
+            atomicMax(&sh.last, last);
+        }
     }
     if (__syncthreads_or(cut) && report && threadIdx.x == 0) atomicOr(a.p.status, kDevBounds);
     n = 0;
-    for (int i = 0; i < kWarps; ++i) n += sh.scan[i];
+    for (int i = 0; i < kPlanWarps; ++i) n += sh.scan[i];
     __syncthreads();
     return n;
 }
 
-// The sequence that holds tile `at` (sh.seq) and the tiles before it (sh.before).
-__device__ void plan_locate(const CacheArgs& a, PlanShared& sh, int64_t at) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The sequence that holds tile `at`, and the tiles before it (one warp).
+__device__ int32_t plan_locate(const CacheArgs& a, int64_t at, int64_t* before) {
+    const int lane = threadIdx.x & 31;
     int64_t carry = 0;
-    if (threadIdx.x == 0) sh.seq = -1;
-    __syncthreads();
-    for (int b0 = 0; b0 < a.p.batch; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
+    for (int b0 = 0;; b0 += 32) {
         bool cut = false;
         int64_t v = 0;
-        if (b < a.p.batch) {
-            const Sequence s = sequence(a, b, &cut);
+        if (b0 + lane < a.p.batch) {
+            const Sequence s = sequence(a, b0 + lane, &cut);
             v = int64_t(s.tiles) * s.units;
         }
         int64_t x = v;
@@ -126,34 +134,29 @@ __device__ void plan_locate(const CacheArgs& a, PlanShared& sh, int64_t at) {
             const int64_t y = __shfl_up_sync(~0u, x, i);
             if (lane >= i) x += y;
         }
-        if (lane == 31) sh.scan[warp] = x;
-        __syncthreads();
-        int64_t base = carry;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) base += sh.scan[i];
-            carry += sh.scan[i];
+        const uint32_t past = __ballot_sync(~0u, carry + x > at);
+        if (past != 0u) {
+            const int src = __ffs(past) - 1;
+            *before = carry + __shfl_sync(~0u, x - v, src);
+            return b0 + src;
         }
-        if (v > 0 && at >= base + x - v && at < base + x) {
-            sh.seq = b;
-            sh.before = base + x - v;
-        }
-        __syncthreads();
-        if (carry > at) break;
+        carry += __shfl_sync(~0u, x, 31);
+        if (b0 + 32 >= a.p.batch) return -1;  // (at is below the total: not reached)
     }
 }
 
-// CTAs that take part, and the first tile of CTA i of them.
-__device__ __forceinline__ int64_t plan_ctas(int64_t total, int64_t grid) {
-    const int64_t most = (total + kMinTiles - 1) / kMinTiles;
-    return most < grid ? most : grid;
+// CTAs that take part, and the first tile of CTA i of them (or of warp i of a CTA's).
+__device__ __forceinline__ int64_t plan_ctas(int64_t total, int64_t most) {
+    const int64_t some = (total + 2 * kMinTiles - 1) / (2 * kMinTiles);
+    return some < most ? some : most;
 }
-__device__ __forceinline__ int64_t plan_first(int64_t total, int64_t ctas, int64_t i) {
-    return total / ctas * i + total % ctas * i / ctas;
+__device__ __forceinline__ int64_t plan_first(int64_t total, int64_t parts, int64_t i) {
+    return total / parts * i + total % parts * i / parts;
 }
 
 // D += A B, m16n8k16, fp16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -167,69 +170,113 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// Writes one row's D / 16 outputs from `col` on, and its LSE.
-template <int D>
+// 8 x 8 transpose of 16-bit values held two to a register across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Writes E of one row's outputs from `col` on, and its LSE.
+template <int E>
 __device__ __forceinline__ void store_row(const CacheArgs& a, int32_t tok, int32_t head, int col, const float* x, float m,
                                           float l, float mw) {
-    constexpr int E = D / 16;
     const bool none = l == 0.0f;
     const float f = none ? 0.0f : ptx::ex2(mw - m) / l;
-    __nv_bfloat16* dst = a.o.p + int64_t(tok) * a.o.ts + head * a.o.hs + col;
-    uint32_t pk[E / 2];
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.o.p + int64_t(tok) * a.o.ts + head * a.o.hs + col);
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) pk[i] = none ? 0u : ptx::pack_bf16x2(x[2 * i] * f, x[2 * i + 1] * f);
-    if (E == 8)
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[E / 2 - 2], pk[E / 2 - 1]);
-    else
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+    for (int i = 0; i < E / 2; ++i) dst[i] = none ? 0u : ptx::pack_bf16x2(x[2 * i] * f, x[2 * i + 1] * f);
     if (col == 0) a.lse[int64_t(head) * a.p.tokens_q + tok] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// Attention over the cache.  For each tile a warp holds S (16 x 32) and O (16 x D) in registers:
-// S = Q K^T, P = 2^(S - m), O += W V by mma.m16n8k16 on fp16 operands with fp32 sums; the codes
-// become fp16 exactly (cvt), so no tensor is widened in memory.  Both products pick their
-// operands' order freely over the summed index: K's 16 bytes of a thread are four k-steps, V's
-// 16 bytes of two tokens sixteen output columns, and neither is ever transposed.
+// Joins one row's n parts (part(c), c = 0 .. n - 1) in one warp: lane i returns columns
+// i * D / 32 on of O in x, and m, l, mw.  Every share-th part from s on.
+template <int D, class Part>
+__device__ __forceinline__ void join_row(int64_t s, int64_t n, int share, const Part& part, float (&x)[D / 32], float& m,
+                                         float& l, float& mw) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    m = mw = kNone;
+    l = 0.0f;
+    for (int64_t c = s + int64_t(lane) * share; c < n; c += 32 * share) {
+        const float4 st = *reinterpret_cast<const float4*>(part(c) + D);
+        m = fmaxf(m, st.x);
+        mw = fmaxf(mw, st.z);
+    }
+    for (int k = 16; k > 0; k >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
+        mw = fmaxf(mw, __shfl_xor_sync(~0u, mw, k));
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.0f;
+#pragma unroll 8
+    for (int64_t c = s; c < n; c += share) {
+        const float* p = part(c);
+        const float4 st = *reinterpret_cast<const float4*>(p + D);
+        const float f = ptx::ex2(st.z - mw);
+        l += st.y * ptx::ex2(st.x - m);
+        if (E == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p + lane * E);
+            x[0] += y.x * f;
+            x[1] += y.y * f;
+            x[E - 2] += y.z * f;
+            x[E - 1] += y.w * f;
+        } else {
+            const float2 y = *reinterpret_cast<const float2*>(p + lane * E);
+            x[0] += y.x * f;
+            x[1] += y.y * f;
+        }
+    }
+}
+
+// Attention over the cache, transposed: S^T = K Q^T and O^T += V^T W^T by mma.m16n8k16, tokens
+// (then columns of V) as the 16 rows of an operand, 8 query rows as the columns.  A unit of 8
+// rows (NT = 1: one token of up to 8 heads to a key head) then takes half the products and
+// half the registers that rows-by-tokens would, and more rows (NT = 2, 4) share one widening
+// of the codes.  Operands are fp16 (the codes exactly, by cvt in registers: no widened copy
+// anywhere), sums fp32.  Both products choose their summed index's order freely: K's 16 bytes
+// of a thread are four k-steps, V's 16 bytes of two tokens are eight 2-row pieces of V^T after
+// a byte interleave, and W^T is one movmatrix from S^T.
 // A block's K scale multiplies the scores.  Its V scale 2^lv enters the exponent: W = 2^(S + lv - mw)
 // with a running maximum mw of its own, so that W rounds to fp16 (2^-11 relative) relative to
 // each row's largest contribution, however far the scales are apart; l sums the unscaled P
-// before any rounding.  Q is scaled by a power of two for each row into fp16's range.
-// HBM-bound: 2 D bytes for each token and key head; mma.sync suffices (a few rows of queries
-// leave a 128-row tcgen05 tile mostly empty, and the codes would have to be widened in
-// shared memory first).
-template <int D>
+// = 2^(S - m) before any rounding.  Both maxima are raised only when a tile passes them by 2^8,
+// which fp16 and fp32 bear and which makes rescaling O rare.  Q is scaled by a power of two
+// for each row into fp16's range.
+// HBM-bound: 2 D bytes for each token and key head.
+template <int D, int NT>
 struct Cfg {
-    static constexpr int kTileBytes = kTile * D;           // of K or V
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kRows = 8 * NT;
+    // O^T and Q^T take (D / 4 + D / 8) * NT registers: 16 warps of 128 where that is at most 48
+    static constexpr int kWarps = NT * D <= 128 ? 16 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kTileBytes = kTile * D;  // of K or V
+    static constexpr int kStages = 192 * 1024 / (kWarps * 2 * kTileBytes) < 8 ? 192 * 1024 / (kWarps * 2 * kTileBytes) : 8;
     static constexpr int kRing = kWarps * kStages * 2 * kTileBytes;
-    static constexpr int kMetaOff = kRing;                 // {ks0, ks1, lv0, lv1} for each warp and stage
-    static constexpr int kBarOff = kMetaOff + kWarps * kStages * 16;
-    static constexpr int kStatOff = kBarOff + kWarps * kStages * 8;  // [3][8 warps][16 rows]: m, l, mw
-    static constexpr int kSmem = kStatOff + 3 * kWarps * kRowTile * 4 + 1024;
-    static_assert(kWarps * kRowTile * (D + 4) * 4 <= kRing, "the warps' O fit in the ring");
-    static_assert(kSmem <= 226 * 1024, "shared memory budget");
+    static constexpr int kMetaOff = kRing;                           // {ks, lv} for each warp and stage
+    static constexpr int kBarOff = kMetaOff + kWarps * kStages * 8;
+    static constexpr int kSmem = kBarOff + kWarps * kStages * 8 + 1024;
+    static_assert(kSmem <= 224 * 1024, "shared memory budget");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const CacheArgs a) {
-    using C = Cfg<D>;
-    constexpr int S = C::kStages;
-    constexpr int kSteps = D / 16;    // k-steps of Q K^T
-    constexpr int kCols = D / 8;      // 8-column tiles of O
+    using C = Cfg<D, NT>;
+    constexpr int S = C::kStages, kWarps = C::kWarps, kThreads = C::kThreads, kRows = C::kRows;
+    constexpr int kSteps = D / 16;    // k-steps of K Q^T, 16-row tiles of O^T
     extern __shared__ uint8_t smem_raw[];
     __shared__ PlanShared plan;
+    __shared__ Unit ends[kWarps][2];  // each warp's parts: of the unit that it begins inside of, of its last
     const uint32_t raw_base = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw_base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int K = a.p.kv_heads, G = a.p.group;
-    float4* meta = reinterpret_cast<float4*>(smem + C::kMetaOff) + warp * S;
+    float2* meta = reinterpret_cast<float2*>(smem + C::kMetaOff) + warp * S;
     const uint32_t bar0 = base + C::kBarOff + warp * S * 8;
     uint8_t* ring = smem + warp * S * 2 * C::kTileBytes;
-    float* part_o = reinterpret_cast<float*>(smem);       // [8 warps][16 rows][D + 4], over the rings
-    float* stat = reinterpret_cast<float*>(smem + C::kStatOff);
     if (lane == 0) {
         for (int i = 0; i < S; ++i) ptx::mbar_init(bar0 + 8u * i, 1);
         ptx::fence_barrier_init();
@@ -249,13 +296,23 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         }
     }
     const int64_t ctas = plan_ctas(total, gridDim.x);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.head[0] = total;
+        a.head[1] = ctas;
+    }
     if (blockIdx.x >= ctas) return;
-    int64_t at = plan_first(total, ctas, blockIdx.x);
-    const int64_t end = plan_first(total, ctas, blockIdx.x + 1);
-    plan_locate(a, plan, at);
-    int32_t b = plan.seq;
-    int64_t before = plan.before;
-    uint32_t issued = 0, taken = 0;  // tiles of this warp so far: ring slot and phase
+    const int64_t cta_begin = plan_first(total, ctas, blockIdx.x), cta_end = plan_first(total, ctas, blockIdx.x + 1);
+    const int64_t n_tiles = cta_end - cta_begin, some = (n_tiles + kMinTiles - 1) / kMinTiles;
+    const int warps = int(some < kWarps ? some : kWarps);  // that have a run
+    const int64_t begin = cta_begin + (warp < warps ? plan_first(n_tiles, warps, warp) : n_tiles);
+    const int64_t end = cta_begin + (warp < warps ? plan_first(n_tiles, warps, warp + 1) : n_tiles);
+    if (lane < 2) ends[warp][lane].unit0 = -1;
+    __syncwarp();
+    float* my_parts = a.warp_parts + (int64_t(blockIdx.x) * kWarps + warp) * 2 * kRows * (D + 4);
+    int64_t at = begin, before = 0;
+    int32_t b = at < end ? plan_locate(a, at, &before) : 0;
+    uint32_t slot_in = 0, slot_out = 0, phase = 0;  // this warp's ring: next slot to fill, to read, its phase
+    uint32_t in_flight = 0;
     bool dead = false;
 
     while (at < end) {
@@ -271,19 +328,16 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         const int rt = unit / K, hk = unit % K;
         const int last = int(min(int64_t(sq.tiles), first + (end - at)));
         at += last - first;
-        // ---- this warp's tiles
-        const int n = last - first;
-        const int t0 = first + n * warp / kWarps, t1 = first + n * (warp + 1) / kWarps;
-        const int rows = min(kRowTile, sq.nq * G - rt * kRowTile);
+        const int t0 = first, t1 = last;
+        const int rows = min(kRows, sq.nq * G - rt * kRows);
         // keys that row r sees: the first raw - nq + token + 1; never more than the table holds
-        auto limit_of = [&](int r) { return min(sq.len, sq.raw - sq.nq + (rt * kRowTile + r) / G + 1); };
-        const int limit_a = g < rows ? limit_of(g) : INT32_MAX, limit_b = g + 8 < rows ? limit_of(g + 8) : INT32_MAX;
+        auto limit_of = [&](int r) { return min(sq.len, sq.raw - sq.nq + (rt * kRows + r) / G + 1); };
         const int least = limit_of(0);  // the smallest limit of the rows
 
         // ---- pages: lane i holds page `p0 + i` of the warp's run
-        const int bt = a.bt, pages = (sq.len + bt - 1) / bt;
+        const int pages = (min(sq.len, t1 * kTile) + a.bt - 1) >> a.bt_log2;
         const int32_t* table = a.tables + int64_t(b) * a.stride;
-        int p0 = -1, page_id = 0;
+        int p0 = -32, page_row = 0;
         float page_ks = 0.0f, page_lv = 0.0f;  // ks < 0: not to be seen
         auto load_pages = [&](int from) {
             p0 = from;
@@ -294,106 +348,92 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 atomicOr(a.p.status, kDevBounds);
                 id = 0;
             }
-            page_id = id;
+            page_row = (id * K + hk) << a.bt_log2;  // of the tensor maps
             page_ks = j < pages && !bad ? a.k_scales[int64_t(id) * K + hk] : -1.0f;
             page_lv = j < pages && !bad ? log2f(a.v_scales[int64_t(id) * K + hk]) : 0.0f;
         };
         auto issue = [&](int tile) {
-            const int tok = tile * kTile, pg = tok / bt;
-            if (p0 < 0 || pg >= p0 + 32 || (bt < kTile && pg + 1 >= p0 + 32)) load_pages(pg);
-            const int id0 = __shfl_sync(~0u, page_id, pg - p0), id1 = __shfl_sync(~0u, page_id, (pg - p0 + 1) & 31);
-            float4 mt;
-            mt.x = __shfl_sync(~0u, page_ks, pg - p0);
-            mt.z = __shfl_sync(~0u, page_lv, pg - p0);
-            mt.y = __shfl_sync(~0u, page_ks, (pg - p0 + 1) & 31);
-            mt.w = __shfl_sync(~0u, page_lv, (pg - p0 + 1) & 31);
-            const int slot = int(issued % S);
+            const int tok = tile * kTile, pg = tok >> a.bt_log2;
+            if (pg >= p0 + 32) load_pages(pg);
+            const int row = __shfl_sync(~0u, page_row, pg - p0) + (tok & (a.bt - 1));
+            const float ks = __shfl_sync(~0u, page_ks, pg - p0), lv = __shfl_sync(~0u, page_lv, pg - p0);
             if (lane == 0) {
-                if (bt >= kTile) {
-                    mt.y = mt.x;
-                    mt.w = mt.z;
-                }
-                meta[slot] = mt;
-                const uint32_t bar = bar0 + 8u * slot, dst = ptx::smem_u32(ring + slot * 2 * C::kTileBytes);
+                meta[slot_in] = make_float2(ks, lv);
+                const uint32_t bar = bar0 + 8u * slot_in, dst = ptx::smem_u32(ring + slot_in * 2 * C::kTileBytes);
                 ptx::mbar_arrive_expect_tx(bar, 2 * C::kTileBytes);
-                const int32_t r0 = (id0 * K + hk) * bt + tok % bt;
-                ptx::tma_load_2d(dst, &tm_k, bar, 0, r0);
-                ptx::tma_load_2d(dst + C::kTileBytes, &tm_v, bar, 0, r0);
-                if (bt < kTile) {
-                    const int32_t r1 = (id1 * K + hk) * bt;
-                    ptx::tma_load_2d(dst + C::kTileBytes / 2, &tm_k, bar, 0, r1);
-                    ptx::tma_load_2d(dst + C::kTileBytes + C::kTileBytes / 2, &tm_v, bar, 0, r1);
-                }
+                ptx::tma_load_2d(dst, &tm_k, bar, 0, row);
+                ptx::tma_load_2d(dst + C::kTileBytes, &tm_v, bar, 0, row);
             }
-            ++issued;
+            slot_in = slot_in + 1 == S ? 0 : slot_in + 1;
+            ++in_flight;
         };
         int next = t0;
         for (; next < t1 && next < t0 + S; ++next) issue(next);
 
-        // ---- Q as the A operand of every k-step: thread (g, t) holds 16-element pieces t, t + 4 of rows g, g + 8
-        uint32_t qa[kSteps][4];
-        float rf_a, rf_b;  // scores of the two rows: factor of the products
-        {
-            uint32_t raw[2][D / 8];  // [row][pairs]
-            float top[2] = {0.0f, 0.0f};
+        // ---- Q^T as the B operand of every k-step: thread (g, t) holds the 16-element pieces t, t + 4 of row g
+        uint32_t qb[NT][kSteps][2];
+        float rf[NT][2];    // factor of the products of rows 2t, 2t + 1
+        int limit[NT][2];   // keys that they see
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = rt * kRowTile + g + 8 * r;
-                const bool have = g + 8 * r < rows;
-                const __nv_bfloat16* src =
-                    a.q.p + int64_t(sq.q0 + (have ? row / G : 0)) * a.q.ts + (hk * G + (have ? row % G : 0)) * a.q.hs;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                        if (have) u = __ldg(reinterpret_cast<const uint4*>(src + (t + 4 * c) * 16 + hh * 8));
-                        raw[r][c * 8 + hh * 4 + 0] = u.x;
-                        raw[r][c * 8 + hh * 4 + 1] = u.y;
-                        raw[r][c * 8 + hh * 4 + 2] = u.z;
-                        raw[r][c * 8 + hh * 4 + 3] = u.w;
-                    }
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) top[r] = fmaxf(top[r], fmaxf(fabsf(bf_lo(raw[r][i])), fabsf(bf_hi(raw[r][i]))));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-            }
-            float sc[2], rf[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                // 2^e with |q| 2^e < 512: fp16 keeps elements down to 2^-33 of the largest
-                const int e = min(max(8 - (int(__float_as_uint(top[r]) >> 23) - 126), -119), 126);
-                sc[r] = __uint_as_float(uint32_t(e + 127) << 23);
-                rf[r] = a.p.scale * kLog2e * __uint_as_float(uint32_t(127 - e) << 23);
-            }
-            rf_a = rf[0];
-            rf_b = rf[1];
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g, row = rt * kRows + r;
+            const bool have = r < rows;
+            const __nv_bfloat16* src =
+                a.q.p + int64_t(sq.q0 + (have ? row / G : 0)) * a.q.ts + (hk * G + (have ? row % G : 0)) * a.q.hs;
+            uint32_t raw[D / 8];
+            float top = 0.0f;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                    if (have) u = __ldg(reinterpret_cast<const uint4*>(src + (t + 4 * c) * 16 + hh * 8));
+                    raw[c * 8 + hh * 4 + 0] = u.x;
+                    raw[c * 8 + hh * 4 + 1] = u.y;
+                    raw[c * 8 + hh * 4 + 2] = u.z;
+                    raw[c * 8 + hh * 4 + 3] = u.w;
+                }
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t u0 = raw[r][c * 8 + 2 * s], u1 = raw[r][c * 8 + 2 * s + 1];
-                        qa[c * 4 + s][r] = half2_of(bf_lo(u0) * sc[r], bf_hi(u0) * sc[r]);
-                        qa[c * 4 + s][2 + r] = half2_of(bf_lo(u1) * sc[r], bf_hi(u1) * sc[r]);
-                    }
+            for (int i = 0; i < D / 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf_lo(raw[i])), fabsf(bf_hi(raw[i]))));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            // 2^e with |q| 2^e < 512: fp16 keeps elements down to 2^-33 of the largest
+            const int e = min(max(8 - (int(__float_as_uint(top) >> 23) - 126), -119), 126);
+            const float sc = __uint_as_float(uint32_t(e + 127) << 23);
+            const float f = a.p.scale * kLog2e * __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                qb[nt][i][0] = half2_of(bf_lo(raw[2 * i]) * sc, bf_hi(raw[2 * i]) * sc);
+                qb[nt][i][1] = half2_of(bf_lo(raw[2 * i + 1]) * sc, bf_hi(raw[2 * i + 1]) * sc);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                rf[nt][i] = __shfl_sync(~0u, f, (2 * t + i) * 4);
+                limit[nt][i] = nt * 8 + 2 * t + i < rows ? limit_of(nt * 8 + 2 * t + i) : INT32_MAX;
+            }
         }
 
-        float o[kCols][4];
+        float o[NT][kSteps][4];
+        float m[NT][2], mw[NT][2], l[NT][2], f[NT][2];  // of rows 2t, 2t + 1; f = 2^(m + lv - mw)
+        float lv_now = 0.0f;                            // the lv that f holds for
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-        float m_a = -INFINITY, m_b = -INFINITY, w_a = -INFINITY, w_b = -INFINITY, l_a = 0.0f, l_b = 0.0f;
+            for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[nt][i] = mw[nt][i] = kNone;
+                l[nt][i] = 0.0f;
+                f[nt][i] = 1.0f;
+            }
+        }
 
         for (int tile = t0; tile < t1; ++tile) {
-            const int slot = int(taken % S);
-            const uint32_t bar = bar0 + 8u * slot, phase = (taken / S) & 1u;
+            const uint32_t bar = bar0 + 8u * slot_out;
             if (!__all_sync(~0u, ptx::mbar_try_wait(bar, phase))) {
                 const uint64_t from = ptx::globaltimer_ns();
-                while (!ptx::mbar_try_wait(bar, phase))
-                    if (ptx::globaltimer_ns() - from > a.timeout_ns) {
+                for (int tries = 0; !ptx::mbar_try_wait(bar, phase); ++tries)
+                    if (tries % 64 == 63 && ptx::globaltimer_ns() - from > a.timeout_ns) {
                         dead = true;  // give up waiting; the results are lost and reported
                         if (lane == 0) atomicOr(a.p.status, kDevTimeout);
                         break;
@@ -403,240 +443,250 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     break;
                 }
             }
-            const float4 mt = meta[slot];
-            const uint8_t* kt = ring + slot * 2 * C::kTileBytes;
+            const float2 mt = meta[slot_out];
+            const uint8_t* kt = ring + slot_out * 2 * C::kTileBytes;
             const uint8_t* vt = kt + C::kTileBytes;
-            // ---- S = Q K^T: four 8-token tiles
-            float s[4][4];
+            // ---- S^T = K Q^T (two sums over the k-steps, for a shorter chain)
+            float s[NT][2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-                const int row = i * 8 + g;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const int chunk = t + 4 * c;
-                    const int off = D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-                    const uint4 u = *reinterpret_cast<const uint4*>(kt + off);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                for (int i = 0; i < 2; ++i) s[nt][i][0] = s[nt][i][1] = s[nt][i][2] = s[nt][i][3] = 0.0f;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mma16816(s[i], qa[c * 4 + q], ops::e4m3_half2(uint16_t(w[q])), ops::e4m3_half2(uint16_t(w[q] >> 16)));
+            for (int c = 0; c < D / 64; ++c) {
+                uint4 u[2];  // tokens g, g + 8 (rows of the swizzle differ by 8: the same chunk)
+                const int chunk = t + 4 * c;
+                const int off = D == 128 ? g * 128 + ((chunk ^ g) << 4) : g * 64 + ((chunk ^ ((g >> 1) & 3)) << 4);
+                u[0] = *reinterpret_cast<const uint4*>(kt + off);
+                u[1] = *reinterpret_cast<const uint4*>(kt + off + 8 * D);
+                const uint32_t w0[4] = {u[0].x, u[0].y, u[0].z, u[0].w}, w1[4] = {u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t ka[4] = {ops::e4m3_half2(uint16_t(w0[q])), ops::e4m3_half2(uint16_t(w1[q])),
+                                            ops::e4m3_half2(uint16_t(w0[q] >> 16)), ops::e4m3_half2(uint16_t(w1[q] >> 16))};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(s[nt][q & 1], ka, qb[nt][c * 4 + q][0], qb[nt][c * 4 + q][1]);
                 }
             }
-            // ---- scores in units of log2; masks
+            // ---- scores in units of log2 (tokens g, g + 8; rows 2t, 2t + 1); masks
             const int tok = tile * kTile;
-            const bool masked = tok + kTile > least || mt.x < 0.0f || mt.y < 0.0f;
+            const bool masked = tok + kTile > least || mt.x < 0.0f;
+            bool rise = false;
+            float x[NT][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ks = i < 2 ? mt.x : mt.y;
-                s[i][0] *= rf_a * ks;
-                s[i][1] *= rf_a * ks;
-                s[i][2] *= rf_b * ks;
-                s[i][3] *= rf_b * ks;
-                if (masked) {
-                    const int j = tok + i * 8 + 2 * t;
-                    const bool out = ks < 0.0f;
-                    if (out || j >= limit_a) s[i][0] = -INFINITY;
-                    if (out || j + 1 >= limit_a) s[i][1] = -INFINITY;
-                    if (out || j >= limit_b) s[i][2] = -INFINITY;
-                    if (out || j + 1 >= limit_b) s[i][3] = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[nt][0][i] = (s[nt][0][i] + s[nt][1][i]) * (rf[nt][i & 1] * mt.x);
+                if (masked)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (mt.x < 0.0f || tok + g + (i >> 1) * 8 >= limit[nt][i & 1]) s[nt][0][i] = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    x[nt][i] = fmaxf(s[nt][0][i], s[nt][0][i + 2]);
+                    rise |= x[nt][i] > m[nt][i] + kRise || x[nt][i] + mt.y > mw[nt][i] + kRise;
                 }
             }
-            float xa0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-            float xa1 = fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1]));
-            float xb0 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-            float xb1 = fmaxf(fmaxf(s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3]));
+            if (__any_sync(~0u, rise)) {
+                // raise the maxima to this tile's, and rescale
 #pragma unroll
-            for (int i = 1; i <= 2; i <<= 1) {
-                xa0 = fmaxf(xa0, __shfl_xor_sync(~0u, xa0, i));
-                xa1 = fmaxf(xa1, __shfl_xor_sync(~0u, xa1, i));
-                xb0 = fmaxf(xb0, __shfl_xor_sync(~0u, xb0, i));
-                xb1 = fmaxf(xb1, __shfl_xor_sync(~0u, xb1, i));
-            }
-            const float mn_a = fmaxf(m_a, fmaxf(xa0, xa1)), mn_b = fmaxf(m_b, fmaxf(xb0, xb1));
-            const float wn_a = fmaxf(w_a, fmaxf(xa0 + mt.z, xa1 + mt.w)), wn_b = fmaxf(w_b, fmaxf(xb0 + mt.z, xb1 + mt.w));
-            const float mu_a = mn_a == -INFINITY ? 0.0f : mn_a, mu_b = mn_b == -INFINITY ? 0.0f : mn_b;
-            const float wu_a = wn_a == -INFINITY ? 0.0f : wn_a, wu_b = wn_b == -INFINITY ? 0.0f : wn_b;
-            if (__any_sync(~0u, mn_a != m_a || mn_b != m_b || wn_a != w_a || wn_b != w_b)) {
-                l_a *= ptx::ex2(m_a - mu_a);
-                l_b *= ptx::ex2(m_b - mu_b);
-                const float ca = ptx::ex2(w_a - wu_a), cb = ptx::ex2(w_b - wu_b);
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    o[j][0] *= ca;
-                    o[j][1] *= ca;
-                    o[j][2] *= cb;
-                    o[j][3] *= cb;
-                }
-                m_a = mn_a;
-                m_b = mn_b;
-                w_a = wn_a;
-                w_b = wn_b;
-            }
-            // W = P 2^(m + lv - mw); where that factor is past fp32, P is 0
-            const float fa[2] = {ptx::ex2(fminf(mu_a + mt.z - wu_a, 126.0f)), ptx::ex2(fminf(mu_a + mt.w - wu_a, 126.0f))};
-            const float fb[2] = {ptx::ex2(fminf(mu_b + mt.z - wu_b, 126.0f)), ptx::ex2(fminf(mu_b + mt.w - wu_b, 126.0f))};
-            uint32_t pa[2][4];
+                    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p0_ = ptx::ex2(s[i][0] - mu_a), p1_ = ptx::ex2(s[i][1] - mu_a);
-                const float p2_ = ptx::ex2(s[i][2] - mu_b), p3_ = ptx::ex2(s[i][3] - mu_b);
-                l_a += p0_ + p1_;
-                l_b += p2_ + p3_;
-                pa[i / 2][(i & 1) * 2] = half2_of(p0_ * fa[i / 2], p1_ * fa[i / 2]);
-                pa[i / 2][(i & 1) * 2 + 1] = half2_of(p2_ * fb[i / 2], p3_ * fb[i / 2]);
-            }
-            // ---- O += W V: two 16-token steps; thread (g, t) takes tokens 2t, 2t + 1, 2t + 8, 2t + 9
-            // and D / 8 columns from g * D / 8 on
+                        for (int k = 4; k <= 16; k <<= 1) x[nt][i] = fmaxf(x[nt][i], __shfl_xor_sync(~0u, x[nt][i], k));
+                        const float mn = fmaxf(m[nt][i], x[nt][i]), wn = fmaxf(mw[nt][i], x[nt][i] + mt.y);
+                        const float cf = ptx::ex2(mw[nt][i] - wn);
+                        l[nt][i] *= ptx::ex2(m[nt][i] - mn);
+                        m[nt][i] = mn;
+                        mw[nt][i] = wn;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t v[4][D / 32];  // [token][words]
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = q * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
-                    if (D == 128) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(vt + row * 128 + ((g ^ (row & 7)) << 4));
-                        v[i][0] = u.x;
-                        v[i][1] = u.y;
-                        v[i][D / 32 - 2] = u.z;
-                        v[i][D / 32 - 1] = u.w;
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(vt + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) +
-                                                                        (g & 1) * 8);
-                        v[i][0] = u.x;
-                        v[i][1] = u.y;
+                        for (int j = 0; j < kSteps; ++j) {
+                            o[nt][j][i] *= cf;
+                            o[nt][j][i + 2] *= cf;
+                        }
                     }
-                    // what lies behind the last token (or in a block not to be seen) may be anything: 0 x NaN
-                    if (masked && (tok + row >= sq.len || (q == 0 ? mt.x : mt.y) < 0.0f))
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j) v[i][j] = 0u;
-                }
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5140), a1 = __byte_perm(v[0][j], v[1][j], 0x7362);
-                    const uint32_t c0 = __byte_perm(v[2][j], v[3][j], 0x5140), c1 = __byte_perm(v[2][j], v[3][j], 0x7362);
-                    mma16816(o[4 * j + 0], pa[q], ops::e4m3_half2(uint16_t(a0)), ops::e4m3_half2(uint16_t(c0)));
-                    mma16816(o[4 * j + 1], pa[q], ops::e4m3_half2(uint16_t(a0 >> 16)), ops::e4m3_half2(uint16_t(c0 >> 16)));
-                    mma16816(o[4 * j + 2], pa[q], ops::e4m3_half2(uint16_t(a1)), ops::e4m3_half2(uint16_t(c1)));
-                    mma16816(o[4 * j + 3], pa[q], ops::e4m3_half2(uint16_t(a1 >> 16)), ops::e4m3_half2(uint16_t(c1 >> 16)));
-                }
+                lv_now = INFINITY;  // f is stale
             }
-            ++taken;
+            if (mt.y != lv_now) {
+                lv_now = mt.y;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)  // where the factor is past fp32, P is 0
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) f[nt][i] = ptx::ex2(fminf(m[nt][i] + mt.y - mw[nt][i], 126.0f));
+            }
+            uint32_t wb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = ptx::ex2(s[nt][0][i] - m[nt][i & 1]);
+                l[nt][0] += p[0] + p[2];
+                l[nt][1] += p[1] + p[3];
+                wb[nt][0] = transpose8x8(half2_of(p[0] * f[nt][0], p[1] * f[nt][1]));
+                wb[nt][1] = transpose8x8(half2_of(p[2] * f[nt][0], p[3] * f[nt][1]));
+            }
+            // ---- O^T += V^T W^T; thread (g, t) takes tokens 2t, 2t + 1, 2t + 8, 2t + 9 and the D / 8 columns
+            // from g * D / 8 on
+            uint32_t v[4][D / 32];  // [token][words]
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 2 * t + (i & 1) + (i >> 1) * 8;
+                if (D == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(vt + row * 128 + ((g ^ (row & 7)) << 4));
+                    v[i][0] = u.x;
+                    v[i][1] = u.y;
+                    v[i][D / 32 - 2] = u.z;
+                    v[i][D / 32 - 1] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(vt + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) +
+                                                                    (g & 1) * 8);
+                    v[i][0] = u.x;
+                    v[i][1] = u.y;
+                }
+                // what lies behind the last token (or in a block not to be seen) may be anything: 0 x NaN
+                if (masked && (tok + row >= sq.len || mt.x < 0.0f))
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) v[i][j] = 0u;
+            }
             __syncwarp();  // every lane has read the slot
+            slot_out = slot_out + 1 == S ? 0 : slot_out + 1;
+            phase ^= slot_out == 0 ? 1u : 0u;
+            --in_flight;
             if (next < t1) issue(next++);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
+                    const uint32_t lo = __byte_perm(v[0][j], v[1][j], sel), hi = __byte_perm(v[2][j], v[3][j], sel);
+                    const uint32_t va[4] = {ops::e4m3_half2(uint16_t(lo)), ops::e4m3_half2(uint16_t(lo >> 16)),
+                                            ops::e4m3_half2(uint16_t(hi)), ops::e4m3_half2(uint16_t(hi >> 16))};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][2 * j + h], va, wb[nt][0], wb[nt][1]);
+                }
         }
-        l_a += __shfl_xor_sync(~0u, l_a, 1);
-        l_a += __shfl_xor_sync(~0u, l_a, 2);
-        l_b += __shfl_xor_sync(~0u, l_b, 1);
-        l_b += __shfl_xor_sync(~0u, l_b, 2);
 
-        // ---- join the warps: O over the rings (every copy has been taken), columns of row r at 32 t ..
-        __syncthreads();
-        {
-            float* dst = part_o + (warp * kRowTile + g) * (D + 4);
+        if (dead) break;
+        // ---- the unit's rows (thread (g, t): D / 8 columns from g * D / 8 on, of rows 2t, 2t + 1)
+        const bool whole = first == 0 && last == sq.tiles;
+        const int64_t unit0 = at - last;  // the unit's first tile
+        const int which = first > 0 ? 0 : 1;  // began in an earlier run (then this is the run's first), or here
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                // column tile j: n = 2t, 2t + 1 are columns 2t * D/8 + j and (2t + 1) * D/8 + j
-                dst[2 * t * (D / 8) + j] = o[j][0];
-                dst[(2 * t + 1) * (D / 8) + j] = o[j][1];
-                dst[8 * (D + 4) + 2 * t * (D / 8) + j] = o[j][2];
-                dst[8 * (D + 4) + (2 * t + 1) * (D / 8) + j] = o[j][3];
-            }
-            if (t == 0) {
-                float* st = stat + warp * kRowTile + g;
-                st[0] = m_a;
-                st[8] = m_b;
-                st[kWarps * kRowTile] = l_a;
-                st[kWarps * kRowTile + 8] = l_b;
-                st[2 * kWarps * kRowTile] = w_a;
-                st[2 * kWarps * kRowTile + 8] = w_b;
-            }
-        }
-        __syncthreads();
-        {
-            constexpr int E = D / 16;
-            const int row = threadIdx.x / 16, col = (threadIdx.x % 16) * E;
-            float m = -INFINITY, mw = -INFINITY, l = 0.0f, x[E];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = 0.0f;
-            for (int w = 0; w < kWarps; ++w) {
-                m = fmaxf(m, stat[w * kRowTile + row]);
-                mw = fmaxf(mw, stat[(2 * kWarps + w) * kRowTile + row]);
-            }
-            const float mu = m == -INFINITY ? 0.0f : m, wu = mw == -INFINITY ? 0.0f : mw;
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ptx::ex2(stat[(2 * kWarps + w) * kRowTile + row] - wu);
-                l += stat[(kWarps + w) * kRowTile + row] * ptx::ex2(stat[w * kRowTile + row] - mu);
-                const float* src = part_o + (w * kRowTile + row) * (D + 4) + col;
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) x[i] += src[i] * f;
-            }
-            if (first == 0 && last == sq.tiles) {
-                const int r = rt * kRowTile + row;
-                if (row < rows) store_row<D>(a, sq.q0 + r / G, hk * G + r % G, col, x, mu, l, wu);
-            } else {
-                // a part of the unit: a run that began in an earlier CTA is this CTA's first
-                const int64_t slot = 2 * int64_t(blockIdx.x) + (first > 0 ? 0 : 1);
-                float* dst = a.parts + (slot * kRowTile + row) * (D + 4);
+                for (int k = 4; k <= 16; k <<= 1) l[nt][i] += __shfl_xor_sync(~0u, l[nt][i], k);
+                const int r = nt * 8 + 2 * t + i;
+                if (r >= rows) continue;
+                float y[D / 8];
 #pragma unroll
-                for (int i = 0; i < E; ++i) dst[col + i] = x[i];
-                if (col == 0) {
-                    dst[D] = m;
-                    dst[D + 1] = l;
-                    dst[D + 2] = mw;
+                for (int j = 0; j < kSteps; ++j) {
+                    y[2 * j] = o[nt][j][i];
+                    y[2 * j + 1] = o[nt][j][i + 2];
+                }
+                if (whole) {
+                    const int row = rt * kRows + r;
+                    store_row<D / 8>(a, sq.q0 + row / G, hk * G + row % G, g * (D / 8), y, m[nt][i], l[nt][i], mw[nt][i]);
+                } else {
+                    float* dst = my_parts + (which * kRows + r) * (D + 4);
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j)
+                        *reinterpret_cast<float4*>(dst + g * (D / 8) + 4 * j) =
+                            make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                    if (g == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(m[nt][i], l[nt][i], mw[nt][i], 0.0f);
                 }
             }
-        }
-        ptx::fence_proxy_async_smem();  // the rings are written by copies again
-        __syncthreads();
-        if (__syncthreads_or(dead)) break;
+        if (lane == 0 && !whole) ends[warp][which] = Unit{unit0, unit0 + sq.tiles, sq.q0, rows, rt * kRows, hk * G};
     }
     // After a wait that ran out: the copies still in flight land before the CTA leaves (bounded).
     if (dead)
-        for (; taken < issued; ++taken) drain_bar(bar0 + 8u * (taken % S), (taken / S) & 1u, a.timeout_ns);
+        for (; in_flight > 0; --in_flight) {
+            drain_bar(bar0 + 8u * slot_out, phase, a.timeout_ns);
+            slot_out = slot_out + 1 == S ? 0 : slot_out + 1;
+            phase ^= slot_out == 0 ? 1u : 0u;
+        }
+    // ---- the CTA's joins: of the unit that its run begins inside of, then of each unit that
+    // begins inside of a warp's run and does not end there
+    if (__syncthreads_or(dead)) return;
+    // (one warp for each row of each such unit)
+    const float* parts0 = a.warp_parts + int64_t(blockIdx.x) * kWarps * 2 * kRows * (D + 4);
+    int turn = 0;
+    for (int w = -1; w < warps; ++w) {
+        const bool early = w < 0;  // the unit began in an earlier CTA's run
+        const Unit u = early ? ends[0][0] : ends[w][1];
+        if (u.unit0 < 0) continue;
+        const int w0 = early ? 0 : w;
+        int w1 = w0 + 1;
+        while (w1 < warps && ends[w1][0].unit0 == u.unit0) ++w1;
+        const bool done = !early && u.unit1 <= cta_end;
+        for (int r = 0; r < u.rows; ++r, ++turn) {
+            if (turn % kWarps != warp) continue;
+            float x[D / 32], jm, jl, jw;
+            join_row<D>(0, w1 - w0, 1, [&](int64_t c) {
+                return parts0 + (((w0 + c) * 2 + (c == 0 && !early ? 1 : 0)) * kRows + r) * (D + 4);
+            }, x, jm, jl, jw);
+            if (done) {
+                const int row = u.row0 + r;
+                store_row<D / 32>(a, u.q0 + row / G, u.head + row % G, lane * (D / 32), x, jm, jl, jw);
+            } else {
+                float* dst = a.cta_parts + ((int64_t(blockIdx.x) * 2 + (early ? 0 : 1)) * kRows + r) * (D + 4);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) dst[lane * (D / 32) + e] = x[e];
+                if (lane == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(jm, jl, jw, 0.0f);
+            }
+        }
+    }
+    if (threadIdx.x == 0) a.begins[blockIdx.x] = ends[0][0];
 }
 
-// Joins the parts of the units that lie in several CTAs' runs: CTA i takes the unit that
-// its run begins inside of, if that is the unit's first such run.
+// Joins the parts of the units that lie in several CTAs' runs: one CTA here for each run that
+// begins inside of a unit, if it is the first such run of its unit.  The parts: what the run
+// before has of its last unit, then what this and the following runs have of their first.
+constexpr int kJoinWarps = 32;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_join_kernel(const CacheArgs a, int grid) {
-    __shared__ PlanShared plan;
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheArgs a) {
+    constexpr int E = D / 32;
+    __shared__ alignas(16) float sh[kJoinWarps * (D + 4)];
     ops::grid_wait();
-    const int64_t total = plan_total(a, plan, false), ctas = plan_ctas(total, grid);
+    const int64_t total = a.head[0], ctas = a.head[1];
     const int64_t i = int64_t(blockIdx.x) + 1;
     if (i >= ctas) return;
-    const int64_t at = plan_first(total, ctas, i);
-    plan_locate(a, plan, at);
-    bool cut = false;
-    const Sequence sq = sequence(a, plan.seq, &cut);
-    const int unit = int((at - plan.before) / sq.tiles);
-    const int64_t unit0 = plan.before + int64_t(unit) * sq.tiles, unit1 = unit0 + sq.tiles;
-    if (at == unit0 || plan_first(total, ctas, i - 1) > unit0) return;
-    constexpr int E = D / 16;
-    const int row = threadIdx.x / 16, col = (threadIdx.x % 16) * E;
-    const int K = a.p.kv_heads, G = a.p.group, rt = unit / K, hk = unit % K, r = rt * kRowTile + row;
-    if (r >= sq.nq * G) return;
-    const float* first = a.parts + ((2 * (i - 1) + 1) * kRowTile + row) * (D + 4);
-    float m = first[D], mw = first[D + 2];
-    int64_t parts = 0;
-    for (int64_t c = i; c < ctas && plan_first(total, ctas, c) < unit1; ++c, ++parts) {
-        const float* p = a.parts + (2 * c * kRowTile + row) * (D + 4);
-        m = fmaxf(m, p[D]);
-        mw = fmaxf(mw, p[D + 2]);
+    const Unit u = a.begins[i];
+    if (u.unit0 < 0 || plan_first(total, ctas, i - 1) > u.unit0) return;
+    int64_t lo = i + 1, hi = ctas;  // the first CTA from i + 1 on whose run begins behind the unit
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (plan_first(total, ctas, mid) < u.unit1)
+            lo = mid + 1;
+        else
+            hi = mid;
     }
-    const float mu = m == -INFINITY ? 0.0f : m, wu = mw == -INFINITY ? 0.0f : mw;
-    float l = first[D + 1] * ptx::ex2(first[D] - mu), x[E];
-    float f = ptx::ex2(first[D + 2] - wu);
+    // a row for each warp, or (few rows) for each `share` warps, every one a share of the parts
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t n = lo - i + 1;
+    int share = 1;
+    while (2 * share * u.rows <= kJoinWarps && 4 * share <= n) share *= 2;
+    const int r = warp / share, s = warp % share;  // (units have at most 32 rows)
+    float x[E], m, l, mw;
+    if (r < u.rows) {
+        join_row<D>(s, n, share, [&](int64_t c) {
+            return a.cta_parts + ((c == 0 ? 2 * (i - 1) + 1 : 2 * (i + c - 1)) * a.row_tile + r) * (D + 4);
+        }, x, m, l, mw);
+        if (share > 1) {
+            float* mine = sh + warp * (D + 4);
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = first[col + e] * f;
-    for (int64_t c = i; c < i + parts; ++c) {
-        const float* p = a.parts + (2 * c * kRowTile + row) * (D + 4);
-        l += p[D + 1] * ptx::ex2(p[D] - mu);
-        f = ptx::ex2(p[D + 2] - wu);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] += p[col + e] * f;
+            for (int e = 0; e < E; ++e) mine[lane * E + e] = x[e];
+            if (lane == 0) *reinterpret_cast<float4*>(mine + D) = make_float4(m, l, mw, 0.0f);
+        }
     }
-    store_row<D>(a, sq.q0 + r / G, hk * G + r % G, col, x, mu, l, wu);
+    __syncthreads();
+    if (r >= u.rows || s > 0) return;
+    if (share > 1) join_row<D>(0, share, 1, [&](int64_t c) { return sh + (warp + c) * (D + 4); }, x, m, l, mw);
+    const int row = u.row0 + r;
+    store_row<E>(a, u.q0 + row / a.p.group, u.head + row % a.p.group, lane * E, x, m, l, mw);
 }
 
 // Map over the codes as rows of D bytes; a box is `rows` of them, 128- or 64-byte swizzle.
@@ -662,20 +712,34 @@ cudaError_t codes_map(CUtensorMap* m, const void* codes, int64_t n_rows, int d, 
     return c == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+template <int D, int NT>
+cudaError_t launch_attention(const sta_cache& c, CacheArgs a, int sms, cudaStream_t stream) {
+    using C = Cfg<D, NT>;
+    const int64_t n_rows = int64_t(c.blocks) * c.kv_heads * c.block_tokens;
+    CUtensorMap mk, mv;
+    a.row_tile = C::kRows;
+    a.cta_parts = a.warp_parts + int64_t(sms) * 2 * C::kWarps * C::kRows * (D + 4);
+    a.begins = reinterpret_cast<Unit*>(a.cta_parts + int64_t(sms) * 2 * C::kRows * (D + 4));
+    a.head = reinterpret_cast<int64_t*>(a.begins + sms);
+    cudaError_t e = codes_map(&mk, c.k_codes, n_rows, D, kTile);
+    if (e == cudaSuccess) e = codes_map(&mv, c.v_codes, n_rows, D, kTile);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(cache_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess)
+        e = packed::launch(cache_attention_kernel<D, NT>, unsigned(sms), C::kThreads, C::kSmem, stream, false, mk, mv, a);
+    if (e == cudaSuccess && sms > 1)
+        e = packed::launch(cache_join_kernel<D>, unsigned(sms - 1), kJoinWarps * 32, 0, stream, true, a);
+    return e;
+}
+
+// Query rows of a unit, from the mean number of rows that a sequence has (its own are known
+// on the device only): units of more rows widen the codes once for all of them.
 template <int D>
 cudaError_t launch_attention(const sta_cache& c, const CacheArgs& a, int sms, cudaStream_t stream) {
-    const int64_t n_rows = int64_t(c.blocks) * c.kv_heads * c.block_tokens;
-    const int box = c.block_tokens < kTile ? c.block_tokens : kTile;
-    CUtensorMap mk, mv;
-    cudaError_t e = codes_map(&mk, c.k_codes, n_rows, D, box);
-    if (e == cudaSuccess) e = codes_map(&mv, c.v_codes, n_rows, D, box);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(cache_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
-    if (e == cudaSuccess)
-        e = packed::launch(cache_attention_kernel<D>, unsigned(sms), kThreads, Cfg<D>::kSmem, stream, false, mk, mv, a);
-    if (e == cudaSuccess && sms > 1)
-        e = packed::launch(cache_join_kernel<D>, unsigned(sms - 1), kThreads, 0, stream, true, a, sms);
-    return e;
+    const int64_t rows = int64_t(a.p.tokens_q) * a.p.group / a.p.batch;
+    if (rows <= 8) return launch_attention<D, 1>(c, a, sms, stream);
+    if (rows <= 16 || D == 128) return launch_attention<D, 2>(c, a, sms, stream);
+    return launch_attention<D, D == 64 ? 4 : 2>(c, a, sms, stream);
 }
 
 // Checks of the cache and the problem together.
@@ -711,7 +775,9 @@ sta_status sta_cache_workspace(const sta_cache* c, const sta_packed* p, int64_t*
         (void)cudaGetLastError();
         sms = kMaxSms;  // no device here: as for the largest
     }
-    *bytes = int64_t(2) * sms * kRowTile * (c->head_dim + 4) * 4;
+    // parts of an SM: its warps' (16 of 8 rows, 8 of 16; d = 64 also 16 of 16, 8 of 32) and its own
+    const int64_t rows = (c->head_dim == 128 ? 128 + 16 : 256 + 32) * 2;
+    *bytes = sms * (rows * (c->head_dim + 4) * 4 + int64_t(sizeof(Unit))) + 16;
     return STA_OK;
 }
 
@@ -735,9 +801,10 @@ sta_status sta_cache_attention(const sta_cache* c, const sta_packed* p, const in
     if (cudaError_t e = op_status_word(&a.p.status); e != cudaSuccess) return op_cuda_status(e);
     a.blocks = c->blocks;
     a.bt = c->block_tokens;
+    a.bt_log2 = a.bt == 16 ? 4 : a.bt == 32 ? 5 : a.bt == 64 ? 6 : 7;
     a.k_scales = c->k_scales;
     a.v_scales = c->v_scales;
-    a.parts = static_cast<float*>(workspace);
+    a.warp_parts = static_cast<float*>(workspace);
     a.timeout_ns = kOpTimeoutNs;
     a.lengths = lengths;
     a.tables = block_tables;
