@@ -57,9 +57,12 @@ cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* 
     constexpr int kPer = D / 8;                          // threads for one token
     constexpr int kStep = kAppendThreads / kPer;         // tokens in one pass
     constexpr int kPasses = BT / kStep > 0 ? BT / kStep : 1;
+    constexpr int kMaxRange = kAppendThreads;
+    __shared__ uint32_t sh_first[kAppendThreads / 32];  // tokens of the range that begin a run
     __shared__ int sh_n;
     __shared__ int sh_off[BT + 1];
     __shared__ float sh_max[kAppendThreads / 32];
+    __shared__ int64_t sh_slot[kMaxRange + BT + 2];  // of tokens t0 - 1, t0, ...
     const int tid = threadIdx.x, h = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
     const Rows x = is_v ? v : k;
@@ -67,20 +70,29 @@ cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* 
     float* scales = is_v ? c.v_scales : c.k_scales;
     const int64_t n_slots = int64_t(c.blocks) * BT;
     const int64_t t0 = int64_t(blockIdx.x) * range, t1 = min(t0 + range, tokens);
-    for (int64_t t = t0; t < t1; ++t) {
-        const int64_t s = slots[t];
-        if (s >= n_slots && tid == 0) atomicOr(status, kDevBounds);
-        if (s < 0 || s >= n_slots) continue;
-        const int64_t blk = s / BT;
-        if (t > 0) {
-            const int64_t before = slots[t - 1];
-            if (before >= 0 && before / BT == blk) continue;  // inside a run that began earlier
-        }
+    for (int i = tid; i < range + BT + 2; i += kAppendThreads) {
+        const int64_t t = t0 - 1 + i;
+        sh_slot[i] = t >= 0 && t < tokens ? slots[t] : -1;
+    }
+    __syncthreads();
+    {
+        const int64_t s = tid < t1 - t0 ? sh_slot[tid + 1] : -1, before = sh_slot[tid < range ? tid : 0];
+        if (s >= n_slots) atomicOr(status, kDevBounds);
+        const uint32_t starts =
+            __ballot_sync(~0u, s >= 0 && s < n_slots && !(before >= 0 && before / BT == s / BT));
+        if (tid % 32 == 0) sh_first[tid / 32] = starts;
+    }
+    __syncthreads();
+    for (int word = 0; word < kAppendThreads / 32; ++word)
+    for (uint32_t left = sh_first[word]; left != 0u; left &= left - 1) {
+        const int64_t t = t0 + word * 32 + __ffs(left) - 1;
+        const int64_t* mine = sh_slot + (t - t0 + 1);
+        const int64_t blk = mine[0] / BT;
         // ---- the run's length and offsets
         if (tid == 0) sh_n = BT;
         __syncthreads();
         for (int i = tid; i < BT + 1; i += kAppendThreads) {
-            const int64_t si = t + i < tokens ? slots[t + i] : -1;
+            const int64_t si = mine[i];
             const bool in = si >= 0 && si / BT == blk;
             sh_off[i] = in ? int(si % BT) : -1;
             if (!in) atomicMin(&sh_n, i);
@@ -157,9 +169,9 @@ template <int D, int BT>
 cudaError_t launch_append(const sta_cache& c, const Rows& k, const Rows& v, int64_t tokens, const int64_t* slots,
                           uint32_t* status, cudaStream_t stream) {
     // One token for each CTA while that is at most some 16 CTAs to an SM: a serving step's
-    // tokens are all in blocks of their own.  Else 16 tokens, which hold the beginning of
-    // one or two runs of a prompt.
-    const int range = tokens * c.kv_heads * 2 <= 4096 ? 1 : 16;
+    // tokens are all in blocks of their own.  Else a block's worth, which holds the beginning
+    // of one or two runs of a prompt.
+    const int range = tokens * c.kv_heads * 2 <= 4096 ? 1 : BT;  // (at most kMaxRange)
     const int64_t gx = (tokens + range - 1) / range;
     if (gx > INT32_MAX) return cudaErrorInvalidValue;
     cache_append_kernel<D, BT><<<dim3(unsigned(gx), unsigned(c.kv_heads), 2), kAppendThreads, 0, stream>>>(
