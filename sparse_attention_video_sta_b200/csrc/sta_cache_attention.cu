@@ -22,7 +22,6 @@ namespace {
 constexpr int kTile = 16;      // tokens of a tile: in one block, whatever the block size
 constexpr int kPlanWarps = 8;  // warps that sum the sequences
 constexpr int kMinTiles = 4;   // a warp takes no fewer tiles, a CTA no fewer than two warps' worth
-constexpr int kMaxSms = 148;   // of a B200, for workspaces asked for without a device
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3.0e38f;  // running maximum of a row that has seen no key
@@ -726,9 +725,9 @@ cudaError_t launch_attention(const sta_cache& c, CacheArgs a, int sms, cudaStrea
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(cache_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess)
-        e = packed::launch(cache_attention_kernel<D, NT>, unsigned(sms), C::kThreads, C::kSmem, stream, false, mk, mv, a);
+        e = packed::launch(cache_attention_kernel<D, NT>, dim3(unsigned(sms)), C::kThreads, C::kSmem, stream, false, mk, mv, a);
     if (e == cudaSuccess && sms > 1)
-        e = packed::launch(cache_join_kernel<D>, unsigned(sms - 1), kJoinWarps * 32, 0, stream, true, a);
+        e = packed::launch(cache_join_kernel<D>, dim3(unsigned(sms - 1)), kJoinWarps * 32, 0, stream, true, a);
     return e;
 }
 
@@ -770,11 +769,7 @@ sta_status sta_cache_workspace(const sta_cache* c, const sta_packed* p, int64_t*
     PackedProblem pp;
     if (bytes == nullptr) return STA_ERR_INVALID_ARG;
     if (sta_status st = cache_problem(c, p, false, &pp); st != STA_OK) return st;
-    int sms = 0;
-    if (packed::sm_count(&sms) != cudaSuccess) {
-        (void)cudaGetLastError();
-        sms = kMaxSms;  // no device here: as for the largest
-    }
+    const int sms = packed::sm_count_or_b200();
     // parts of an SM: its warps' (16 of 8 rows, 8 of 16; d = 64 also 16 of 16, 8 of 32) and its own
     const int64_t rows = (c->head_dim == 128 ? 128 + 16 : 256 + 32) * 2;
     *bytes = sms * (rows * (c->head_dim + 4) * 4 + int64_t(sizeof(Unit))) + 16;

@@ -21,6 +21,7 @@ namespace sta {
 namespace {
 
 using packed::QBlock;
+using packed::QWork;
 
 constexpr int kMaxDevices = 64;
 __device__ uint32_t g_op_status;  // one word per device: kDevTimeout | kDevBounds
@@ -139,8 +140,10 @@ struct Cfg {
     // o_full, o_empty, drain[2], item_full[Q], item_empty[Q], v_tail[S], v_clean[S]
     static constexpr int kNumBars = 4 * kStages + 4 + kSBufs + 2 * kSBufs + kSBufs + 4 + 2 * kItemQ;
     static constexpr int kXchOff = kBarOff + kNumBars * 8;   // [2 halves][128 rows] fp32 exchange
-    static constexpr int kMiscOff = kXchOff + 2 * 128 * 4;   // tmem base slot, abort flag, item queue
-    static constexpr int kSmemBytes = kMiscOff + 8 + 4 * kItemQ + 1024;
+    static constexpr int kMiscOff = kXchOff + 2 * 128 * 4;   // tmem base slot, abort flag
+    static constexpr int kQueueOff = kMiscOff + 16;          // item queue
+    static constexpr int kSmemBytes = kQueueOff + kItemQ * int(sizeof(QWork)) + 1024;
+    static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     __host__ __device__ static constexpr uint32_t col_s(int buf) { return uint32_t(buf) * 128u; }
     static constexpr uint32_t kColO = kSBufs * 128u;
     static_assert(kSBufs * 128 + D <= int(kTmemCols), "TMEM budget");
@@ -183,14 +186,15 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-    volatile int32_t* item_q = reinterpret_cast<volatile int32_t*>(smem + C::kMiscOff + 8);
+    QWork* item_q = reinterpret_cast<QWork*>(smem + C::kQueueOff);
     auto wait_bar = [&](uint32_t bar, uint32_t parity) {
         return wait_bar_limited(bar, parity, abort_flag, p.status, p.timeout_ns);
     };
-    auto take_item = [&](uint32_t k, int32_t& u) -> bool {
+    // The CTA's k-th item, copied out of the queue; its entry is then free for item k + kItemQ.
+    auto take_item = [&](uint32_t k, QWork& w) -> bool {
         const int q = int(k % kItemQ);
         if (!wait_bar(bar_item_full(q), (k / kItemQ) & 1u)) return false;
-        u = item_q[q];
+        w = item_q[q];
         return true;
     };
 
@@ -237,19 +241,18 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int32_t K = p.kv_heads;
-    auto block_of = [&](int32_t u) { return p.v.qblocks + p.v.order_q[u / K]; };
     // Ring entry of chunk c's K and V in a block of n chunks (the load order:
     // K(0), K(1), K(2), then V(i), K(i + 3) for i = 0, 1, ...).
     auto entry_k = [](uint32_t c) { return c < uint32_t(NB) ? c : 2u * c - uint32_t(NB - 1); };
     auto entry_v = [](uint32_t i, uint32_t n) { return i + uint32_t(NB) <= n ? uint32_t(NB) + 2u * i : n + i; };
-    // Does the block's last chunk reach past the sequence's last key?
-    auto ragged = [](const QBlock& q) { return q.chunks * 128 > q.nkeys; };
+    // Does the walk's last chunk reach past the sequence's last key?
+    auto ragged = [](const QWork& q) { return (q.c0 + q.n) * 128 > q.nkeys; };
 
     if (warp == kLoadWarp) {
         ptx::regs_dec<kRegsProducer>();
         if (lane == 0) {
             // ------------------------------------------------------------ load
-            const int32_t n_items = p.v.lists->n_q * K;
+            const int32_t n_items = p.v.lists->w_q * K;
             uint32_t ring = 0;
             uint32_t q_loads[2] = {0u, 0u};
             bool ok = true;
@@ -264,16 +267,37 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 ++ring;
                 return true;
             };
+            // A CTA's first item is its own number; the others come from the counter.  Where items
+            // are many (8 to a CTA: short ones), the counter's answer for item k + 2 and the walk of
+            // item k + 1 are on their way while item k's copies are issued; where they are few, an
+            // item is only taken when the one before is issued, so that longest-first levels the
+            // CTAs.  (8192 causal tokens, 24 / 8 heads, d = 128, dK / dV: 730 us late, 905 early.)
+            const bool early = n_items >= 8 * int32_t(gridDim.x);
+            auto next = [&] { return int32_t(gridDim.x) + atomicAdd(&p.v.lists->next_q, 1); };
+            auto fetch = [&](int32_t u) {
+                QWork w{};
+                w.n = -1;
+                if (u < n_items) {
+                    w = p.v.qwalks[u / K];
+                    w.hk = u % K;
+                }
+                return w;
+            };
+            int32_t u2 = early ? next() : 0;
+            QWork w1 = fetch(int32_t(blockIdx.x));
             for (uint32_t k = 0; ok; ++k) {
-                int32_t u = atomicAdd(&p.v.lists->next_q, 1);
-                if (u >= n_items) u = -1;
+                if (!early && k > 0) w1 = fetch(next());
+                const QWork q = w1;
                 const int qe = int(k % kItemQ);
                 if (k >= uint32_t(kItemQ) && !wait_bar(bar_item_empty(qe), ((k / kItemQ) - 1) & 1u)) break;
-                item_q[qe] = u;
+                item_q[qe] = q;
                 ptx::mbar_arrive(bar_item_full(qe));
-                if (u < 0) break;
-                const QBlock q = *block_of(u);
-                const int32_t hk = u % K, n = q.chunks;
+                if (q.n < 0) break;
+                if (early) {
+                    w1 = fetch(u2);
+                    if (u2 < n_items) u2 = next();
+                }
+                const int32_t hk = q.hk, n = q.n, row0 = q.key0 + q.c0 * 128;
                 const int qb = int(k & 1u);
                 if (!wait_bar(bar_q_empty(qb), ((k >> 1) & 1u) ^ 1u)) break;
                 ptx::mbar_arrive_expect_tx(bar_q_full(qb), C::kColBlocks * p.q_box_bytes);
@@ -282,11 +306,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     ops::tma_load_3d(base + C::kQOff + qb * C::kQBytes + cb * kBoxBytes, &tm_q, bar_q_full(qb), cb * 64,
                                      hk * p.group, q.tok0);
                 ++q_loads[qb];
-                for (int32_t c = 0; ok && c < n && c < NB; ++c) ok = issue(&tm_k, hk, q.key0 + c * 128);
+                for (int32_t c = 0; ok && c < n && c < NB; ++c) ok = issue(&tm_k, hk, row0 + c * 128);
                 for (int32_t i = 0; ok && i < n; ++i) {
-                    ok = issue(&tm_v, hk, q.key0 + i * 128);
+                    ok = issue(&tm_v, hk, row0 + i * 128);
                     if (ok && i == n - 1 && ragged(q)) ptx::mbar_arrive(bar_v_tail(int((ring - 1) % S)));
-                    if (ok && i + NB < n) ok = issue(&tm_k, hk, q.key0 + (i + NB) * 128);
+                    if (ok && i + NB < n) ok = issue(&tm_k, hk, row0 + (i + NB) * 128);
                 }
             }
             // Drain the copies that may still be in flight (after an abort).
@@ -300,20 +324,19 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // ------------------------------------------------------------ V tails
         uint32_t e0 = 0, tails = 0;  // tails, bit r: phase of slot r's v_tail
         for (uint32_t kq = 0;; ++kq) {
-            int32_t u = -1;
-            if (!__all_sync(~0u, take_item(kq, u))) break;
+            QWork q;
+            if (!__all_sync(~0u, take_item(kq, q))) break;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_item_empty(int(kq % kItemQ)));
-            if (u < 0) break;
-            const QBlock q = *block_of(u);
-            const uint32_t n = uint32_t(q.chunks);
+            if (q.n < 0) break;
+            const uint32_t n = uint32_t(q.n);
             if (ragged(q)) {
                 const uint32_t e = e0 + entry_v(n - 1, n);
                 const int r = int(e % S);
                 if (!__all_sync(~0u, wait_bar(bar_v_tail(r), (tails >> r) & 1u))) break;
                 tails ^= 1u << r;
                 if (!__all_sync(~0u, wait_bar(bar_full(r), (e / S) & 1u))) break;
-                const int from = q.nkeys - int(n - 1) * 128;  // rows [from, 128) hold no key
+                const int from = q.nkeys - (q.c0 + q.n - 1) * 128;  // rows [from, 128) hold no key
                 uint8_t* v0 = smem + C::kRingOff + r * C::kKVBytes;
                 for (int i = from * 8 + lane; i < 128 * 8; i += 32)
 #pragma unroll
@@ -342,12 +365,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 return true;
             };
             for (uint32_t kq = 0; ok; ++kq) {
-                int32_t u;
-                if (!take_item(kq, u)) break;
+                QWork q;
+                if (!take_item(kq, q)) break;
                 ptx::mbar_arrive(bar_item_empty(int(kq % kItemQ)));
-                if (u < 0) break;
-                const QBlock q = *block_of(u);
-                const uint32_t n = uint32_t(q.chunks);
+                if (q.n < 0) break;
+                const uint32_t n = uint32_t(q.n);
                 const uint32_t g0 = g;
                 if (pv_role) {
                     const uint32_t tO = tmem + C::kColO;
@@ -429,17 +451,17 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         uint32_t g = 0;
         bool ok = true;
         for (uint32_t kq = 0; ok; ++kq) {
-            int32_t u = -1;
-            const bool took = __all_sync(~0u, take_item(kq, u));
+            QWork q;
+            q.n = -1;
+            const bool took = __all_sync(~0u, take_item(kq, q));
             __syncwarp();
             if (took && lane == 0) ptx::mbar_arrive(bar_item_empty(int(kq % kItemQ)));
             if (ptx::bar_red_or(pair_bar, 64, !took)) {  // leave together
                 ok = false;
                 break;
             }
-            if (u < 0) break;
-            const QBlock q = *block_of(u);
-            const uint32_t n = uint32_t(q.chunks);
+            if (q.n < 0) break;
+            const uint32_t n = uint32_t(q.n);
             const bool real = r_tok < q.ntok;
             const int limit = real ? min(q.nkeys, q.limit0 + (p.causal ? r_tok : 0)) : INT32_MAX;
             const int warp_limit = __reduce_min_sync(~0u, limit);  // over the rows that are stored
@@ -459,7 +481,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
                 }
                 pre = false;
-                const int kbeg = int(i) * 128 + half * 64;
+                const int kbeg = (q.c0 + int(i)) * 128 + half * 64;
                 const bool masked = kbeg + 64 > warp_limit;
                 if (wok && masked) mask_from(sr, limit - kbeg);
                 // Is S(g + 1) of this block complete?  If so, its load starts
@@ -562,13 +584,25 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const bool none = l_sum == 0.0f;  // no visible key: O = 0, whatever TMEM holds
             const float inv_l = 1.0f / l_sum;
             const uint64_t f2inv = ptx::f2(inv_l, inv_l);
-            const int32_t head = (u % K) * p.group + r_head;
+            const int32_t head = q.hk * p.group + r_head;
             const int64_t tok = q.tok0 + r_tok;
             uint4* dst = reinterpret_cast<uint4*>(p.o.p + tok * p.o.ts + head * p.o.hs + half * (D / 2));
+            // a part: O unnormalised in fp32, and after the rows m (in units of log2) and l
+            float* part = p.v.parts + (int64_t(q.slot) * K + q.hk) * (128 * (D + 2));
 #pragma unroll 1
             for (int cb = 0; cb < D / 64; ++cb) {
                 uint32_t orr[32];
                 ptx::tmem_ld32(tOh + cb * 32, orr);  // every lane loads: the access is warp-wide
+                if (q.slot >= 0) {
+                    float4* d4 = reinterpret_cast<float4*>(part + row * D + half * (D / 2) + cb * 32);
+                    if (real)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            d4[j] = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                         : make_float4(__uint_as_float(orr[4 * j]), __uint_as_float(orr[4 * j + 1]),
+                                                       __uint_as_float(orr[4 * j + 2]), __uint_as_float(orr[4 * j + 3]));
+                    continue;
+                }
                 uint32_t pk[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -584,7 +618,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         dst[cb * 4 + j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
                 }
             }
-            if (half == 0 && real)
+            if (q.slot >= 0) {
+                if (half == 0 && real)
+                    *reinterpret_cast<float2*>(part + 128 * D + 2 * row) = make_float2(none ? -INFINITY : m_used * c, l_sum);
+            } else if (half == 0 && real)
                 p.lse[int64_t(head) * p.tokens_q + tok] = none ? -INFINITY : m_used * p.scale + logf(l_sum);
             ptx::tc_fence_before();
             __syncwarp();
@@ -617,9 +654,50 @@ __global__ void packed_no_keys_kernel(const PackedProblem p, const packed::View 
     }
 }
 
+// Joins the parts of split query blocks: O = sum 2^(m_i - m) O_i / l, in the order of the parts.
+// One warp for each row, 8 rows (of blockIdx.y) to a CTA.
+template <int D>
+__global__ void __launch_bounds__(256) packed_join_kernel(const FwdParams p) {
+    constexpr int E = D / 32;
+    ops::grid_wait();
+    const int lane = threadIdx.x & 31, K = p.kv_heads;
+    const int64_t n = int64_t(p.v.lists->n_q) * K;
+    for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+        const QBlock q = p.v.qblocks[w / K];
+        const int hk = int(w % K);
+        if (q.split < 2) continue;
+        const int row = blockIdx.y * 8 + threadIdx.x / 32;
+        if (row < q.ntok * p.group) {
+            auto part = [&](int i) { return p.v.parts + (int64_t(q.slot + i) * K + hk) * (128 * (D + 2)); };
+            float m = -INFINITY, l = 0.0f, x[E] = {};
+            for (int i = lane; i < q.split; i += 32) m = fmaxf(m, part(i)[128 * D + 2 * row]);
+            for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
+            const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
+            for (int i = 0; i < q.split; ++i) {
+                const float* src = part(i);
+                const float2 st = *reinterpret_cast<const float2*>(src + 128 * D + 2 * row);
+                const float f = ptx::ex2(st.x - mu);
+                l += st.y * f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] += src[row * D + lane * E + e] * f;
+            }
+            const bool none = l == 0.0f;
+            const float inv = none ? 0.0f : 1.0f / l;
+            const int64_t tok = q.tok0 + row / p.group;
+            const int head = hk * p.group + row % p.group;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o.p + tok * p.o.ts + head * p.o.hs + lane * E);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) dst[e] = none ? 0u : ptx::pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+            if (lane == 0)
+                p.lse[int64_t(head) * p.tokens_q + tok] = none ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+        }
+    }
+}
+
 template <int D>
 cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, const Rows& v, const Rows& o, float* lse,
-                       const packed::View& view, int64_t max_items, int sms, cudaStream_t stream) {
+                       const packed::Layout& w, const packed::View& view, cudaStream_t stream) {
     const int tpb = 128 / p.group;
     CUtensorMap mq, mk, mv;
     cudaError_t e = packed::rows_map(&mq, q, p.tokens_q, p.heads, D, p.group, tpb);
@@ -631,8 +709,14 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     constexpr int kSmem = Cfg<D>::kSmemBytes;
     e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = unsigned(max_items < sms ? max_items : sms);
-    return packed::launch(packed_fwd_kernel<D>, grid, kThreads, kSmem, stream, true, mq, mk, mv, fp);
+    const int64_t items = w.max_wq * p.kv_heads;
+    e = packed::launch(packed_fwd_kernel<D>, dim3(unsigned(items < w.sms ? items : w.sms)), kThreads, kSmem, stream, true, mq, mk,
+                       mv, fp);
+    if (e == cudaSuccess && w.split_q) {
+        const int64_t blocks = w.max_q * p.kv_heads;
+        e = packed::launch(packed_join_kernel<D>, dim3(unsigned(blocks), 16), 256, 0, stream, true, fp);  // (fewer than 2 SMs' worth)
+    }
+    return e;
 }
 
 }  // namespace
@@ -676,7 +760,9 @@ sta_status packed_problem(const sta_packed* p, bool pointers, PackedProblem* out
 
 cudaError_t launch_packed_forward(const PackedProblem& p, int head_dim, const Rows& q, const Rows& k, const Rows& v,
                                   const Rows& o, float* lse, void* workspace, cudaStream_t stream) {
-    const packed::Layout w = packed::layout(p, false);
+    int sms = 0;
+    if (cudaError_t e = packed::sm_count(&sms); e != cudaSuccess) return e;
+    const packed::Layout w = packed::layout(p, false, head_dim, sms);
     const packed::View view = packed::view(w, workspace);
     packed::Tails tails{};
     tails.r[0] = o;
@@ -684,15 +770,12 @@ cudaError_t launch_packed_forward(const PackedProblem& p, int head_dim, const Ro
     tails.is_q[0] = 1;
     tails.n = 1;
     tails.lse = lse;
-    int sms = 0;
-    cudaError_t e = packed::sm_count(&sms);
-    if (e == cudaSuccess) e = packed::launch_lists(p, view, false, head_dim, tails, stream);
+    const cudaError_t e = packed::launch_lists(p, view, false, head_dim, tails, stream);
     if (e != cudaSuccess || p.batch == 0) return e;
     if (p.tokens_k == 0)
-        return packed::launch(packed_no_keys_kernel, unsigned(sms), 256, 0, stream, true, p, view, head_dim, o, lse);
-    const int64_t items = w.max_q * p.kv_heads;
-    if (head_dim == 128) return launch_fwd<128>(p, q, k, v, o, lse, view, items, sms, stream);
-    return launch_fwd<64>(p, q, k, v, o, lse, view, items, sms, stream);
+        return packed::launch(packed_no_keys_kernel, dim3(unsigned(w.sms)), 256, 0, stream, true, p, view, head_dim, o, lse);
+    if (head_dim == 128) return launch_fwd<128>(p, q, k, v, o, lse, w, view, stream);
+    return launch_fwd<64>(p, q, k, v, o, lse, w, view, stream);
 }
 
 }  // namespace sta
@@ -705,7 +788,7 @@ sta_status sta_packed_workspace(const sta_packed* p, int32_t backward, int64_t* 
     PackedProblem pp;
     if (bytes == nullptr || (backward != 0 && backward != 1)) return STA_ERR_INVALID_ARG;
     if (sta_status st = packed_problem(p, false, &pp); st != STA_OK) return st;
-    *bytes = packed::layout(pp, backward != 0).bytes;
+    *bytes = packed::layout(pp, backward != 0, p->head_dim, packed::sm_count_or_b200()).bytes;
     return STA_OK;
 }
 

@@ -7,8 +7,13 @@
 // short sequences then fill a block G times better than one head's would, the
 // causal diagonal wastes T tokens of a key chunk instead of 128, and the
 // gradients of a shared key head are sums over one block's rows.  A key block is
-// 128 keys of one sequence and key head.  The lists hold blocks, ordered by
-// falling work; an item is (block, key head).
+// 128 keys of one sequence and key head.
+//
+// Work.  A query block walks the 128-key chunks that it sees, a key block the query
+// blocks that see it.  Where there are too few blocks to level the GPU (the caller's
+// rule on sizes), long walks are split into parts: each part keeps fp32 sums in the
+// workspace, a last kernel joins them in order.  The lists hold the walks (whole or
+// parts), longest first; an item is (walk, key head).
 #pragma once
 
 #include <cuda.h>
@@ -28,34 +33,66 @@ struct alignas(16) QBlock {
     int32_t key0, nkeys;    // the sequence's keys
     int32_t limit0;         // keys that the block's first token sees (< 1: none); causal: one more for each token
     int32_t chunks;         // 128-key chunks to walk, at least 1
-    int32_t pad[2];
+    int32_t split;          // parts of its walk (1: whole)
+    int32_t slot;           // split: first of the parts' places in the workspace
 };
 struct alignas(16) KBlock {
     int32_t key0, nkeys;    // first key (row of the tensors), keys (1..128)
     int32_t pos;            // its position in the sequence
     int32_t q0, nq;         // the query blocks that see it: [q0, q0 + nq)
-    int32_t pad[3];
+    int32_t split, slot;    // as above
+    int32_t pad;
+};
+// A walk, or a part of one, as the kernels' load warps take it (n < 0: no more).
+struct alignas(16) QWork {
+    int32_t tok0, ntok, key0, nkeys;
+    int32_t limit0, c0, n, slot;   // chunks [c0, c0 + n); slot < 0: whole
+    int32_t block, hk, pad[2];     // query block; key head (set by the load warp)
+};
+struct alignas(16) KWork {
+    int32_t key0, nkeys, pos, q0;
+    int32_t n, slot, hk, pad;      // query blocks [q0, q0 + n)
 };
 
 // Head of the workspace.
 struct Lists {
-    int32_t n_q, n_k;       // blocks
+    int32_t n_q, n_k;                 // blocks
+    int32_t w_q, w_k;                 // walks
     int32_t next_q, next_k, next_dq;  // item counters of the kernels (zeroed with the lists)
 };
 
+constexpr int kSplitParts = 4;  // split walks have at most this many parts to an SM, over all key heads
+constexpr int kMinPart = 4;     // steps of a part
+
 // Offsets into the workspace, from the problem's sizes alone.
 struct Layout {
-    int64_t qblocks, kblocks, order_q, order_k, bounds, neg_l, neg_d, bytes;
-    int64_t max_q, max_k;
+    int64_t qblocks, kblocks, qwalks, kwalks, scratch, bounds, neg_l, neg_d, parts, bytes;
+    int64_t max_q, max_k;      // blocks
+    int64_t max_wq, max_wk;    // walks
+    int32_t split_q, split_k;  // may walks be split?
+    int32_t sms;
 };
 
 inline int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
-inline Layout layout(const PackedProblem& p, bool backward) {
+// Split where every SM would get fewer than two blocks: with more, the longest walks first
+// level the SMs nearly by themselves (a long sequence has many blocks), and the parts' sums
+// cost what they save.  (Six sequences of 300-2047 tokens, 16 / 2 heads, d = 64: dK / dV
+// 227 us whole, 75 split, plus the sums; one of 8192 tokens, 24 / 8 heads, d = 128, 520 blocks:
+// 730 whole, 848 split.)
+inline Layout layout(const PackedProblem& p, bool backward, int head_dim, int sms) {
     Layout w{};
     const int tpb = kRows / p.group;
+    w.sms = sms;
     w.max_q = p.tokens_q / tpb + p.batch;
     w.max_k = backward ? p.tokens_k / kRows + p.batch : 0;
+    // (nothing to gain where the sequences' mean is a few steps: the join would be launched for nothing)
+    const int64_t long_k = int64_t(p.batch) * kMinPart * kRows, long_q = int64_t(p.batch) * kMinPart * tpb;
+    w.split_q = w.max_q * p.kv_heads < 2 * int64_t(sms) && p.tokens_k > long_k;
+    w.split_k = backward && w.max_k * p.kv_heads < 2 * int64_t(sms) && p.tokens_q > long_q;
+    const int64_t extra = int64_t(kSplitParts) * sms;
+    w.max_wq = w.max_q + (w.split_q ? extra : 0);
+    w.max_wk = w.max_k + (w.split_k ? extra : 0);
     int64_t at = 256;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -64,13 +101,18 @@ inline Layout layout(const PackedProblem& p, bool backward) {
     };
     w.qblocks = take(w.max_q * sizeof(QBlock));
     w.kblocks = take(w.max_k * sizeof(KBlock));
-    w.order_q = take(w.max_q * 4);
-    w.order_k = take(w.max_k * 4);
+    w.qwalks = take(w.max_wq * sizeof(QWork));
+    w.kwalks = take(w.max_wk * sizeof(KWork));
+    w.scratch = take((w.max_wq > w.max_wk ? w.max_wq : w.max_wk) * 8);
     w.bounds = take((int64_t(p.batch) + 1) * 4 * 4);
     if (backward) {
         w.neg_l = take(w.max_q * p.kv_heads * kRows * 4);
         w.neg_d = take(w.max_q * p.kv_heads * kRows * 4);
     }
+    // parts: O with m and l, or dQ; dK and dV (dQ's are joined before dK / dV's are written)
+    const int64_t of_q = w.split_q ? extra * kRows * (head_dim + 2) * 4 : 0;
+    const int64_t of_k = w.split_k ? extra * kRows * head_dim * 2 * 4 : 0;
+    w.parts = take(of_q > of_k ? of_q : of_k);
     w.bytes = at;
     return w;
 }
@@ -80,15 +122,20 @@ struct View {
     Lists* lists;
     QBlock* qblocks;
     KBlock* kblocks;
-    int32_t* order_q;
-    int32_t* order_k;
+    QWork* qwalks;
+    KWork* kwalks;
+    int2* scratch;    // (block, part) of each walk before they are ordered
     int32_t* bounds;  // [4][batch + 1]: cut cu_q, cut cu_k, first query block, first key block
+    float* parts;
+    int32_t split_q, split_k, sms;
 };
 inline View view(const Layout& w, void* ws) {
     char* b = static_cast<char*>(ws);
     return View{reinterpret_cast<Lists*>(b), reinterpret_cast<QBlock*>(b + w.qblocks),
-                reinterpret_cast<KBlock*>(b + w.kblocks), reinterpret_cast<int32_t*>(b + w.order_q),
-                reinterpret_cast<int32_t*>(b + w.order_k), reinterpret_cast<int32_t*>(b + w.bounds)};
+                reinterpret_cast<KBlock*>(b + w.kblocks), reinterpret_cast<QWork*>(b + w.qwalks),
+                reinterpret_cast<KWork*>(b + w.kwalks), reinterpret_cast<int2*>(b + w.scratch),
+                reinterpret_cast<int32_t*>(b + w.bounds), reinterpret_cast<float*>(b + w.parts),
+                w.split_q, w.split_k, w.sms};
 }
 
 // Rows of outputs to clear behind the last sequence (clear_tail).
@@ -112,13 +159,13 @@ cudaError_t rows_map(CUtensorMap* m, const Rows& r, int64_t tokens, int heads, i
 // Launch attributes: `pdl`: the kernel may start while its predecessor in the
 // stream ends, and waits for it (griddepcontrol.wait) before it reads memory.
 template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, bool pdl,
+cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, bool pdl,
                    A&&... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -131,6 +178,14 @@ inline cudaError_t sm_count(int* sms) {
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+// The same for workspace sizes, which may be asked for without a device (then a B200's).
+inline int sm_count_or_b200() {
+    int sms = 0;
+    if (sm_count(&sms) == cudaSuccess) return sms;
+    (void)cudaGetLastError();
+    return 148;
 }
 
 }  // namespace packed

@@ -34,7 +34,9 @@ namespace sta {
 namespace {
 
 using packed::KBlock;
+using packed::KWork;
 using packed::QBlock;
+using packed::QWork;
 
 constexpr int kThreads = 320;  // warps 0-7 elementwise, 8 load, 9 MMA
 constexpr int kLoadWarp = 8;
@@ -73,22 +75,29 @@ __device__ __forceinline__ void load_block(uint32_t dst, const CUtensorMap* m, u
     for (int cb = 0; cb < D / 64; ++cb) ops::tma_load_3d(dst + cb * kBoxBytes, m, bar, cb * 64, head, tok);
 }
 
-// Producer side of the item queue (one thread): publish this CTA's k-th item (-1: none left).
-// Returns it, or -2 when the CTA is aborting.
-__device__ __forceinline__ int32_t put_item(uint32_t k, int32_t* next, int32_t n_items, uint32_t full0, uint32_t empty0,
-                                            volatile int32_t* q, volatile int* abort_flag, const BwdParams& p) {
-    int32_t u = atomicAdd(next, 1);
-    if (u >= n_items) u = -1;
+// The item queue.  A CTA's first item is its own number, the others come from a counter; an item
+// is only taken when the copies of the one before are issued, so that longest-first levels the CTAs.
+template <class Work>
+__device__ __forceinline__ bool put_item(uint32_t k, Work& w, const Work* walks, int32_t* next, int32_t n_items, int32_t heads,
+                                         uint32_t full0, uint32_t empty0, Work* q, volatile int* abort_flag,
+                                         const BwdParams& p) {
+    const int32_t u = k == 0 ? int32_t(blockIdx.x) : int32_t(gridDim.x) + atomicAdd(next, 1);
+    w.n = -1;
+    if (u < n_items) {
+        w = walks[u / heads];
+        w.hk = u % heads;
+    }
     const uint32_t e = k % kItemQ;
-    if (k >= uint32_t(kItemQ) && !wait_bw(empty0 + 8u * e, ((k / kItemQ) - 1) & 1u, abort_flag, p)) return -2;
-    q[e] = u;
+    if (k >= uint32_t(kItemQ) && !wait_bw(empty0 + 8u * e, ((k / kItemQ) - 1) & 1u, abort_flag, p)) return false;
+    q[e] = w;
     ptx::mbar_arrive(full0 + 8u * e);
-    return u;
+    return w.n >= 0;
 }
-__device__ __forceinline__ bool get_item(uint32_t k, uint32_t full0, volatile int32_t* q, volatile int* abort_flag,
-                                        const BwdParams& p, int32_t& u) {
+template <class Work>
+__device__ __forceinline__ bool get_item(uint32_t k, uint32_t full0, const Work* q, volatile int* abort_flag,
+                                        const BwdParams& p, Work& w) {
     if (!wait_bw(full0 + 8u * (k % kItemQ), (k / kItemQ) & 1u, abort_flag, p)) return false;
-    u = q[k % kItemQ];
+    w = q[k % kItemQ];
     return true;
 }
 
@@ -116,6 +125,22 @@ __device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloa
             v.w = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 6]) * mul, __uint_as_float(r[8 * j + 7]) * mul);
             d4[cb * 4 + j] = zero ? make_uint4(0u, 0u, 0u, 0u) : v;
         }
+    }
+}
+
+// The same as fp32, as they are: a part's sums.
+template <int kCols>
+__device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool store) {
+    float4* d4 = reinterpret_cast<float4*>(dst);
+#pragma unroll 1
+    for (int cb = 0; cb < kCols / 32; ++cb) {
+        uint32_t r[32];
+        ptx::tmem_ld32(taddr + cb * 32, r);
+        if (!store) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            d4[cb * 8 + j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                         __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
     }
 }
 
@@ -188,7 +213,9 @@ struct DqCfg {
     // s_full[2], dp_full, ds_full, dq_full, drain, item_full[Q], item_empty[Q]
     static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 8 + 2 * kItemQ;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kSmemBytes = kMiscOff + 8 + 4 * kItemQ + 1024;
+    static constexpr int kQueueOff = kMiscOff + 16;
+    static constexpr int kSmemBytes = kQueueOff + kItemQ * int(sizeof(QWork)) + 1024;
+    static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     static constexpr uint32_t kColS0 = 0, kColDP = 256, kColDQ = 384;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
     static_assert(kColDQ + D <= kTmemCols, "TMEM budget");
@@ -219,7 +246,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t item_full0 = xb + 64, item_empty0 = xb + 64 + 8 * kItemQ;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-    volatile int32_t* item_q = reinterpret_cast<volatile int32_t*>(smem + C::kMiscOff + 8);
+    QWork* item_q = reinterpret_cast<QWork*>(smem + C::kQueueOff);
 
     if (threadIdx.x == 0) {
         for (int r = 0; r < KS; ++r) {
@@ -267,20 +294,20 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == kLoadWarp) {
         if (lane == 0) {
             // ------------------------------------------------------------ load
-            const int32_t n_items = p.v.lists->n_q * K;
+            const int32_t n_items = p.v.lists->w_q * K;
             uint32_t kit = 0, vit = 0, qc = 0;
             bool ok = true;
             for (uint32_t kq = 0; ok; ++kq) {
-                const int32_t u = put_item(kq, &p.v.lists->next_dq, n_items, item_full0, item_empty0, item_q, abort_flag, p);
-                if (u < 0) break;
-                const QBlock q = p.v.qblocks[p.v.order_q[u / K]];
-                const int32_t hk = u % K;
+                QWork q;
+                if (!put_item(kq, q, p.v.qwalks, &p.v.lists->next_dq, n_items, K, item_full0, item_empty0, item_q, abort_flag, p))
+                    break;
+                const int32_t hk = q.hk;
                 if (!wait_bw(q_empty, (qc & 1u) ^ 1u, abort_flag, p)) break;
                 ptx::mbar_arrive_expect_tx(q_full, 2 * (D / 64) * p.q_box_bytes);
                 load_block<D>(base + C::kQOff, &tm_q, q_full, hk * p.group, q.tok0);
                 load_block<D>(base + C::kDOOff, &tm_do, q_full, hk * p.group, q.tok0);
                 ++qc;
-                for (int32_t c = 0; c < q.chunks; ++c) {
+                for (int32_t c = q.c0; c < q.c0 + q.n; ++c) {
                     const int rk = int(kit % KS);
                     if (kit >= uint32_t(KS) && !wait_bw(k_empty(rk), ((kit / KS) - 1) & 1u, abort_flag, p)) {
                         ok = false;
@@ -315,11 +342,11 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             uint32_t kbase = 0, gs = 0, qc = 0;
             bool ok = true;
             for (uint32_t kq = 0; ok; ++kq) {
-                int32_t u;
-                if (!get_item(kq, item_full0, item_q, abort_flag, p, u)) break;
+                QWork q;
+                if (!get_item(kq, item_full0, item_q, abort_flag, p, q)) break;
                 ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
-                if (u < 0) break;
-                const int32_t n = p.v.qblocks[p.v.order_q[u / K]].chunks;
+                if (q.n < 0) break;
+                const int32_t n = q.n;
                 if (!wait_bw(q_full, qc & 1u, abort_flag, p)) break;
                 ++qc;
                 ptx::tc_fence_after();
@@ -391,18 +418,16 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint32_t gs = 0, dqc = 0;
         bool ok = true;
         for (uint32_t kq = 0; ok; ++kq) {
-            int32_t u = -1;
-            if (!__all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, u))) break;
+            QWork q;
+            if (!__all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, q))) break;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
-            if (u < 0) break;
-            const int32_t e = p.v.order_q[u / K], hk = u % K;
-            const QBlock q = p.v.qblocks[e];
-            const int32_t n = q.chunks;
+            if (q.n < 0) break;
+            const int32_t hk = q.hk, n = q.n;
             const bool real = r_tok < q.ntok;
             const int limit = real ? min(q.nkeys, q.limit0 + (p.causal ? r_tok : 0)) : INT32_MAX;
             const int warp_limit = __reduce_min_sync(~0u, limit);
-            const int64_t grow = (int64_t(e) * K + hk) * 128 + row;
+            const int64_t grow = (int64_t(q.block) * K + hk) * 128 + row;
             const float nl = p.neg_l[grow], nd = p.neg_d[grow];
             const uint64_t nl2 = ptx::f2(nl, nl), nd2 = ptx::f2(nd, nd);
             for (int32_t j = 0; j < n; ++j) {
@@ -412,10 +437,11 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     break;
                 }
                 ptx::tc_fence_after();
-                const int seen = limit - (j * 128 + 64 * h);  // keys of this half that the row sees
-                const bool masked = warp_limit < j * 128 + 64 * h + 64;
-                if ((j + 1) * 128 > q.nkeys)  // the sequence's last chunk: S has read K, dQ has not
-                    zero_rows<D>(smem + C::kKOff + (step % KS) * C::kBlk, q.nkeys - j * 128, threadIdx.x);
+                const int key = (q.c0 + j) * 128;  // the chunk's first
+                const int seen = limit - (key + 64 * h);  // keys of this half that the row sees
+                const bool masked = warp_limit < key + 64 * h + 64;
+                if (key + 128 > q.nkeys)  // the sequence's last chunk: S has read K, dQ has not
+                    zero_rows<D>(smem + C::kKOff + (step % KS) * C::kBlk, q.nkeys - key, threadIdx.x);
                 float pr[64];
                 {
                     uint32_t sr[64];
@@ -468,7 +494,11 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!__all_sync(~0u, wait_bw(dq_full, dqc & 1u, abort_flag, p))) break;
             ++dqc;
             ptx::tc_fence_after();
-            store_cols<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h, p.scale,
+            if (q.slot >= 0)
+                store_part<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h,
+                                  p.v.parts + (int64_t(q.slot) * K + hk) * (128 * D) + row * D + (D / 2) * h, real);
+            else
+                store_cols<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h, p.scale,
                               p.out_a.p + int64_t(q.tok0 + r_tok) * p.out_a.ts + (hk * p.group + r_head) * p.out_a.hs +
                                   (D / 2) * h,
                               real, limit <= 0);
@@ -501,7 +531,9 @@ struct DkvCfg {
     // ds_full, dkv_full, drain, item_full[Q], item_empty[Q]
     static constexpr int kNumBars = 2 * kStages + 8 + 2 * kItemQ;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kSmemBytes = kMiscOff + 8 + 4 * kItemQ + 1024;
+    static constexpr int kQueueOff = kMiscOff + 16;
+    static constexpr int kSmemBytes = kQueueOff + kItemQ * int(sizeof(QWork)) + 1024;
+    static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     static constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 256 + D;
     static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -531,7 +563,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto stage_off = [&](int r) { return C::kStageOff + r * C::kStageBytes; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-    volatile int32_t* item_q = reinterpret_cast<volatile int32_t*>(smem + C::kMiscOff + 8);
+    KWork* item_q = reinterpret_cast<KWork*>(smem + C::kQueueOff);
     const int rows_used = (128 / p.group) * p.group;  // rows of a query block's box
 
     if (threadIdx.x == 0) {
@@ -581,20 +613,20 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == kLoadWarp) {
         if (lane == 0) {
             // ------------------------------------------------------------ load
-            const int32_t n_items = p.v.lists->n_k * K;
+            const int32_t n_items = p.v.lists->w_k * K;
             uint32_t sit = 0, kvc = 0;
             bool ok = true;
             for (uint32_t kq = 0; ok; ++kq) {
-                const int32_t u = put_item(kq, &p.v.lists->next_k, n_items, item_full0, item_empty0, item_q, abort_flag, p);
-                if (u < 0) break;
-                const KBlock kb = p.v.kblocks[p.v.order_k[u / K]];
-                const int32_t hk = u % K;
+                KWork kb;
+                if (!put_item(kq, kb, p.v.kwalks, &p.v.lists->next_k, n_items, K, item_full0, item_empty0, item_q, abort_flag, p))
+                    break;
+                const int32_t hk = kb.hk;
                 if (!wait_bw(kv_empty, (kvc & 1u) ^ 1u, abort_flag, p)) break;
                 ptx::mbar_arrive_expect_tx(kv_full, 2 * C::kBlk);
                 load_block<D>(base + C::kKOff, &tm_k, kv_full, hk, kb.key0);
                 load_block<D>(base + C::kVOff, &tm_v, kv_full, hk, kb.key0);
                 ++kvc;
-                for (int32_t j = 0; j < kb.nq; ++j) {
+                for (int32_t j = 0; j < kb.n; ++j) {
                     const int r = int(sit % NS);
                     if (sit >= uint32_t(NS) && !wait_bw(st_empty(r), ((sit / NS) - 1) & 1u, abort_flag, p)) {
                         ok = false;
@@ -624,11 +656,11 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             uint32_t gs = 0, kvc = 0;
             bool ok = true;
             for (uint32_t kq = 0; ok; ++kq) {
-                int32_t u;
-                if (!get_item(kq, item_full0, item_q, abort_flag, p, u)) break;
+                KWork kb;
+                if (!get_item(kq, item_full0, item_q, abort_flag, p, kb)) break;
                 ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
-                if (u < 0) break;
-                const int32_t n = p.v.kblocks[p.v.order_k[u / K]].nq;
+                if (kb.n < 0) break;
+                const int32_t n = kb.n;
                 if (!wait_bw(kv_full, kvc & 1u, abort_flag, p)) break;
                 ++kvc;
                 ptx::tc_fence_after();
@@ -705,13 +737,12 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t gs = 0, kvc = 0;
         bool ok = true;
         for (uint32_t kq = 0; ok; ++kq) {
-            int32_t u = -1;
-            if (!__all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, u))) break;
+            KWork kb;
+            if (!__all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, kb))) break;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
-            if (u < 0) break;
-            const KBlock kb = p.v.kblocks[p.v.order_k[u / K]];
-            const int32_t hk = u % K, n = kb.nq;
+            if (kb.n < 0) break;
+            const int32_t hk = kb.hk, n = kb.n;
             for (int32_t j = 0; j < n; ++j) {
                 const uint32_t step = gs + uint32_t(j);
                 const int r = int(step % NS);
@@ -808,6 +839,14 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ptx::tc_fence_after();
             const bool real = row < kb.nkeys;
             const int64_t tok = kb.key0 + row;
+            if (kb.slot >= 0) {
+                float* part = p.v.parts + (int64_t(kb.slot) * K + hk) * (2 * 128 * D) + row * D + (D / 2) * h;
+                store_part<D / 2>(tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h, part, real);
+                store_part<D / 2>(tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h, part + 128 * D, real);
+                ptx::tc_fence_before();
+                gs += uint32_t(n);
+                continue;
+            }
             store_cols<D / 2>(tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h, 1.0f,
                               p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + (D / 2) * h, real, n == 0);
             store_cols<D / 2>(tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h, p.scale,
@@ -823,6 +862,61 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncwarp();
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- parts
+// Sums of the parts of split blocks, in their order: dQ (kKeys = false), or dK and dV.  16 bytes
+// of the result for each thread; blockIdx.y: 256 threads' worth of a block.
+template <int D, bool kKeys>
+__global__ void __launch_bounds__(256) packed_sum_kernel(const BwdParams p) {
+    ops::grid_wait();
+    const int K = p.kv_heads;
+    const int64_t n = int64_t(kKeys ? p.v.lists->n_k : p.v.lists->n_q) * K;
+    for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+        const int hk = int(w % K);
+        int32_t split, slot, rows, row0;
+        if (kKeys) {
+            const KBlock b = p.v.kblocks[w / K];
+            split = b.split;
+            slot = b.slot;
+            rows = b.nkeys;
+            row0 = b.key0;
+        } else {
+            const QBlock b = p.v.qblocks[w / K];
+            split = b.split;
+            slot = b.slot;
+            rows = b.ntok * p.group;
+            row0 = b.tok0;
+        }
+        if (split < 2) continue;
+        constexpr int kPlanes = kKeys ? 2 : 1;
+        const int i = blockIdx.y * 256 + threadIdx.x;
+        if (i < rows * (D / 8) * kPlanes) {
+            const int plane = i / (rows * (D / 8)), at = i % (rows * (D / 8)), row = at / (D / 8), col = at % (D / 8) * 8;
+            float x[8] = {};
+#pragma unroll 4
+            for (int k = 0; k < split; ++k) {
+                const float4* src = reinterpret_cast<const float4*>(
+                    p.v.parts + ((int64_t(slot + k) * K + hk) * kPlanes + plane) * (128 * D) + row * D + col);
+                const float4 a = src[0], b = src[1];
+                x[0] += a.x;
+                x[1] += a.y;
+                x[2] += a.z;
+                x[3] += a.w;
+                x[4] += b.x;
+                x[5] += b.y;
+                x[6] += b.z;
+                x[7] += b.w;
+            }
+            const float mul = plane == 0 ? p.scale : 1.0f;
+            const Rows& out = plane == 0 ? p.out_a : p.out_b;
+            const int64_t tok = row0 + (kKeys ? row : row / p.group);
+            const int head = kKeys ? hk : hk * p.group + row % p.group;
+            *reinterpret_cast<uint4*>(out.p + tok * out.ts + head * out.hs + col) =
+                make_uint4(ptx::pack_bf16x2(x[0] * mul, x[1] * mul), ptx::pack_bf16x2(x[2] * mul, x[3] * mul),
+                           ptx::pack_bf16x2(x[4] * mul, x[5] * mul), ptx::pack_bf16x2(x[6] * mul, x[7] * mul));
+        }
     }
 }
 
@@ -874,17 +968,20 @@ cudaError_t launch_bwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(packed_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkv);
     const int64_t nq = w.max_q * p.kv_heads, nk = w.max_k * p.kv_heads;
+    const int64_t wq = w.max_wq * p.kv_heads, wk = w.max_wk * p.kv_heads;
+    auto grid = [&](int64_t n, int64_t most) { return dim3(unsigned(n < most ? n : most)); };
     if (e == cudaSuccess)
-        e = packed::launch(packed_prep_kernel<D>, unsigned(nq < 4 * sms ? nq : 4 * sms), 256, 0, stream, true, p, view, o,
-                           dout, lse, neg_l, neg_d);
+        e = packed::launch(packed_prep_kernel<D>, grid(nq, 4 * sms), 256, 0, stream, true, p, view, o, dout, lse, neg_l, neg_d);
     if (e == cudaSuccess)
-        e = packed::launch(packed_dq_kernel<D>, unsigned(nq < sms ? nq : sms), kThreads, kDq, stream, true, mq, mk, mv, md,
-                           bp);
+        e = packed::launch(packed_dq_kernel<D>, grid(wq, sms), kThreads, kDq, stream, true, mq, mk, mv, md, bp);
+    if (e == cudaSuccess && w.split_q)
+        e = packed::launch(packed_sum_kernel<D, false>, dim3(unsigned(nq), D / 16), 256, 0, stream, true, bp);
     bp.out_a = dk;
     bp.out_b = dv;
     if (e == cudaSuccess)
-        e = packed::launch(packed_dkdv_kernel<D>, unsigned(nk < sms ? nk : sms), kThreads, kDkv, stream, true, mq, mk, mv,
-                           md, bp);
+        e = packed::launch(packed_dkdv_kernel<D>, grid(wk, sms), kThreads, kDkv, stream, true, mq, mk, mv, md, bp);
+    if (e == cudaSuccess && w.split_k)
+        e = packed::launch(packed_sum_kernel<D, true>, dim3(unsigned(nk), D / 8), 256, 0, stream, true, bp);
     return e;
 }
 
@@ -893,7 +990,9 @@ cudaError_t launch_bwd(const PackedProblem& p, const Rows& q, const Rows& k, con
 cudaError_t launch_packed_backward(const PackedProblem& p, int head_dim, const Rows& q, const Rows& k, const Rows& v,
                                    const Rows& o, const Rows& dout, const float* lse, const Rows& dq, const Rows& dk,
                                    const Rows& dv, void* workspace, cudaStream_t stream) {
-    const packed::Layout w = packed::layout(p, true);
+    int sms = 0;
+    if (cudaError_t e = packed::sm_count(&sms); e != cudaSuccess) return e;
+    const packed::Layout w = packed::layout(p, true, head_dim, sms);
     const packed::View view = packed::view(w, workspace);
     packed::Tails tails{};
     tails.r[0] = dq;
@@ -903,14 +1002,12 @@ cudaError_t launch_packed_backward(const PackedProblem& p, int head_dim, const R
     tails.heads[1] = tails.heads[2] = p.kv_heads;
     tails.is_q[0] = 1;
     tails.n = 3;
-    int sms = 0;
-    cudaError_t e = packed::sm_count(&sms);
-    if (e == cudaSuccess) e = packed::launch_lists(p, view, true, head_dim, tails, stream);
+    const cudaError_t e = packed::launch_lists(p, view, true, head_dim, tails, stream);
     if (e != cudaSuccess || p.batch == 0) return e;
     if (p.tokens_k == 0)
-        return packed::launch(packed_zero_dq_kernel, unsigned(sms), 256, 0, stream, true, p, view, head_dim, dq);
+        return packed::launch(packed_zero_dq_kernel, dim3(unsigned(sms)), 256, 0, stream, true, p, view, head_dim, dq);
     if (p.tokens_q == 0)
-        return packed::launch(packed_zero_dkdv_kernel, unsigned(sms), 256, 0, stream, true, p, view, head_dim, dk, dv);
+        return packed::launch(packed_zero_dkdv_kernel, dim3(unsigned(sms)), 256, 0, stream, true, p, view, head_dim, dk, dv);
     if (head_dim == 128)
         return launch_bwd<128>(p, q, k, v, o, dout, lse, dq, dk, dv, static_cast<char*>(workspace), w, view, sms, stream);
     return launch_bwd<64>(p, q, k, v, o, dout, lse, dq, dk, dv, static_cast<char*>(workspace), w, view, sms, stream);

@@ -12,7 +12,7 @@ namespace packed {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kBins = 1024;     // blocks are ordered by min(work, kBins - 1), falling
+constexpr int kBins = 1024;     // walks are ordered by min(steps, kBins - 1), falling
 constexpr int kNear = 1024;     // up to this many sequences the bounds stay in shared memory
 
 struct Scan {
@@ -59,21 +59,100 @@ __device__ int owner(const int32_t* first, int batch, int e) {
     return lo;
 }
 
-// Blocks 0 .. n - 1 into `order` by falling work(e); within a bin in any order
-// (which block runs first changes no result).
-template <class Work>
-__device__ void by_work(int32_t n, int32_t* order, int32_t* bins, Scan& s, const Work& work) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) bins[i] = 0;
+constexpr int kNearBlocks = 2048;  // up to this many blocks their work and parts stay in shared memory
+
+// Part `i` of `parts` of a walk of w steps: its first step and their number.
+__device__ __forceinline__ int2 part_of(int32_t w, int32_t parts, int32_t i) {
+    const int32_t each = w / parts, more = w - each * parts;
+    return make_int2(i * each + min(i, more), each + (i < more ? 1 : 0));
+}
+
+// Walks of blocks 0 .. n - 1 by falling work, split into parts where `split`.  work(e): the steps
+// of block e; set(e, parts, slot): writes its split and slot; put(i, e, first, n, slot): writes
+// walk i.  Returns the number of walks.  Which walk runs first changes no result, so the order
+// within a bin is free.
+template <class Work, class Set, class Put>
+__device__ int32_t make_walks(int32_t n, int32_t kv_heads, bool split, int32_t sms, int2* near, int2* scratch, int32_t* bins,
+                              Scan& s, const Work& work, const Set& set, const Put& put) {
+    __shared__ unsigned long long sh_total;
+    __shared__ int32_t sh_most, sh_end[2];
+    if (threadIdx.x == 0) {
+        sh_total = 0ull;
+        sh_most = 0;
+    }
+    bins[threadIdx.x] = 0;
     __syncthreads();
-    for (int e = threadIdx.x; e < n; e += kThreads) atomicAdd(&bins[kBins - 1 - min(work(e), kBins - 1)], 1);
+    int32_t cap = INT32_MAX;
+    if (split) {
+        unsigned long long mine = 0ull;
+        int32_t most = 0;
+        for (int e = threadIdx.x; e < n; e += kThreads) {
+            mine += unsigned(work(e));
+            most = max(most, work(e));
+        }
+        for (int i = 16; i > 0; i >>= 1) {
+            mine += __shfl_xor_sync(~0u, mine, i);
+            most = max(most, __shfl_xor_sync(~0u, most, i));
+        }
+        if (threadIdx.x % 32 == 0) {
+            atomicAdd(&sh_total, mine);
+            atomicMax(&sh_most, most);
+        }
+        __syncthreads();
+        // nothing to split while the longest walk is below an SM's share; else into halves of a
+        // share: a block of w > cap steps has fewer than 2 w / cap parts, all together fewer
+        // than kSplitParts to an SM
+        const unsigned long long share = sh_total * unsigned(kv_heads) / unsigned(sms);
+        if (4ull * unsigned(sh_most) > 3ull * share) cap = max(kMinPart, int32_t(min(share / 2 + 1, 1ull << 30)));
+        split = cap < sh_most;
+    }
+    const auto add_ = [](int32_t a, int32_t b) { return a + b; };
+    int32_t walks = n, slots = 0;
+    // whole walks are their blocks in order; else (block, part) of each are listed first
+    int2* list = nullptr;
+    if (split) {
+        walks = 0;
+        list = n + kSplitParts * sms <= kNearBlocks ? near : scratch;
+        for (int e0 = 0; e0 < n; e0 += kThreads) {
+            const int e = e0 + threadIdx.x;
+            const int32_t w = e < n ? work(e) : 0, parts = e < n ? (w > cap ? (w + cap - 1) / cap : 1) : 0;
+            const int32_t at = walks + scan(parts, s, add_) - parts;
+            const int32_t more = parts > 1 ? parts : 0, slot = slots + scan(more, s, add_) - more;
+            if (threadIdx.x == kThreads - 1) {
+                sh_end[0] = at + parts;
+                sh_end[1] = slot + more;
+            }
+            if (e < n) {
+                set(e, parts, slot);
+                for (int i = 0; i < parts; ++i) {
+                    list[at + i] = make_int2(e, i);
+                    atomicAdd(&bins[kBins - 1 - min(part_of(w, parts, i).y, kBins - 1)], 1);
+                }
+            }
+            __syncthreads();
+            walks = sh_end[0];
+            slots = sh_end[1];
+            __syncthreads();
+        }
+    } else {
+        for (int e = threadIdx.x; e < n; e += kThreads) {
+            set(e, 1, 0);
+            atomicAdd(&bins[kBins - 1 - min(work(e), kBins - 1)], 1);
+        }
+    }
     __syncthreads();
     const int32_t mine = bins[threadIdx.x];
-    const int32_t upto = scan(mine, s, [](int32_t a, int32_t b) { return a + b; });
+    const int32_t upto = scan(mine, s, add_);
     bins[threadIdx.x] = upto - mine;
     __syncthreads();
-    for (int e = threadIdx.x; e < n; e += kThreads)
-        order[atomicAdd(&bins[kBins - 1 - min(work(e), kBins - 1)], 1)] = e;
+    for (int i = threadIdx.x; i < walks; i += kThreads) {
+        const int2 it = split ? list[i] : make_int2(i, 0);
+        const int32_t w = work(it.x), parts = w > cap ? (w + cap - 1) / cap : 1;
+        const int2 p = part_of(w, parts, it.y);
+        put(atomicAdd(&bins[kBins - 1 - min(p.y, kBins - 1)], 1), it.x, p.x, p.y, parts > 1, it.y);
+    }
     __syncthreads();
+    return walks;
 }
 static_assert(kBins == kThreads, "one bin for each thread in the scan");
 
@@ -119,6 +198,8 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
     __shared__ Scan s;
     __shared__ int32_t bins[kBins];
     __shared__ int32_t near_[4][kNear + 1];
+    __shared__ int32_t near_work[kNearBlocks];
+    __shared__ int2 near_list[kNearBlocks];
     const int B = p.batch, tid = threadIdx.x, tpb = kRows / p.group;
     int32_t* bound[4];  // cut cu_q, cut cu_k, first query block, first key block
     for (int i = 0; i < 4; ++i) bound[i] = B <= kNear ? near_[i] : v.bounds + int64_t(i) * (B + 1);
@@ -178,6 +259,7 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
         const int32_t sees = p.causal ? min(nk, q.limit0 + q.ntok - 1) : nk;  // of the block's last token
         q.chunks = max(1, (sees + kRows - 1) / kRows);
         v.qblocks[e] = q;
+        if (nbq <= kNearBlocks) near_work[e] = q.chunks;
     }
     for (int e = tid; e < nbk; e += kThreads) {
         const int b = owner(bound[3], B, e);
@@ -194,9 +276,34 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
         v.kblocks[e] = k;
     }
     __syncthreads();
-    by_work(nbq, v.order_q, bins, s, [&](int e) { return v.qblocks[e].chunks; });
-    if (backward) by_work(nbk, v.order_k, bins, s, [&](int e) { return v.kblocks[e].nq; });
-    if (tid == 0) *v.lists = Lists{nbq, nbk, 0, 0, 0};
+    const int32_t wq = make_walks(
+        nbq, p.kv_heads, v.split_q != 0, v.sms, near_list, v.scratch, bins, s,
+        [&](int e) { return nbq <= kNearBlocks ? near_work[e] : v.qblocks[e].chunks; },
+        [&](int e, int32_t parts, int32_t slot) {
+            v.qblocks[e].split = parts;
+            v.qblocks[e].slot = slot;
+        },
+        [&](int i, int e, int32_t first, int32_t n, bool part, int32_t which) {
+            const QBlock q = v.qblocks[e];
+            v.qwalks[i] = QWork{q.tok0, q.ntok, q.key0, q.nkeys, q.limit0, first, n, part ? q.slot + which : -1, e, 0, {0, 0}};
+        });
+    int32_t wk = 0;
+    if (backward) {
+        for (int e = tid; e < nbk && nbk <= kNearBlocks; e += kThreads) near_work[e] = v.kblocks[e].nq;
+        __syncthreads();
+        wk = make_walks(
+            nbk, p.kv_heads, v.split_k != 0, v.sms, near_list, v.scratch, bins, s,
+            [&](int e) { return nbk <= kNearBlocks ? near_work[e] : v.kblocks[e].nq; },
+            [&](int e, int32_t parts, int32_t slot) {
+                v.kblocks[e].split = parts;
+                v.kblocks[e].slot = slot;
+            },
+            [&](int i, int e, int32_t first, int32_t n, bool part, int32_t which) {
+                const KBlock k = v.kblocks[e];
+                v.kwalks[i] = KWork{k.key0, k.nkeys, k.pos, k.q0 + first, n, part ? k.slot + which : -1, 0, 0};
+            });
+    }
+    if (tid == 0) *v.lists = Lists{nbq, nbk, wq, wk, 0, 0, 0};
 }
 
 }  // namespace
