@@ -415,7 +415,8 @@ typedef struct {
 } sta_packed;
 
 /* Bytes of workspace that sta_packed_forward (backward = 0) or
- * sta_packed_backward (1) needs for this problem (its pointers are not read).
+ * sta_packed_backward (1) needs for this problem (its pointers are not read);
+ * 0 for a small forward, whose workspace may then be NULL.
  * Host only.  INVALID_ARG / UNSUPPORTED as the calls themselves. */
 STA_API sta_status sta_packed_workspace(const sta_packed* p, int32_t backward, int64_t* bytes);
 

@@ -68,6 +68,8 @@ def bind(lib, check) -> None:
 
 
 # ---------------------------------------------------------------- arguments
+# A serving step makes these calls for every layer, and the smallest kernels take a few
+# microseconds: the checks below are written for few Python operations.
 class _on:
     """The device and stream of one call: makes the tensors' device current, and hands the call's
     scratch and outputs to ``stream`` when that is not the current one."""
@@ -79,11 +81,12 @@ class _on:
 
     def __enter__(self):
         self.guard = None
-        if self.device.index != torch.cuda.current_device():
+        index = self.device.index
+        if index != torch._C._cuda_getDevice():
             self.guard = torch.cuda.device(self.device)
             self.guard.__enter__()
         if self.stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(self.device.index)
+            self.handle = torch._C._cuda_getCurrentRawStream(index)
         else:
             if not isinstance(self.stream, torch.cuda.Stream):
                 self.stream = torch.cuda.ExternalStream(int(self.stream), device=self.device)
@@ -101,23 +104,24 @@ class _on:
 
 
 def _rows(name: str, t: torch.Tensor, device, tokens: int, heads: int, d: int) -> _Rows:
-    if t.dtype != torch.bfloat16 or t.device != device:
+    if t.dtype is not torch.bfloat16 or t.device != device:
         raise ValueError(f"{name} must be a bf16 tensor on {device}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != d:
+    if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{tokens}, {heads}, {d}]")
     st, sh, sd = t.stride()
     if heads == 1:
         sh = d
     if tokens <= 1:
         st = heads * d
-    if sd != 1 or st <= 0 or sh <= 0 or st % 8 or sh % 8 or t.data_ptr() % 16:
+    p = t.data_ptr()
+    if sd != 1 or st <= 0 or sh <= 0 or (st | sh) & 7 or p & 15:
         raise ValueError(f"{name}: the last dimension must be contiguous, the other strides positive multiples of 8 "
                          f"elements and the data 16-byte aligned (strides {t.stride()})")
-    return _Rows(t.data_ptr(), st, sh)
+    return _Rows(p, st, sh)
 
 
 def _ints(name: str, t: torch.Tensor, device, size: int | None, dtype=torch.int32) -> int:
-    if t.dtype != dtype or t.device != device or t.dim() != 1 or not t.is_contiguous() or \
+    if t.dtype is not dtype or t.device != device or t.dim() != 1 or not t.is_contiguous() or \
             (size is not None and t.shape[0] != size):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape [{'n' if size is None else size}] on {device}")
     return t.data_ptr()
@@ -146,20 +150,35 @@ def _lse_ptr(lse, q) -> int:
     return lse.data_ptr()
 
 
-def _scratch(bytes_, device):
-    return torch.empty(max(int(bytes_), 256), dtype=torch.uint8, device=device)
+_sizes = {}  # workspace bytes by the sizes that they follow from
 
 
-def _workspace(call, what, workspace, device, *args):
+def _workspace(key, call, what, workspace, device, *args):
     """(tensor, pointer, bytes) of a call's scratch; allocated unless given."""
-    need = ctypes.c_int64(0)
-    _check(call(*args, ctypes.byref(need)), what)
+    need = _sizes.get(key)
+    if need is None:
+        n = ctypes.c_int64(0)
+        _check(call(*args, ctypes.byref(n)), what)
+        if len(_sizes) > 10000:
+            _sizes.clear()
+        need = _sizes[key] = n.value
     if workspace is None:
-        workspace = _scratch(need.value, device)
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-            workspace.numel() < need.value:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need.value} bytes on {device}")
+            workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {device}")
     return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _packed_workspace(p, backward, workspace, device):
+    key = (p.batch, p.heads, p.kv_heads, p.head_dim, p.tokens_q, p.tokens_k, backward, device.index)
+    return _workspace(key, _lib.sta_packed_workspace, "sta_packed_workspace", workspace, device, ctypes.byref(p), backward)
+
+
+def _empty_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 # ---------------------------------------------------------------- packed attention
@@ -181,9 +200,10 @@ def sta_packed_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: tor
                 _rows("o", o, dev, p.tokens_q, p.heads, p.head_dim), _lse_ptr(lse, q))
         if q.shape[0] == 0:
             return o, lse
-        w, wp, wn = _workspace(_lib.sta_packed_workspace, "sta_packed_workspace", workspace, dev, ctypes.byref(p), 0)
+        w, wp, wn = _packed_workspace(p, 0, workspace, dev)
         _check(_lib.sta_packed_forward(*args, wp, wn, on.handle), "sta_packed_forward")
-        on.keep(w)
+        if w is not None:
+            on.keep(w)
     return o, lse
 
 
@@ -203,7 +223,7 @@ def sta_packed_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: to
         lp = _lse_ptr(lse, q)
         if q.shape[0] == 0 and k.shape[0] == 0:
             return dq, dk, dv
-        w, wp, wn = _workspace(_lib.sta_packed_workspace, "sta_packed_workspace", workspace, dev, ctypes.byref(p), 1)
+        w, wp, wn = _packed_workspace(p, 1, workspace, dev)
         _check(_lib.sta_packed_backward(ctypes.byref(p), qs[0], ks[0], ks[1], qs[1], qs[2], lp, qs[3], ks[2], ks[3],
                                         wp, wn, on.handle), "sta_packed_backward")
         on.keep(w)
@@ -215,7 +235,9 @@ def sta_packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
                          stream=None):
     """``sta_packed_forward`` into new tensors; rows behind the last sequence are zeros (``lse`` -inf).
     Returns ``(o bf16 [tokens, heads, d], lse fp32 [heads, tokens])``."""
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, d]")
+    o = _empty_like(q)
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
     sta_packed_forward(q, k, v, o, lse, cu_q, cu_k, causal, softmax_scale, True, None, stream)
     _keep(stream, o, lse)
@@ -227,7 +249,7 @@ def sta_packed_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
                                   cu_k: torch.Tensor | None = None, causal: bool = True,
                                   softmax_scale: float | None = None, stream=None):
     """``sta_packed_backward`` into new tensors ``(dq, dk, dv)``; rows behind the last sequence are zeros."""
-    dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+    dq, dk, dv = _empty_like(q), _empty_like(k), _empty_like(v)
     sta_packed_backward(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, causal, softmax_scale, True, None, stream)
     _keep(stream, dq, dk, dv)
     return dq, dk, dv
@@ -276,14 +298,24 @@ def _cache(k_cache, v_cache, k_scales, v_scales) -> _Cache:
     if k_cache.dim() != 4 or not k_cache.is_cuda:
         raise ValueError("k_cache must be a CUDA tensor [blocks, kv_heads, block_tokens, d]")
     dev, shape = k_cache.device, k_cache.shape
+    blocks, heads, bt, d = shape
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if t.dtype not in _CODES or t.device != dev or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous e4m3 (or uint8) tensor of shape {tuple(shape)} on {dev}")
     for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t.dtype != torch.float32 or t.device != dev or t.shape != shape[:2] or not t.is_contiguous():
+        if t.dtype is not torch.float32 or t.device != dev or t.shape != (blocks, heads) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape[:2])} on {dev}")
-    return _Cache(shape[0], shape[2], shape[1], shape[3], k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-                  v_scales.data_ptr())
+    return _Cache(blocks, bt, heads, d, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
+
+
+def _tables(block_tables, batch, device):
+    """(pointer, width, stride) of the block tables."""
+    width = block_tables.shape[1] if block_tables.dim() == 2 else 0
+    rows, cols = block_tables.stride() if width else (0, 0)
+    if block_tables.dtype is not torch.int32 or block_tables.device != device or width == 0 or \
+            block_tables.shape[0] != batch or (width > 1 and cols != 1) or (batch > 1 and rows < width):
+        raise ValueError(f"block_tables must be an int32 tensor [{batch}, width] on {device} with contiguous rows")
+    return block_tables.data_ptr(), width, rows if batch > 1 else width
 
 
 def sta_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -322,17 +354,13 @@ def sta_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     cp = None if cu_q is None else _ints("cu_q", cu_q, dev, B + 1)
     if cu_q is None and T != B:
         raise ValueError(f"{T} queries for {B} sequences: give cu_q")
-    if block_tables.dtype != torch.int32 or block_tables.device != dev or block_tables.dim() != 2 or \
-            block_tables.shape[0] != B or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1) or \
-            (B > 1 and block_tables.stride(0) < block_tables.shape[1]):
-        raise ValueError(f"block_tables must be an int32 tensor [{B}, width] on {dev} with contiguous rows")
-    width = block_tables.shape[1]
+    tp, width, stride = _tables(block_tables, B, dev)
     new = o is None
     scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
     p = _Packed(B, H, c.kv_heads, d, T, 0, cp, None, 1, 1 if new else 0, scale)
     with _on(dev, stream) as on:
         if new:
-            o = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+            o = _empty_like(q)
             on.keep(o)
         if lse is None:
             lse = torch.empty((H, T), dtype=torch.float32, device=dev)
@@ -343,11 +371,11 @@ def sta_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
             if new:
                 o.zero_(), lse.fill_(-math.inf)
             return o, lse
-        w, wp, wn = _workspace(_lib.sta_cache_workspace, "sta_cache_workspace", workspace, dev, ctypes.byref(c),
+        key = (c.block_tokens, c.kv_heads, d, B, H, T, dev.index)
+        w, wp, wn = _workspace(key, _lib.sta_cache_workspace, "sta_cache_workspace", workspace, dev, ctypes.byref(c),
                                ctypes.byref(p))
-        _check(_lib.sta_cache_attention(ctypes.byref(c), ctypes.byref(p), lp, block_tables.data_ptr(), width,
-                                        block_tables.stride(0) if B > 1 else width, qr, orow, lsp, wp, wn, on.handle),
-               "sta_cache_attention")
+        _check(_lib.sta_cache_attention(ctypes.byref(c), ctypes.byref(p), lp, tp, width, stride, qr, orow, lsp, wp, wn,
+                                        on.handle), "sta_cache_attention")
         on.keep(w)
     return o, lse
 
@@ -374,21 +402,17 @@ def sta_cache_extend(new_tokens: torch.Tensor, lengths: torch.Tensor, block_tabl
     B = lengths.shape[0] if lengths.dim() == 1 else -1
     lp, np_ = _ints("lengths", lengths, dev, None), _ints("new_tokens", new_tokens, dev, B)
     fp, cp = _ints("free_blocks", free_blocks, dev, None), _ints("free_count", free_count, dev, 1)
-    if block_tables.dtype != torch.int32 or block_tables.device != dev or block_tables.dim() != 2 or \
-            block_tables.shape[0] != B or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1) or \
-            (B > 1 and block_tables.stride(0) < block_tables.shape[1]):
-        raise ValueError(f"block_tables must be an int32 tensor [{B}, width] on {dev} with contiguous rows")
-    width, max_slots = block_tables.shape[1], int(max_slots)
+    tp, width, stride = _tables(block_tables, B, dev)
+    max_slots = int(max_slots)
     with _on(dev, stream) as on:
         slots = torch.empty(max(max_slots, 0), dtype=torch.int64, device=dev)
         cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        short = torch.empty(1, dtype=torch.int32, device=dev)
+        short = torch.empty_like(free_count)
         len_out = lengths if in_place else torch.empty_like(lengths)
         count_out = free_count if in_place else torch.empty_like(free_count)
-        _check(_lib.sta_cache_extend(B, int(block_tokens), np_, lp, len_out.data_ptr(), block_tables.data_ptr(), width,
-                                     block_tables.stride(0) if B > 1 else width, fp, free_blocks.shape[0], cp,
-                                     count_out.data_ptr(), slots.data_ptr(), max_slots, cu.data_ptr(), short.data_ptr(),
-                                     on.handle), "sta_cache_extend")
+        _check(_lib.sta_cache_extend(B, int(block_tokens), np_, lp, len_out.data_ptr(), tp, width, stride, fp,
+                                     free_blocks.shape[0], cp, count_out.data_ptr(), slots.data_ptr(), max_slots,
+                                     cu.data_ptr(), short.data_ptr(), on.handle), "sta_cache_extend")
         on.keep(slots, cu, short)
         if not in_place:
             on.keep(len_out, count_out)

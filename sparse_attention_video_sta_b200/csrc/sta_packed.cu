@@ -46,8 +46,16 @@ constexpr int kSBufs = 3;               // S buffers in TMEM
 constexpr float kRescaleRowSum = 65536.0f;
 constexpr int kBoxBytes = 128 * 128;    // 128 rows x 128 bytes
 
+// Small problems need no lists: every CTA finds its (at most kSelfItems) items from the bounds
+// itself, CTA c taking items c, c + grid, ...  That saves a launch and its workspace where
+// the whole call is a few microseconds.
+constexpr int kSelfItems = kItemQ - 1;
+constexpr int kSelfBatch = 32;  // one lane of the load warp for each sequence
+
 struct FwdParams {
     packed::View v;
+    PackedProblem prob;
+    int32_t self;  // no lists
     int32_t kv_heads, group, causal, tokens_q;
     Rows o;
     float* lse;
@@ -150,6 +158,70 @@ struct Cfg {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
+// The items of a CTA from the bounds (one warp): sequence b in lane b, its bounds cut to the
+// tensors and made rising as sta_packed_lists.cu does.
+__device__ void self_items(const PackedProblem& p, QWork* items) {
+    const int lane = threadIdx.x & 31, tpb = 128 / p.group;
+    auto bounds = [&](const int32_t* cu, int32_t tokens, int32_t& from, int32_t& n) {
+        const int32_t c0 = cu[0], c = lane < p.batch ? cu[lane + 1] : INT32_MIN;
+        const int32_t start = max(0, min(c0, tokens));
+        int32_t h = max(start, min(c, tokens));
+        for (int i = 1; i < 32; i <<= 1) {
+            const int32_t y = __shfl_up_sync(~0u, h, i);
+            if (lane >= i) h = max(h, y);
+        }
+        const int32_t y = __shfl_up_sync(~0u, h, 1);
+        from = lane == 0 ? start : y;
+        n = h - from;
+        const bool cut = c0 != start || (lane < p.batch && c != h);
+        if (__any_sync(~0u, cut) && lane == 0 && blockIdx.x == 0) atomicOr(p.status, kDevBounds);
+    };
+    int32_t q0, nq, key0, nk;
+    bounds(p.cu_q, p.tokens_q, q0, nq);
+    bounds(p.cu_k, p.tokens_k, key0, nk);
+    const int32_t mine = (nq + tpb - 1) / tpb;
+    int32_t upto = mine;
+    for (int i = 1; i < 32; i <<= 1) {
+        const int32_t y = __shfl_up_sync(~0u, upto, i);
+        if (lane >= i) upto += y;
+    }
+    const int32_t blocks = __shfl_sync(~0u, upto, 31), first = upto - mine;
+    for (int i = 0; i <= kSelfItems; ++i) {
+        const int32_t u = blockIdx.x + i * gridDim.x;
+        const bool any = i < kSelfItems && u < blocks * p.kv_heads;
+        const int32_t e = any ? blocks - 1 - u / p.kv_heads : 0;  // a causal sequence's last blocks are its longest
+        const int b = 31 - __clz(__ballot_sync(~0u, first <= e && mine > 0) | 1u);
+        const int32_t t = (e - __shfl_sync(~0u, first, b)) * tpb, n = __shfl_sync(~0u, nq, b), m = __shfl_sync(~0u, nk, b);
+        QWork w{};
+        w.tok0 = __shfl_sync(~0u, q0, b) + t;
+        w.ntok = min(tpb, n - t);
+        w.key0 = __shfl_sync(~0u, key0, b);
+        w.nkeys = m;
+        w.limit0 = p.causal ? m - n + t + 1 : m;
+        const int32_t sees = p.causal ? min(m, w.limit0 + w.ntok - 1) : m;
+        w.n = any ? max(1, (sees + 127) / 128) : -1;
+        w.slot = -1;
+        w.hk = u % p.kv_heads;
+        if (lane == 0) items[i] = w;
+    }
+    __syncwarp();
+}
+
+// Zero the rows behind the last sequence (one warp of each CTA).
+__device__ void self_clear(const PackedProblem& p, int head_dim, const Rows& o, float* lse) {
+    const int lane = threadIdx.x & 31;
+    int32_t last = max(0, min(p.cu_q[lane <= p.batch ? lane : 0], p.tokens_q));
+    if (p.batch == kSelfBatch) last = max(last, min(p.cu_q[kSelfBatch], p.tokens_q));
+    last = __reduce_max_sync(~0u, last);
+    const int32_t tail = p.tokens_q - last, parts = head_dim / 8;
+    for (int64_t i = int64_t(blockIdx.x) * 32 + lane; i < int64_t(tail) * p.heads * parts; i += int64_t(gridDim.x) * 32) {
+        const int64_t row = i / parts;
+        const int32_t tok = last + int32_t(row / p.heads), h = int32_t(row % p.heads);
+        *reinterpret_cast<uint4*>(o.p + tok * o.ts + h * o.hs + i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
+        if (i % parts == 0) lse[int64_t(h) * p.tokens_q + tok] = -INFINITY;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -250,9 +322,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
     if (warp == kLoadWarp) {
         ptx::regs_dec<kRegsProducer>();
+        if (p.self) self_items(p.prob, item_q);
         if (lane == 0) {
             // ------------------------------------------------------------ load
-            const int32_t n_items = p.v.lists->w_q * K;
+            const int32_t n_items = p.self ? 0 : p.v.lists->w_q * K;
             uint32_t ring = 0;
             uint32_t q_loads[2] = {0u, 0u};
             bool ok = true;
@@ -272,7 +345,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             // item k + 1 are on their way while item k's copies are issued; where they are few, an
             // item is only taken when the one before is issued, so that longest-first levels the
             // CTAs.  (8192 causal tokens, 24 / 8 heads, d = 128, dK / dV: 730 us late, 905 early.)
-            const bool early = n_items >= 8 * int32_t(gridDim.x);
+            const bool early = !p.self && n_items >= 8 * int32_t(gridDim.x);
             auto next = [&] { return int32_t(gridDim.x) + atomicAdd(&p.v.lists->next_q, 1); };
             auto fetch = [&](int32_t u) {
                 QWork w{};
@@ -284,13 +357,16 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 return w;
             };
             int32_t u2 = early ? next() : 0;
-            QWork w1 = fetch(int32_t(blockIdx.x));
+            QWork w1 = p.self ? item_q[0] : fetch(int32_t(blockIdx.x));
             for (uint32_t k = 0; ok; ++k) {
-                if (!early && k > 0) w1 = fetch(next());
-                const QWork q = w1;
                 const int qe = int(k % kItemQ);
+                if (k > 0 && p.self)
+                    w1 = item_q[qe];  // (the last entry is an end)
+                else if (k > 0 && !early)
+                    w1 = fetch(next());
+                const QWork q = w1;
                 if (k >= uint32_t(kItemQ) && !wait_bar(bar_item_empty(qe), ((k / kItemQ) - 1) & 1u)) break;
-                item_q[qe] = q;
+                if (!p.self) item_q[qe] = q;
                 ptx::mbar_arrive(bar_item_full(qe));
                 if (q.n < 0) break;
                 if (early) {
@@ -321,6 +397,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
     } else if (warp == kTailWarp) {
         ptx::regs_dec<kRegsProducer>();
+        if (p.self && p.prob.clear_tail) self_clear(p.prob, D, p.o, p.lse);
         // ------------------------------------------------------------ V tails
         uint32_t e0 = 0, tails = 0;  // tails, bit r: phase of slot r's v_tail
         for (uint32_t kq = 0;; ++kq) {
@@ -697,26 +774,32 @@ __global__ void __launch_bounds__(256) packed_join_kernel(const FwdParams p) {
 
 template <int D>
 cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, const Rows& v, const Rows& o, float* lse,
-                       const packed::Layout& w, const packed::View& view, cudaStream_t stream) {
+                       const packed::Layout& w, const packed::View& view, bool self, cudaStream_t stream) {
     const int tpb = 128 / p.group;
     CUtensorMap mq, mk, mv;
     cudaError_t e = packed::rows_map(&mq, q, p.tokens_q, p.heads, D, p.group, tpb);
     if (e == cudaSuccess) e = packed::rows_map(&mk, k, p.tokens_k, p.kv_heads, D, 1, 128);
     if (e == cudaSuccess) e = packed::rows_map(&mv, v, p.tokens_k, p.kv_heads, D, 1, 128);
     if (e != cudaSuccess) return e;
-    FwdParams fp{view, p.kv_heads, p.group, p.causal, p.tokens_q, o, lse, p.scale, p.scale * 1.4426950408889634f,
+    FwdParams fp{view, p, self ? 1 : 0, p.kv_heads, p.group, p.causal, p.tokens_q, o, lse, p.scale, p.scale * 1.4426950408889634f,
                  uint32_t(p.group * tpb) * 128u, p.status, kOpTimeoutNs};
     constexpr int kSmem = Cfg<D>::kSmemBytes;
     e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int64_t items = w.max_wq * p.kv_heads;
-    e = packed::launch(packed_fwd_kernel<D>, dim3(unsigned(items < w.sms ? items : w.sms)), kThreads, kSmem, stream, true, mq, mk,
-                       mv, fp);
-    if (e == cudaSuccess && w.split_q) {
+    e = packed::launch(packed_fwd_kernel<D>, dim3(unsigned(items < w.sms ? items : w.sms)), kThreads, kSmem, stream, !self, mq,
+                       mk, mv, fp);
+    if (e == cudaSuccess && !self && w.split_q) {
         const int64_t blocks = w.max_q * p.kv_heads;
         e = packed::launch(packed_join_kernel<D>, dim3(unsigned(blocks), 16), 256, 0, stream, true, fp);  // (fewer than 2 SMs' worth)
     }
     return e;
+}
+
+// Does the forward plan this problem in the kernel?
+bool self_planned(const PackedProblem& p, const packed::Layout& w) {
+    return p.batch > 0 && p.batch <= kSelfBatch && p.tokens_k > 0 && !w.split_q &&
+           w.max_q * p.kv_heads <= int64_t(kSelfItems) * w.sms;
 }
 
 }  // namespace
@@ -764,6 +847,10 @@ cudaError_t launch_packed_forward(const PackedProblem& p, int head_dim, const Ro
     if (cudaError_t e = packed::sm_count(&sms); e != cudaSuccess) return e;
     const packed::Layout w = packed::layout(p, false, head_dim, sms);
     const packed::View view = packed::view(w, workspace);
+    if (self_planned(p, w)) {
+        if (head_dim == 128) return launch_fwd<128>(p, q, k, v, o, lse, w, view, true, stream);
+        return launch_fwd<64>(p, q, k, v, o, lse, w, view, true, stream);
+    }
     packed::Tails tails{};
     tails.r[0] = o;
     tails.heads[0] = p.heads;
@@ -774,8 +861,8 @@ cudaError_t launch_packed_forward(const PackedProblem& p, int head_dim, const Ro
     if (e != cudaSuccess || p.batch == 0) return e;
     if (p.tokens_k == 0)
         return packed::launch(packed_no_keys_kernel, dim3(unsigned(w.sms)), 256, 0, stream, true, p, view, head_dim, o, lse);
-    if (head_dim == 128) return launch_fwd<128>(p, q, k, v, o, lse, w, view, stream);
-    return launch_fwd<64>(p, q, k, v, o, lse, w, view, stream);
+    if (head_dim == 128) return launch_fwd<128>(p, q, k, v, o, lse, w, view, false, stream);
+    return launch_fwd<64>(p, q, k, v, o, lse, w, view, false, stream);
 }
 
 }  // namespace sta
@@ -788,7 +875,8 @@ sta_status sta_packed_workspace(const sta_packed* p, int32_t backward, int64_t* 
     PackedProblem pp;
     if (bytes == nullptr || (backward != 0 && backward != 1)) return STA_ERR_INVALID_ARG;
     if (sta_status st = packed_problem(p, false, &pp); st != STA_OK) return st;
-    *bytes = packed::layout(pp, backward != 0, p->head_dim, packed::sm_count_or_b200()).bytes;
+    const packed::Layout w = packed::layout(pp, backward != 0, p->head_dim, packed::sm_count_or_b200());
+    *bytes = !backward && self_planned(pp, w) ? 0 : w.bytes;
     return STA_OK;
 }
 
@@ -802,7 +890,7 @@ static sta_status packed_buffers(const sta_packed* p, bool backward, PackedProbl
         if (!rows_ok(rows[i], i < n_q ? p->tokens_q : p->tokens_k)) return STA_ERR_INVALID_ARG;
     if (p->tokens_q > 0 && (lse == nullptr || reinterpret_cast<uintptr_t>(lse) % 4 != 0)) return STA_ERR_INVALID_ARG;
     if (p->tokens_q == 0 && (!backward || p->tokens_k == 0)) return STA_OK;  // nothing to do
-    if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < need)
+    if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < need))
         return STA_ERR_INVALID_ARG;
     return STA_OK;
 }

@@ -63,6 +63,7 @@ struct Lists {
 
 constexpr int kSplitParts = 4;  // split walks have at most this many parts to an SM, over all key heads
 constexpr int kMinPart = 4;     // steps of a part
+constexpr int kSplitFrom = 16;  // mean steps of a sequence's longest walk from which splitting is considered
 
 // Offsets into the workspace, from the problem's sizes alone.
 struct Layout {
@@ -86,8 +87,8 @@ inline Layout layout(const PackedProblem& p, bool backward, int head_dim, int sm
     w.sms = sms;
     w.max_q = p.tokens_q / tpb + p.batch;
     w.max_k = backward ? p.tokens_k / kRows + p.batch : 0;
-    // (nothing to gain where the sequences' mean is a few steps: the join would be launched for nothing)
-    const int64_t long_k = int64_t(p.batch) * kMinPart * kRows, long_q = int64_t(p.batch) * kMinPart * tpb;
+    // (nothing to gain where walks are a few steps of a microsecond: the join's launch costs as much)
+    const int64_t long_k = int64_t(p.batch) * kSplitFrom * kRows, long_q = int64_t(p.batch) * kSplitFrom * tpb;
     w.split_q = w.max_q * p.kv_heads < 2 * int64_t(sms) && p.tokens_k > long_k;
     w.split_k = backward && w.max_k * p.kv_heads < 2 * int64_t(sms) && p.tokens_q > long_q;
     const int64_t extra = int64_t(kSplitParts) * sms;

@@ -48,7 +48,7 @@ def test_problem_is_refused(kw, status):
 
 
 def test_packed_buffers_are_refused():
-    L, p, n = sta._lib, packed(), ctypes.c_int64(0)
+    L, p, n = sta._lib, packed(batch=40), ctypes.c_int64(0)  # (a forward of few sequences needs no workspace)
     assert L.sta_packed_workspace(p, 2, ctypes.byref(n)) == INV
     assert L.sta_packed_workspace(p, 0, None) == INV
     assert L.sta_packed_workspace(None, 0, ctypes.byref(n)) == INV
@@ -75,7 +75,9 @@ def test_packed_buffers_are_refused():
         assert f(lse=None) == INV and f(lse=P + 2) == INV
         assert f(ws=None) == INV and f(ws=P + 128) == INV and f(size=size - 1) == INV
         for kw in (dict(cu_q=None), dict(cu_k=None), dict(cu_q=P + 2), dict(cu_k=P + 1)):
-            assert f(p=packed(**kw)) == INV
+            assert f(p=packed(batch=40, **kw)) == INV
+    assert L.sta_packed_workspace(packed(), 0, ctypes.byref(n)) == OK and n.value == 0
+    assert L.sta_packed_workspace(packed(), 1, ctypes.byref(n)) == OK and n.value > 0
     # nothing to do: pointers are not read
     none = rows(data=None)
     assert fwd(q=none, o=none, lse=None, p=packed(tokens_q=0)) == OK
