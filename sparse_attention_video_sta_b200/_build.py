@@ -15,9 +15,10 @@ LIB_PATH = os.path.join(PKG_DIR, "libsta.so")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libsta_debug.so")
 
 SOURCES = ["sta_api.cu", "sta_permute.cu", "sta_forward.cu", "sta_backward.cu", "sta_search.cu", "sta_pipe.cu", "sta_noalloc.cu",
-           "sta_packed_lists.cu", "sta_packed.cu", "sta_packed_backward.cu", "sta_cache.cu", "sta_cache_attention.cu"]
+           "sta_packed_lists.cu", "sta_packed.cu", "sta_packed_pair.cu",
+           "sta_packed_backward.cu", "sta_cache.cu", "sta_cache_attention.cu"]
 HEADERS = ["sta_internal.h", "sta_ptx.cuh", "sta_raster.cuh", "sta_wait.cuh", "sta_bounds.cuh",
-           "sta_ops.h", "sta_ops.cuh", "sta_packed.cuh"]
+           "sta_ops.h", "sta_ops.cuh", "sta_packed.cuh", "sta_packed_fwd.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",

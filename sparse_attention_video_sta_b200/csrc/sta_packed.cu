@@ -14,6 +14,7 @@
 #include "sta_ops.cuh"
 #include "sta_ops.h"
 #include "sta_packed.cuh"
+#include "sta_packed_fwd.cuh"
 #include "sta_ptx.cuh"
 #include "sta_wait.cuh"
 
@@ -22,11 +23,7 @@ namespace {
 
 using packed::QBlock;
 using packed::QWork;
-
-constexpr int kMaxDevices = 64;
-__device__ uint32_t g_op_status;  // one word per device: kDevTimeout | kDevBounds
-std::mutex g_status_mutex;
-uint32_t* g_status_ptr[kMaxDevices] = {};
+using namespace packed_fwd;
 
 constexpr int kThreads = 384;  // 3 warpgroups: softmax half A, softmax half B, producers
 constexpr int kLoadWarp = 8;
@@ -39,77 +36,16 @@ constexpr uint32_t kRegsSoftmax = 208;
 constexpr uint32_t kRegsProducer = 88;
 static_assert(128 * (2 * kRegsSoftmax + kRegsProducer) <= kThreads * 168, "register split exceeds the launch");
 constexpr uint32_t kTmemCols = 512;
-constexpr int kItemQ = 4;               // entries of the item queue in shared memory
 constexpr int kItemConsumers = 3 + 8;   // the issuing threads, the tail warp and the eight softmax warps
 constexpr int kSBufs = 3;               // S buffers in TMEM
 // A half-row sum above this takes the slow path (the running maximum is raised).
 constexpr float kRescaleRowSum = 65536.0f;
-constexpr int kBoxBytes = 128 * 128;    // 128 rows x 128 bytes
 
-// Small problems need no lists: every CTA finds its (at most kSelfItems) items from the bounds
-// itself, CTA c taking items c, c + grid, ...  That saves a launch and its workspace where
-// the whole call is a few microseconds.
-constexpr int kSelfItems = kItemQ - 1;
-constexpr int kSelfBatch = 32;  // one lane of the load warp for each sequence
 
-struct FwdParams {
-    packed::View v;
-    PackedProblem prob;
-    int32_t self;  // no lists
-    int32_t kv_heads, group, causal, tokens_q;
-    Rows o;
-    float* lse;
-    float scale, scale_log2;
-    uint32_t q_box_bytes;  // bytes of one box of a query block: group * (128 / group) rows of 128 bytes
-    uint32_t* status;
-    uint64_t timeout_ns;
-};
-
-// Scores of the 64 keys of a half row from index `n` on to -inf.
-__device__ __forceinline__ void mask_from(uint32_t (&sr)[64], int n) {
-#pragma unroll
-    for (int j = 0; j < 64; ++j)
-        if (j >= n) sr[j] = 0xff800000u;
-}
-
-// P = exp2(S * c - m * c) for one 64-score half row, packed to bf16 pairs; returns
-// the fp32 sum of the unrounded values: LSE is their logarithm, to fp32 accuracy.
-// (P's rounding to bf16, at most 2^-8 relative, is the operand type of P V.)
-__device__ __forceinline__ float softmax_exp64(const uint32_t (&sr)[64], float c, float m, uint32_t (&pk)[32]) {
-    const uint64_t c2 = ptx::f2(c, c);
-    const uint64_t nmc2 = ptx::f2(-m * c, -m * c);
-    uint64_t acc0 = ptx::f2(0.0f, 0.0f), acc1 = acc0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        float x0, x1;
-        ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), c2, nmc2), x0, x1);
-        const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-        pk[j] = ptx::pack_bf16x2(p0, p1);
-        if (j & 1)
-            acc1 = ptx::f2_add(acc1, ptx::f2(p0, p1));
-        else
-            acc0 = ptx::f2_add(acc0, ptx::f2(p0, p1));
-    }
-    float r0, r1, r2, r3;
-    ptx::f2_split(acc0, r0, r1);
-    ptx::f2_split(acc1, r2, r3);
-    return (r0 + r1) + (r2 + r3);
-}
-
-__device__ __forceinline__ float row_max64(const uint32_t (&sr)[64]) {
-    float a0 = __uint_as_float(sr[0]), a1 = __uint_as_float(sr[1]);
-    float a2 = __uint_as_float(sr[2]), a3 = __uint_as_float(sr[3]);
-#pragma unroll
-    for (int j = 4; j < 60; j += 8) {
-        a0 = ptx::max3(a0, __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
-        a1 = ptx::max3(a1, __uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3]));
-        a2 = ptx::max3(a2, __uint_as_float(sr[j + 4]), __uint_as_float(sr[j + 5]));
-        a3 = ptx::max3(a3, __uint_as_float(sr[j + 6]), __uint_as_float(sr[j + 7]));
-    }
-    a0 = ptx::max3(a0, __uint_as_float(sr[60]), __uint_as_float(sr[61]));
-    a1 = ptx::max3(a1, __uint_as_float(sr[62]), __uint_as_float(sr[63]));
-    return ptx::max3(a0, a1, fmaxf(a2, a3));
-}
+constexpr int kMaxDevices = 64;
+__device__ uint32_t g_op_status;  // one word per device: kDevTimeout | kDevBounds
+std::mutex g_status_mutex;
+uint32_t* g_status_ptr[kMaxDevices] = {};
 
 // The forward kernel.  One item is one query block (128 rows: tokens x the query
 // heads of one key head, sta_packed.cuh) of one key head; the pipeline is the
@@ -157,70 +93,6 @@ struct Cfg {
     static_assert(kSBufs * 128 + D <= int(kTmemCols), "TMEM budget");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
-
-// The items of a CTA from the bounds (one warp): sequence b in lane b, its bounds cut to the
-// tensors and made rising as sta_packed_lists.cu does.
-__device__ void self_items(const PackedProblem& p, QWork* items) {
-    const int lane = threadIdx.x & 31, tpb = 128 / p.group;
-    auto bounds = [&](const int32_t* cu, int32_t tokens, int32_t& from, int32_t& n) {
-        const int32_t c0 = cu[0], c = lane < p.batch ? cu[lane + 1] : INT32_MIN;
-        const int32_t start = max(0, min(c0, tokens));
-        int32_t h = max(start, min(c, tokens));
-        for (int i = 1; i < 32; i <<= 1) {
-            const int32_t y = __shfl_up_sync(~0u, h, i);
-            if (lane >= i) h = max(h, y);
-        }
-        const int32_t y = __shfl_up_sync(~0u, h, 1);
-        from = lane == 0 ? start : y;
-        n = h - from;
-        const bool cut = c0 != start || (lane < p.batch && c != h);
-        if (__any_sync(~0u, cut) && lane == 0 && blockIdx.x == 0) atomicOr(p.status, kDevBounds);
-    };
-    int32_t q0, nq, key0, nk;
-    bounds(p.cu_q, p.tokens_q, q0, nq);
-    bounds(p.cu_k, p.tokens_k, key0, nk);
-    const int32_t mine = (nq + tpb - 1) / tpb;
-    int32_t upto = mine;
-    for (int i = 1; i < 32; i <<= 1) {
-        const int32_t y = __shfl_up_sync(~0u, upto, i);
-        if (lane >= i) upto += y;
-    }
-    const int32_t blocks = __shfl_sync(~0u, upto, 31), first = upto - mine;
-    for (int i = 0; i <= kSelfItems; ++i) {
-        const int32_t u = blockIdx.x + i * gridDim.x;
-        const bool any = i < kSelfItems && u < blocks * p.kv_heads;
-        const int32_t e = any ? blocks - 1 - u / p.kv_heads : 0;  // a causal sequence's last blocks are its longest
-        const int b = 31 - __clz(__ballot_sync(~0u, first <= e && mine > 0) | 1u);
-        const int32_t t = (e - __shfl_sync(~0u, first, b)) * tpb, n = __shfl_sync(~0u, nq, b), m = __shfl_sync(~0u, nk, b);
-        QWork w{};
-        w.tok0 = __shfl_sync(~0u, q0, b) + t;
-        w.ntok = min(tpb, n - t);
-        w.key0 = __shfl_sync(~0u, key0, b);
-        w.nkeys = m;
-        w.limit0 = p.causal ? m - n + t + 1 : m;
-        const int32_t sees = p.causal ? min(m, w.limit0 + w.ntok - 1) : m;
-        w.n = any ? max(1, (sees + 127) / 128) : -1;
-        w.slot = -1;
-        w.hk = u % p.kv_heads;
-        if (lane == 0) items[i] = w;
-    }
-    __syncwarp();
-}
-
-// Zero the rows behind the last sequence (one warp of each CTA).
-__device__ void self_clear(const PackedProblem& p, int head_dim, const Rows& o, float* lse) {
-    const int lane = threadIdx.x & 31;
-    int32_t last = max(0, min(p.cu_q[lane <= p.batch ? lane : 0], p.tokens_q));
-    if (p.batch == kSelfBatch) last = max(last, min(p.cu_q[kSelfBatch], p.tokens_q));
-    last = __reduce_max_sync(~0u, last);
-    const int32_t tail = p.tokens_q - last, parts = head_dim / 8;
-    for (int64_t i = int64_t(blockIdx.x) * 32 + lane; i < int64_t(tail) * p.heads * parts; i += int64_t(gridDim.x) * 32) {
-        const int64_t row = i / parts;
-        const int32_t tok = last + int32_t(row / p.heads), h = int32_t(row % p.heads);
-        *reinterpret_cast<uint4*>(o.p + tok * o.ts + h * o.hs + i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
-        if (i % parts == 0) lse[int64_t(h) * p.tokens_q + tok] = -INFINITY;
-    }
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -322,7 +194,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
     if (warp == kLoadWarp) {
         ptx::regs_dec<kRegsProducer>();
-        if (p.self) self_items(p.prob, item_q);
+        if (p.self) self_items(p.prob, item_q, int32_t(blockIdx.x), int32_t(gridDim.x));
         if (lane == 0) {
             // ------------------------------------------------------------ load
             const int32_t n_items = p.self ? 0 : p.v.lists->w_q * K;
@@ -772,6 +644,14 @@ __global__ void __launch_bounds__(256) packed_join_kernel(const FwdParams p) {
     }
 }
 
+// Are the walks short enough for two items at a time (sta_packed_pair.cu)?  By the mean number of
+// keys of a sequence; 16384 tokens, pair / one at a time, us: d = 128, 24 / 8 heads, causal, sequences
+// of 256: 107 / 140, 512: 137 / 152, 1024: 194 / 191, 4096: 537 / 441; 24 / 24 heads, not causal, 512: 169 / 174,
+// 1024: 291 / 263; d = 64, 16 / 2 heads, causal, 1024: 115 / 143, 2048: 189 / 225, 4096: 324 / 323, 8192: 611 / 550.
+bool short_walks(const PackedProblem& p, int head_dim) {
+    return p.tokens_k <= int64_t(p.batch) * (head_dim == 128 ? 768 : 3500);
+}
+
 template <int D>
 cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, const Rows& v, const Rows& o, float* lse,
                        const packed::Layout& w, const packed::View& view, bool self, cudaStream_t stream) {
@@ -784,11 +664,15 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     FwdParams fp{view, p, self ? 1 : 0, p.kv_heads, p.group, p.causal, p.tokens_q, o, lse, p.scale, p.scale * 1.4426950408889634f,
                  uint32_t(p.group * tpb) * 128u, p.status, kOpTimeoutNs};
     constexpr int kSmem = Cfg<D>::kSmemBytes;
-    e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
     const int64_t items = w.max_wq * p.kv_heads;
-    e = packed::launch(packed_fwd_kernel<D>, dim3(unsigned(items < w.sms ? items : w.sms)), kThreads, kSmem, stream, !self, mq,
-                       mk, mv, fp);
+    if (short_walks(p, D)) {
+        e = packed_fwd::launch_forward_pair(D, mq, mk, mv, fp, items, w.sms, !self, stream);
+    } else {
+        e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess)
+            e = packed::launch(packed_fwd_kernel<D>, dim3(unsigned(items < w.sms ? items : w.sms)), kThreads, kSmem, stream,
+                               !self, mq, mk, mv, fp);
+    }
     if (e == cudaSuccess && !self && w.split_q) {
         const int64_t blocks = w.max_q * p.kv_heads;
         e = packed::launch(packed_join_kernel<D>, dim3(unsigned(blocks), 16), 256, 0, stream, true, fp);  // (fewer than 2 SMs' worth)
