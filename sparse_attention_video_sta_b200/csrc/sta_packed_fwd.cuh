@@ -147,6 +147,45 @@ __device__ __forceinline__ void self_clear(const PackedProblem& p, int head_dim,
 }
 
 
+// The same pieces for 32 scores, sr[kAt] .. sr[kAt + 31].
+template <int kAt>
+__device__ __forceinline__ void mask_from32(uint32_t (&sr)[64], int n) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j >= n) sr[kAt + j] = 0xff800000u;
+}
+template <int kAt>
+__device__ __forceinline__ float row_max32(const uint32_t (&sr)[64]) {
+    float a0 = __uint_as_float(sr[kAt]), a1 = __uint_as_float(sr[kAt + 1]);
+#pragma unroll
+    for (int j = 2; j < 30; j += 4) {
+        a0 = ptx::max3(a0, __uint_as_float(sr[kAt + j]), __uint_as_float(sr[kAt + j + 1]));
+        a1 = ptx::max3(a1, __uint_as_float(sr[kAt + j + 2]), __uint_as_float(sr[kAt + j + 3]));
+    }
+    return fmaxf(a0, ptx::max3(a1, __uint_as_float(sr[kAt + 30]), __uint_as_float(sr[kAt + 31])));
+}
+template <int kAt>
+__device__ __forceinline__ float softmax_exp32(const uint32_t (&sr)[64], float c, float m, uint32_t (&pk)[32]) {
+    const uint64_t c2 = ptx::f2(c, c), nmc2 = ptx::f2(-m * c, -m * c);
+    uint64_t acc0 = ptx::f2(0.0f, 0.0f), acc1 = acc0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float x0, x1;
+        ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[kAt + 2 * j]), __uint_as_float(sr[kAt + 2 * j + 1])), c2, nmc2),
+                      x0, x1);
+        const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+        pk[kAt / 2 + j] = ptx::pack_bf16x2(p0, p1);
+        if (j & 1)
+            acc1 = ptx::f2_add(acc1, ptx::f2(p0, p1));
+        else
+            acc0 = ptx::f2_add(acc0, ptx::f2(p0, p1));
+    }
+    float r0, r1, r2, r3;
+    ptx::f2_split(acc0, r0, r1);
+    ptx::f2_split(acc1, r2, r3);
+    return (r0 + r1) + (r2 + r3);
+}
+
 // The kernel for short walks (sta_packed_pair.cu).
 cudaError_t launch_forward_pair(int head_dim, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                 const FwdParams& fp, int64_t items, int sms, bool pdl, cudaStream_t stream);

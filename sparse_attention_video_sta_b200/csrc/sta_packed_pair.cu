@@ -276,7 +276,8 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             if (q.n < 0) break;
             const bool real = r_tok < q.ntok;
             const int limit = real ? min(q.nkeys, q.limit0 + (p.causal ? r_tok : 0)) : INT32_MAX;
-            const int warp_limit = __reduce_min_sync(~0u, limit);  // over the rows that are stored
+            // over the rows that are stored: below `least` nothing is masked, from `most` on everything
+            const int least = __reduce_min_sync(~0u, limit), most = __reduce_max_sync(~0u, real ? limit : INT32_MIN);
             float m = 0.0f, l = 0.0f;
             for (int32_t i = 0; i < q.n; ++i, ++g) {
                 if (!__all_sync(~0u, wait_bar(s_full, g & 1u))) { ok = false; break; }
@@ -297,11 +298,21 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                             *reinterpret_cast<uint4*>(v0 + cb * kBoxBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
                     ptx::fence_proxy_async_smem();
                 }
-                if (key + 128 > warp_limit) {
-                    mask_from(s0, limit - key);
-                    mask_from(s1, limit - key - 64);
+                // 32 keys at a time: masked where some row's limit falls in them, left out where every row's has passed
+                const bool cut = key + 128 > least;
+                float mx;
+                if (!cut) {
+                    mx = fmaxf(row_max64(s0), row_max64(s1));
+                } else {
+                    if (key + 32 > least) mask_from32<0>(s0, limit - key);
+                    if (key + 64 > least) mask_from32<32>(s0, limit - key - 32);
+                    if (key + 96 > least) mask_from32<0>(s1, limit - key - 64);
+                    if (key + 128 > least) mask_from32<32>(s1, limit - key - 96);
+                    mx = row_max32<0>(s0);
+                    if (key + 32 < most) mx = fmaxf(mx, row_max32<32>(s0));
+                    if (key + 64 < most) mx = fmaxf(mx, row_max32<0>(s1));
+                    if (key + 96 < most) mx = fmaxf(mx, row_max32<32>(s1));
                 }
-                const float mx = fmaxf(row_max64(s0), row_max64(s1));
                 float alpha = 1.0f;
                 if (i == 0) {
                     m = mx == -INFINITY ? 0.0f : mx;  // no key: a finite stand-in
@@ -329,9 +340,21 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     }
                 }
                 uint32_t pk[32];
-                l += softmax_exp64(s0, c, m, pk);
-                ptx::tmem_st32(mS, pk);
-                l += softmax_exp64(s1, c, m, pk);
+                if (!cut) {
+                    l += softmax_exp64(s0, c, m, pk);
+                    ptx::tmem_st32(mS, pk);
+                    l += softmax_exp64(s1, c, m, pk);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) pk[j] = 0u;
+                    l += softmax_exp32<0>(s0, c, m, pk);
+                    if (key + 32 < most) l += softmax_exp32<32>(s0, c, m, pk);
+                    ptx::tmem_st32(mS, pk);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) pk[j] = 0u;
+                    if (key + 64 < most) l += softmax_exp32<0>(s1, c, m, pk);
+                    if (key + 96 < most) l += softmax_exp32<32>(s1, c, m, pk);
+                }
                 ptx::tmem_st32(mS + 32, pk);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
