@@ -85,6 +85,7 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b, bool* cu
 
 struct PlanShared {
     int64_t scan[kPlanWarps];
+    int64_t upto[kPlanWarps * 32];  // tiles of the sequences up to and with b (at most 256 sequences)
     int32_t last;     // end of the last sequence's queries
 };
 
@@ -101,25 +102,39 @@ __device__ int64_t plan_total(const CacheArgs& a, PlanShared& sh, bool report) {
             n += int64_t(s.tiles) * s.units;
             last = max(last, s.q0 + s.nq);
         }
-        for (int i = 16; i > 0; i >>= 1) {
-            n += __shfl_xor_sync(~0u, n, i);
-            last = max(last, __shfl_xor_sync(~0u, last, i));
+        const int lane = threadIdx.x & 31;
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, n, i);
+            if (lane >= i) n += y;
         }
-        if (threadIdx.x % 32 == 0) {
+        last = __reduce_max_sync(~0u, last);
+        if (lane == 31) {
             sh.scan[threadIdx.x / 32] = n;
             atomicMax(&sh.last, last);
         }
     }
     if (__syncthreads_or(cut) && report && threadIdx.x == 0) atomicOr(a.p.status, kDevBounds);
-    n = 0;
-    for (int i = 0; i < kPlanWarps; ++i) n += sh.scan[i];
+    int64_t total = 0;
+    for (int i = 0; i < kPlanWarps; ++i) {
+        if (i < int(threadIdx.x / 32)) n += sh.scan[i];
+        total += sh.scan[i];
+    }
+    if (threadIdx.x < kPlanWarps * 32) sh.upto[threadIdx.x] = n;
     __syncthreads();
-    return n;
+    return total;
 }
 
 // The sequence that holds tile `at`, and the tiles before it (one warp).
-__device__ int32_t plan_locate(const CacheArgs& a, int64_t at, int64_t* before) {
+__device__ int32_t plan_locate(const CacheArgs& a, const PlanShared& sh, int64_t at, int64_t* before) {
     const int lane = threadIdx.x & 31;
+    if (a.p.batch <= kPlanWarps * 32)
+        for (int b0 = 0;; b0 += 32) {  // (upto does not fall, and its last is the total)
+            const uint32_t past = __ballot_sync(~0u, sh.upto[b0 + lane] > at);
+            if (past == 0u) continue;
+            const int b = b0 + __ffs(past) - 1;
+            *before = b == 0 ? 0 : sh.upto[b - 1];
+            return b;
+        }
     int64_t carry = 0;
     for (int b0 = 0;; b0 += 32) {
         bool cut = false;
@@ -246,14 +261,14 @@ __device__ __forceinline__ void join_row(int64_t s, int64_t n, int share, const 
 template <int D, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;
-    // O^T and Q^T take (D / 4 + D / 8) * NT registers: 16 warps of 128 where that is at most 48
-    static constexpr int kWarps = NT * D <= 128 ? 16 : 8;
+    // O^T and Q^T take (D / 4 + D / 8) * NT registers: 12 warps of up to 168 where that is at most 48
+    // (16 warps of 128 spill and take as long)
+    static constexpr int kWarps = NT * D <= 128 ? 12 : 8;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kTileBytes = kTile * D;  // of K or V
     static constexpr int kStages = 192 * 1024 / (kWarps * 2 * kTileBytes) < 8 ? 192 * 1024 / (kWarps * 2 * kTileBytes) : 8;
     static constexpr int kRing = kWarps * kStages * 2 * kTileBytes;
-    static constexpr int kMetaOff = kRing;                           // {ks, lv} for each warp and stage
-    static constexpr int kBarOff = kMetaOff + kWarps * kStages * 8;
+    static constexpr int kBarOff = kRing;
     static constexpr int kSmem = kBarOff + kWarps * kStages * 8 + 1024;
     static_assert(kSmem <= 224 * 1024, "shared memory budget");
 };
@@ -273,7 +288,6 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     uint8_t* smem = smem_raw + (base - raw_base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int K = a.p.kv_heads, G = a.p.group;
-    float2* meta = reinterpret_cast<float2*>(smem + C::kMetaOff) + warp * S;
     const uint32_t bar0 = base + C::kBarOff + warp * S * 8;
     uint8_t* ring = smem + warp * S * 2 * C::kTileBytes;
     if (lane == 0) {
@@ -309,7 +323,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     __syncwarp();
     float* my_parts = a.warp_parts + (int64_t(blockIdx.x) * kWarps + warp) * 2 * kRows * (D + 4);
     int64_t at = begin, before = 0;
-    int32_t b = at < end ? plan_locate(a, at, &before) : 0;
+    int32_t b = at < end ? plan_locate(a, plan, at, &before) : 0;
     uint32_t slot_in = 0, slot_out = 0, phase = 0;  // this warp's ring: next slot to fill, to read, its phase
     uint32_t in_flight = 0;
     bool dead = false;
@@ -333,31 +347,30 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         auto limit_of = [&](int r) { return min(sq.len, sq.raw - sq.nq + (rt * kRows + r) / G + 1); };
         const int least = limit_of(0);  // the smallest limit of the rows
 
-        // ---- pages: lane i holds page `p0 + i` of the warp's run
+        // ---- pages: lane i holds page `p0 + i` of the warp's run; the copies run ahead of the tiles, so the
+        // tiles' scales have a window of their own (and the copies do not wait for them)
         const int pages = (min(sq.len, t1 * kTile) + a.bt - 1) >> a.bt_log2;
         const int32_t* table = a.tables + int64_t(b) * a.stride;
-        int p0 = -32, page_row = 0;
-        float page_ks = 0.0f, page_lv = 0.0f;  // ks < 0: not to be seen
-        auto load_pages = [&](int from) {
-            p0 = from;
+        auto page = [&](int from, bool report) {  // block of page from + lane; -1: none, or not in the pool
             const int j = from + lane;
-            int id = j < pages ? table[j] : 0;
-            const bool bad = id < 0 || id >= a.blocks;
-            if (bad) {
-                atomicOr(a.p.status, kDevBounds);
-                id = 0;
+            int id = j < pages ? table[j] : -1;
+            if (j < pages && (id < 0 || id >= a.blocks)) {
+                if (report) atomicOr(a.p.status, kDevBounds);
+                id = -1;
             }
-            page_row = (id * K + hk) << a.bt_log2;  // of the tensor maps
-            page_ks = j < pages && !bad ? a.k_scales[int64_t(id) * K + hk] : -1.0f;
-            page_lv = j < pages && !bad ? log2f(a.v_scales[int64_t(id) * K + hk]) : 0.0f;
+            return id;
         };
+        int p0 = t0 * kTile >> a.bt_log2, s0 = p0;
+        const int id0 = page(p0, true);
+        int page_row = (max(id0, 0) * K + hk) << a.bt_log2;  // of the tensor maps; nothing is seen of a page that is not
         auto issue = [&](int tile) {
             const int tok = tile * kTile, pg = tok >> a.bt_log2;
-            if (pg >= p0 + 32) load_pages(pg);
+            if (pg >= p0 + 32) {
+                p0 = pg;
+                page_row = (max(page(pg, true), 0) * K + hk) << a.bt_log2;
+            }
             const int row = __shfl_sync(~0u, page_row, pg - p0) + (tok & (a.bt - 1));
-            const float ks = __shfl_sync(~0u, page_ks, pg - p0), lv = __shfl_sync(~0u, page_lv, pg - p0);
             if (lane == 0) {
-                meta[slot_in] = make_float2(ks, lv);
                 const uint32_t bar = bar0 + 8u * slot_in, dst = ptx::smem_u32(ring + slot_in * 2 * C::kTileBytes);
                 ptx::mbar_arrive_expect_tx(bar, 2 * C::kTileBytes);
                 ptx::tma_load_2d(dst, &tm_k, bar, 0, row);
@@ -366,6 +379,26 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             slot_in = slot_in + 1 == S ? 0 : slot_in + 1;
             ++in_flight;
         };
+        float page_ks, page_lv;  // ks < 0: not to be seen
+        auto load_scales = [&](int id) {
+            page_ks = id >= 0 ? a.k_scales[int64_t(id) * K + hk] : -1.0f;
+            page_lv = id >= 0 ? a.v_scales[int64_t(id) * K + hk] : 1.0f;  // (its logarithm is taken when it is here)
+        };
+        // the queries' loads go out first, the first copies while they are on their way
+        uint4 q_raw[NT][D / 32];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g, row = rt * kRows + r;
+            const bool have = r < rows;
+            const __nv_bfloat16* src =
+                a.q.p + int64_t(sq.q0 + (have ? row / G : 0)) * a.q.ts + (hk * G + (have ? row % G : 0)) * a.q.hs;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                q_raw[nt][i] = make_uint4(0u, 0u, 0u, 0u);
+                if (have) q_raw[nt][i] = __ldg(reinterpret_cast<const uint4*>(src + (t + 4 * (i >> 1)) * 16 + (i & 1) * 8));
+            }
+        }
+        load_scales(id0);
         int next = t0;
         for (; next < t1 && next < t0 + S; ++next) issue(next);
 
@@ -375,23 +408,15 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         int limit[NT][2];   // keys that they see
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + g, row = rt * kRows + r;
-            const bool have = r < rows;
-            const __nv_bfloat16* src =
-                a.q.p + int64_t(sq.q0 + (have ? row / G : 0)) * a.q.ts + (hk * G + (have ? row % G : 0)) * a.q.hs;
             uint32_t raw[D / 8];
             float top = 0.0f;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                    if (have) u = __ldg(reinterpret_cast<const uint4*>(src + (t + 4 * c) * 16 + hh * 8));
-                    raw[c * 8 + hh * 4 + 0] = u.x;
-                    raw[c * 8 + hh * 4 + 1] = u.y;
-                    raw[c * 8 + hh * 4 + 2] = u.z;
-                    raw[c * 8 + hh * 4 + 3] = u.w;
-                }
+            for (int i = 0; i < D / 32; ++i) {
+                raw[4 * i + 0] = q_raw[nt][i].x;
+                raw[4 * i + 1] = q_raw[nt][i].y;
+                raw[4 * i + 2] = q_raw[nt][i].z;
+                raw[4 * i + 3] = q_raw[nt][i].w;
+            }
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf_lo(raw[i])), fabsf(bf_hi(raw[i]))));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
@@ -412,6 +437,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             }
         }
 
+        page_lv = log2f(page_lv);
         float o[NT][kSteps][4];
         float m[NT][2], mw[NT][2], l[NT][2], f[NT][2];  // of rows 2t, 2t + 1; f = 2^(m + lv - mw)
         float lv_now = 0.0f;                            // the lv that f holds for
@@ -442,7 +468,6 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     break;
                 }
             }
-            const float2 mt = meta[slot_out];
             const uint8_t* kt = ring + slot_out * 2 * C::kTileBytes;
             const uint8_t* vt = kt + C::kTileBytes;
             // ---- S^T = K Q^T (two sums over the k-steps, for a shorter chain)
@@ -468,7 +493,15 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 }
             }
             // ---- scores in units of log2 (tokens g, g + 8; rows 2t, 2t + 1); masks
-            const int tok = tile * kTile;
+            const int tok = tile * kTile, pg = tok >> a.bt_log2;
+            if (pg >= s0 + 32) {
+                s0 = pg;
+                load_scales(page(pg, false));
+                page_lv = log2f(page_lv);
+            }
+            float2 mt;
+            mt.x = __shfl_sync(~0u, page_ks, pg - s0);
+            mt.y = __shfl_sync(~0u, page_lv, pg - s0);
             const bool masked = tok + kTile > least || mt.x < 0.0f;
             bool rise = false;
             float x[NT][2];
@@ -611,14 +644,18 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     if (__syncthreads_or(dead)) return;
     // (one warp for each row of each such unit)
     const float* parts0 = a.warp_parts + int64_t(blockIdx.x) * kWarps * 2 * kRows * (D + 4);
+    // lane i < 16: does warp i's run begin inside of a unit, does it leave one unfinished
+    const int64_t began = lane < warps ? ends[lane][0].unit0 : -1, left = lane < warps ? ends[lane][1].unit0 : -1;
+    const uint32_t starts = __ballot_sync(~0u, left >= 0) << 1 | (__shfl_sync(~0u, began, 0) >= 0 ? 1u : 0u);
     int turn = 0;
-    for (int w = -1; w < warps; ++w) {
-        const bool early = w < 0;  // the unit began in an earlier CTA's run
+    for (uint32_t todo = starts; todo != 0u; todo &= todo - 1) {
+        const int w = __ffs(todo) - 2;  // -1: the unit that the CTA's run begins inside of
+        const bool early = w < 0;
         const Unit u = early ? ends[0][0] : ends[w][1];
-        if (u.unit0 < 0) continue;
         const int w0 = early ? 0 : w;
-        int w1 = w0 + 1;
-        while (w1 < warps && ends[w1][0].unit0 == u.unit0) ++w1;
+        // the following runs that begin inside of the same unit
+        const uint32_t same = __ballot_sync(~0u, began == u.unit0) >> (w0 + 1);
+        const int w1 = w0 + __ffs(~same);
         const bool done = !early && u.unit1 <= cta_end;
         for (int r = 0; r < u.rows; ++r, ++turn) {
             if (turn % kWarps != warp) continue;
@@ -770,7 +807,7 @@ sta_status sta_cache_workspace(const sta_cache* c, const sta_packed* p, int64_t*
     if (bytes == nullptr) return STA_ERR_INVALID_ARG;
     if (sta_status st = cache_problem(c, p, false, &pp); st != STA_OK) return st;
     const int sms = packed::sm_count_or_b200();
-    // parts of an SM: its warps' (16 of 8 rows, 8 of 16; d = 64 also 16 of 16, 8 of 32) and its own
+    // parts of an SM: its warps' (12 of 8 rows, 8 of 16; d = 64 also 12 of 16, 8 of 32) and its own
     const int64_t rows = (c->head_dim == 128 ? 128 + 16 : 256 + 32) * 2;
     *bytes = sms * (rows * (c->head_dim + 4) * 4 + int64_t(sizeof(Unit))) + 16;
     return STA_OK;
