@@ -246,8 +246,8 @@ __device__ __forceinline__ void join_row(int64_t s, int64_t n, int share, const 
 // Attention over the cache, transposed: S^T = K Q^T and O^T += V^T W^T by mma.m16n8k16, tokens
 // (then columns of V) as the 16 rows of an operand, 8 query rows as the columns.  A unit of 8
 // rows (NT = 1: one token of up to 8 heads to a key head) then takes half the products and
-// half the registers that rows-by-tokens would, and more rows (NT = 2, 4) share one widening
-// of the codes.  Operands are fp16 (the codes exactly, by cvt in registers: no widened copy
+// half the registers that rows-by-tokens would, and 16 rows (NT = 2) share one widening of the
+// codes.  Operands are fp16 (the codes exactly, by cvt in registers: no widened copy
 // anywhere), sums fp32.  Both products choose their summed index's order freely: K's 16 bytes
 // of a thread are four k-steps, V's 16 bytes of two tokens are eight 2-row pieces of V^T after
 // a byte interleave, and W^T is one movmatrix from S^T.
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
     const int64_t n = lo - i + 1;
     int share = 1;
     while (2 * share * u.rows <= kJoinWarps && 4 * share <= n) share *= 2;
-    const int r = warp / share, s = warp % share;  // (units have at most 32 rows)
+    const int r = warp / share, s = warp % share;  // (units have at most 16 rows)
     float x[E], m, l, mw;
     if (r < u.rows) {
         join_row<D>(s, n, share, [&](int64_t c) {
@@ -769,13 +769,13 @@ cudaError_t launch_attention(const sta_cache& c, CacheArgs a, int sms, cudaStrea
 }
 
 // Query rows of a unit, from the mean number of rows that a sequence has (its own are known
-// on the device only): units of more rows widen the codes once for all of them.
+// on the device only): units of 16 rows widen the codes once for both halves.  (Units of 32
+// leave 8 warps of 250 registers: 7 requests of 3000-30000 tokens with 1-6 drafted ones,
+// 16 / 2 heads, d = 64, take 54 us, units of 16 take 41.)
 template <int D>
 cudaError_t launch_attention(const sta_cache& c, const CacheArgs& a, int sms, cudaStream_t stream) {
     const int64_t rows = int64_t(a.p.tokens_q) * a.p.group / a.p.batch;
-    if (rows <= 8) return launch_attention<D, 1>(c, a, sms, stream);
-    if (rows <= 16 || D == 128) return launch_attention<D, 2>(c, a, sms, stream);
-    return launch_attention<D, D == 64 ? 4 : 2>(c, a, sms, stream);
+    return rows <= 8 ? launch_attention<D, 1>(c, a, sms, stream) : launch_attention<D, 2>(c, a, sms, stream);
 }
 
 // Checks of the cache and the problem together.
@@ -807,8 +807,8 @@ sta_status sta_cache_workspace(const sta_cache* c, const sta_packed* p, int64_t*
     if (bytes == nullptr) return STA_ERR_INVALID_ARG;
     if (sta_status st = cache_problem(c, p, false, &pp); st != STA_OK) return st;
     const int sms = packed::sm_count_or_b200();
-    // parts of an SM: its warps' (12 of 8 rows, 8 of 16; d = 64 also 12 of 16, 8 of 32) and its own
-    const int64_t rows = (c->head_dim == 128 ? 128 + 16 : 256 + 32) * 2;
+    // parts of an SM: its warps' (12 of 8 rows, 8 of 16; d = 64: 12 of 16) and its own
+    const int64_t rows = (c->head_dim == 128 ? 128 + 16 : 192 + 16) * 2;
     *bytes = sms * (rows * (c->head_dim + 4) * 4 + int64_t(sizeof(Unit))) + 16;
     return STA_OK;
 }
