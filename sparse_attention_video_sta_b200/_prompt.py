@@ -284,6 +284,7 @@ class StaPackedAttention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
         dq, dk, dv = sta_packed_attention_backward(q, k, v, o, lse, _usable(dout), cu_q, cu_k, ctx.causal, ctx.scale)

@@ -367,12 +367,11 @@ sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* 
                             int32_t* lengths_out, int32_t* block_tables, int32_t table_width, int64_t table_stride,
                             int32_t* free_blocks, int32_t pool, const int32_t* free_count, int32_t* free_count_out,
                             int64_t* slots, int64_t max_slots, int32_t* cu_new, int32_t* shortage, void* stream) {
-    if (batch < 1 || table_width < 1 || table_stride < table_width || pool < 1 || max_slots < 0 || block_tokens < 1)
+    if (batch < 0 || table_width < 1 || table_stride < table_width || pool < 1 || max_slots < 0 || block_tokens < 1)
         return STA_ERR_INVALID_ARG;
-    for (const void* p : {(const void*)new_tokens, (const void*)lengths, (const void*)lengths_out,
-                          (const void*)block_tables, (const void*)free_blocks, (const void*)free_count,
-                          (const void*)free_count_out, (const void*)cu_new, (const void*)shortage})
-        if (p == nullptr || reinterpret_cast<uintptr_t>(p) % 4 != 0) return STA_ERR_INVALID_ARG;
+    auto bad = [](const void* p) { return p == nullptr || reinterpret_cast<uintptr_t>(p) % 4 != 0; };
+    if (batch > 0 && (bad(new_tokens) || bad(lengths) || bad(lengths_out) || bad(block_tables))) return STA_ERR_INVALID_ARG;
+    if (bad(free_blocks) || bad(free_count) || bad(free_count_out) || bad(cu_new) || bad(shortage)) return STA_ERR_INVALID_ARG;
     if (max_slots > 0 && (slots == nullptr || reinterpret_cast<uintptr_t>(slots) % 8 != 0)) return STA_ERR_INVALID_ARG;
     if (batch > kMaxRequests || (block_tokens != 16 && block_tokens != 32 && block_tokens != 64 && block_tokens != 128))
         return STA_ERR_UNSUPPORTED;

@@ -363,6 +363,57 @@ def test_rows_behind_the_last_query_stay(sta):
     assert torch.equal(o2[:5], o[:5]) and not bool(o2[5:].any()) and bool((lse2[:, 5:] == -math.inf).all())
 
 
+def test_pool_past_32_bits(sta):
+    """A pool whose codes pass 2^32 bytes: append and attention in its last blocks."""
+    bt, K, d, blocks = 128, 4, 128, (1 << 32) // (128 * 4 * 128) + 9
+    kc, vc = (torch.empty(blocks, K, bt, d, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones(blocks, K, device="cuda") for _ in range(2))
+    n = 300
+    ids = torch.tensor([[blocks - 1, blocks - 4, blocks - 2]], dtype=torch.int32, device="cuda")
+    low = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    kv = torch.randn(n, 2 * K, d, generator=torch.Generator("cuda").manual_seed(4), device="cuda").bfloat16()
+    q = torch.randn(1, 8, d, device="cuda").bfloat16()
+    lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = []
+    for table in (ids, low):
+        sta.sta_cache_append(kv[:, :K], kv[:, K:], slots_for(table[0], 0, n, bt), kc, vc, ks, vs)
+        out.append(sta.sta_cache_attention(q, kc, vc, ks, vs, table, lengths))
+    assert sta.sta_operator_status() == 0
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1]) and bool(out[0][0].any())
+
+
+def test_empty_calls(sta):
+    kc, vc, ks, vs = empty_cache(4, 2, 16, 64)
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    free, count = torch.arange(4, dtype=torch.int32, device="cuda"), torch.tensor([3], dtype=torch.int32, device="cuda")
+    s = sta.sta_cache_extend(e, e, torch.empty(0, 5, dtype=torch.int32, device="cuda"), free, count, 16, 3)
+    assert s.slots.tolist() == [-1] * 3 and s.cu_new.tolist() == [0] and int(s.free_count) == 3 and int(s.short) == 0
+    x = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    sta.sta_cache_append(x, x, torch.empty(0, dtype=torch.int64, device="cuda"), kc, vc, ks, vs)
+    o, lse = sta.sta_cache_attention(torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), kc, vc, ks, vs,
+                                     torch.empty(0, 5, dtype=torch.int32, device="cuda"), e)
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    # queries behind no sequence at all
+    q = torch.ones(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = sta.sta_cache_attention(q, kc, vc, ks, vs, torch.empty(0, 5, dtype=torch.int32, device="cuda"), e,
+                                     cu_q=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert not bool(o.any()) and bool((lse == -math.inf).all())
+
+
+def test_many_requests(sta):
+    """More requests than one pass of the lengths takes, with and without queries of their own."""
+    r = random.Random(2)
+    lengths = [r.randint(0, 90) for _ in range(700)]
+    lens_q = [min(n, r.choice([0, 1, 1, 2])) for n in lengths]
+    kc, vc, ks, vs, table = filled_cache(lengths, 1, 16, 64, seed=9)
+    q = torch.randn(sum(lens_q), 4, 64, generator=torch.Generator("cuda").manual_seed(1), device="cuda").bfloat16()
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    want = attention_reference(q, kc, vc, ks, vs, table, lengths, lens_q, 0.125, 16)
+    o, lse = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n, cu_q=ref.cu_of(lens_q))
+    ref.check(o, want, "o")
+    ref.check(lse, want, "lse")
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("H,K,d,bt", [(6, 2, 128, 16), (8, 1, 64, 64)])
 def test_serving_prompts_and_tokens(sta, H, K, d, bt):

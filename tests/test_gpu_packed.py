@@ -326,3 +326,95 @@ def test_bounds_that_do_not_fit_are_cut_and_reported(sta, cu_q, cu_k):
     assert sta.sta_operator_status() == sta.STA_ERR_BOUNDS
     assert sta.sta_operator_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_no_sequences_clear_every_row(sta):
+    q, k, v, do = make([5], [7], 4, 2, 64)
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = sta.sta_packed_attention(q, k, v, cu)
+    assert not bool(o.any()) and bool((lse == -math.inf).all())
+    for t in sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu):
+        assert not bool(t.any())
+    assert sta.sta_operator_status() == 0
+
+
+@pytest.mark.parametrize("lens_q,lens_k,heads,kv_heads,d,causal", [
+    ([5], [9000], 2, 1, 64, True), ([40, 1], [4100, 6000], 6, 2, 128, True), ([3000], [130], 4, 1, 128, False),
+    ([2300], [2300], 8, 1, 64, True), ([1500, 60], [3000, 2900], 3, 1, 128, False)])
+def test_long_walks_are_split_and_joined(sta, lens_q, lens_k, heads, kv_heads, d, causal):
+    """Few blocks with long walks, over keys (forward, dQ) and over queries (dK, dV): split into parts."""
+    q, k, v, do = make(lens_q, lens_k, heads, kv_heads, d, seed=21)
+    k[::5] *= 2
+    cq, ck, scale = ref.cu_of(lens_q), ref.cu_of(lens_k), 0.15
+    want = ref.packed(q, k, v, lens_q, lens_k, causal, scale, do)
+    o, lse = sta.sta_packed_attention(q, k, v, cq, ck, causal=causal, softmax_scale=scale)
+    grads = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cq, ck, causal=causal, softmax_scale=scale)
+    assert sta.sta_operator_status() == 0
+    for name, t in zip(("o", "lse", "dq", "dk", "dv"), (o, lse) + grads):
+        ref.check(t, want, name)
+
+
+def test_offsets_past_32_bits(sta):
+    """Rows 2^27 elements apart: byte and element offsets past 2^32 and 2^31, in every tensor."""
+    n, H, d, apart = 40, 2, 64, 1 << 27
+    big = torch.empty((n - 1) * apart + 8 * H * d, dtype=torch.bfloat16, device="cuda")
+
+    def rows(i):
+        return big[i * H * d:].as_strided((n, H, d), (apart, d, 1))
+    small = make([n], [n], H, H, d, seed=15)
+    q, k, v, do, o, dq, dk, dv = (rows(i) for i in range(8))
+    for a, b in zip((q, k, v, do), small):
+        a.copy_(b)
+    cu = ref.cu_of([n])
+    want_o, want_lse = sta.sta_packed_attention(*small[:3], cu)
+    want = sta.sta_packed_attention_backward(*small[:3], want_o, want_lse, small[3], cu)
+    lse = torch.empty_like(want_lse)
+    sta.sta_packed_forward(q, k, v, o, lse, cu)
+    sta.sta_packed_backward(q, k, v, o, lse, do, dq, dk, dv, cu)
+    assert torch.equal(o, want_o) and torch.equal(lse, want_lse)
+    assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), want))
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing of the calls' first-time set-up breaks a capture: a fresh process captures before it has
+    made any call, and the replay gives the eager bits."""
+    code = """
+import torch, sys
+sys.path.insert(0, "tests")
+import sparse_attention_video_sta_b200 as sta
+import prompt_ref as ref
+torch.manual_seed(0)
+lens = [300, 77] * 20
+q, k, v, do = (torch.randn(sum(lens), h, 64, device="cuda").bfloat16() for h in (4, 2, 2, 4))
+cu = ref.cu_of(lens)
+table = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20)
+codes = [torch.zeros(40, 2, 16, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+scales = [torch.ones(40, 2, device="cuda") for _ in range(2)]
+n = torch.tensor([9, 300], dtype=torch.int32, device="cuda")
+one = torch.ones(2, dtype=torch.int32, device="cuda")
+free, count = torch.arange(8, dtype=torch.int32, device="cuda"), torch.tensor([8], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+def run():
+    o, lse = sta.sta_packed_attention(q, k, v, cu)
+    g = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu)
+    s = sta.sta_cache_extend(one, n, table.clone(), free.clone(), count, 16, 2)
+    sta.sta_cache_append(k[:2], v[:2], s.slots, *codes, *scales)
+    return (o, lse) + g + sta.sta_cache_attention(q[:2], *codes, *scales, table, n)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+want = run()
+assert all(torch.equal(a, b) for a, b in zip(got, want)), [torch.equal(a, b) for a, b in zip(got, want)]
+assert sta.sta_operator_status() == 0
+del graph
+print("fine")
+"""
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-3000:]

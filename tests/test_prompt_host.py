@@ -123,7 +123,7 @@ def test_cache_calls_are_refused():
 def test_extend_is_refused():
     def ext(batch=2, bt=16, new=P, ln=P, lo=P, t=P, w=4, st=4, f=P, pool=8, c=P, co=P, s=P, ms=5, cu=P, sh=P):
         return sta._lib.sta_cache_extend(batch, bt, new, ln, lo, t, w, st, f, pool, c, co, s, ms, cu, sh, None)
-    for kw in (dict(batch=0), dict(bt=0), dict(w=0), dict(st=3), dict(pool=0), dict(ms=-1), dict(s=None), dict(s=P + 4),
+    for kw in (dict(batch=-1), dict(bt=0), dict(w=0), dict(st=3), dict(pool=0), dict(ms=-1), dict(s=None), dict(s=P + 4),
                dict(new=None), dict(ln=None), dict(lo=None), dict(t=None), dict(f=None), dict(c=None), dict(co=None),
                dict(cu=None), dict(sh=None), dict(ln=P + 2)):
         assert ext(**kw) == INV, kw
