@@ -51,7 +51,7 @@ __device__ uint2 codes8(const float (&x)[8]) {
 // is read once: 128 threads hold a block of 128 tokens x 128 in 64 registers.
 // Bound by HBM: 2 bytes read and 1 written for each value.
 template <int D, int BT>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, D * BT <= 8192 ? 8 : 4)
 cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* __restrict__ slots, int range,
                     uint32_t* status) {
     constexpr int kPer = D / 8;                          // threads for one token
