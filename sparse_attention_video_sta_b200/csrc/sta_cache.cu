@@ -185,7 +185,7 @@ constexpr int kExtendCluster = 8;
 constexpr int kMaxRequests = 8192;
 
 struct ExtendParams {
-    int32_t batch, bt, width, pool;
+    int32_t batch, bt, bt_log2, width, pool;
     int64_t stride, max_slots;
     const int32_t* add;
     const int32_t* len;
@@ -297,23 +297,35 @@ __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const Exte
                 p.tables[b * p.stride + held + j] = p.free_blocks[there - 1 - s_need[b] - j];
         }
     const int32_t n_new = fine ? s_cu[B] : 0;
-    for (int64_t t = rank * kExtendThreads + tid; t < p.max_slots; t += size * kExtendThreads) {
-        int64_t slot = -1;
-        if (t < n_new) {
-            int lo = 0, hi = B - 1;  // the last request whose tokens begin at or before t
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (s_cu[mid] <= t)
-                    lo = mid;
+    // four slots to a thread: one search, four table entries on their way at once
+    for (int64_t t0 = (rank * kExtendThreads + tid) * 4; t0 < p.max_slots; t0 += size * kExtendThreads * 4) {
+        int b = 0;
+        if (t0 < n_new) {
+            int hi = B - 1;  // the last request whose tokens begin at or before t0
+            while (b < hi) {
+                const int mid = (b + hi + 1) / 2;
+                if (s_cu[mid] <= t0)
+                    b = mid;
                 else
                     hi = mid - 1;
             }
-            const int held = (s_len[lo] + p.bt - 1) / p.bt, pos = s_len[lo] + int(t - s_cu[lo]), j = pos / p.bt;
-            const int32_t blk = j < held ? p.tables[lo * p.stride + j]
-                                         : p.free_blocks[there - 1 - s_need[lo] - (j - held)];
-            if (blk >= 0 && blk < p.pool) slot = int64_t(blk) * p.bt + pos % p.bt;
         }
-        p.slots[t] = slot;
+        int32_t blk[4], off[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            blk[i] = -1;
+            off[i] = 0;
+            if (t0 + i < n_new) {
+                while (b < B - 1 && s_cu[b + 1] <= t0 + i) ++b;
+                const int held = (s_len[b] + p.bt - 1) >> p.bt_log2, pos = s_len[b] + int(t0 + i - s_cu[b]), j = pos >> p.bt_log2;
+                blk[i] = j < held ? p.tables[b * p.stride + j] : p.free_blocks[there - 1 - s_need[b] - (j - held)];
+                off[i] = pos & (p.bt - 1);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t0 + i < p.max_slots)
+                p.slots[t0 + i] = blk[i] >= 0 && blk[i] < p.pool ? int64_t(blk[i]) * p.bt + off[i] : -1;
     }
     if (rank == 0) {
         for (int b = tid; b <= B; b += kExtendThreads) p.cu[b] = fine ? s_cu[b] : 0;
@@ -376,7 +388,7 @@ sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* 
     if (batch > kMaxRequests || (block_tokens != 16 && block_tokens != 32 && block_tokens != 64 && block_tokens != 128))
         return STA_ERR_UNSUPPORTED;
     if (cudaError_t e = op_begin(); e != cudaSuccess) return op_cuda_status(e);
-    ExtendParams p{batch, block_tokens, table_width, pool, table_stride, max_slots, new_tokens, lengths, lengths_out,
+    ExtendParams p{batch, block_tokens, block_tokens == 16 ? 4 : block_tokens == 32 ? 5 : block_tokens == 64 ? 6 : 7, table_width, pool, table_stride, max_slots, new_tokens, lengths, lengths_out,
                    block_tables, free_blocks, free_count, free_count_out, slots, cu_new, shortage};
     const size_t smem = size_t(4 * batch + 3) * sizeof(int32_t);
     if (smem > 48 * 1024)
@@ -385,7 +397,7 @@ sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* 
             e != cudaSuccess)
             return op_cuda_status(e);
     // a serving step's few slots and tables need no second CTA
-    const unsigned ctas = max_slots > 4 * kExtendThreads || batch > 4 * kExtendThreads / 32 ? kExtendCluster : 1;
+    const unsigned ctas = max_slots > 8 * kExtendThreads || batch > 4 * kExtendThreads / 32 ? kExtendCluster : 1;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
