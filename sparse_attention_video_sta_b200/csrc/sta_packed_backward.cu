@@ -56,7 +56,7 @@ struct BwdParams {
     packed::View v;
     int32_t kv_heads, group, causal;
     const float* neg_l;  // [query blocks][kv_heads][128]: -LSE log2(e); -inf: no such row, or it sees no key
-    const float* neg_d;  // the same for -D
+    float* neg_d;        // the same for -D (the dQ kernel sharpens those of one-chunk walks)
     Rows out_a;          // dQ, or dK
     Rows out_b;          // dV
     float scale, scale_log2;
@@ -214,7 +214,8 @@ struct DqCfg {
     static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 8 + 2 * kItemQ;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kQueueOff = kMiscOff + 16;
-    static constexpr int kSmemBytes = kQueueOff + kItemQ * int(sizeof(QWork)) + 1024;
+    static constexpr int kXchOff = kQueueOff + kItemQ * int(sizeof(QWork));  // [2 halves][128 rows]
+    static constexpr int kSmemBytes = kXchOff + 1024 + 1024;
     static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     static constexpr uint32_t kColS0 = 0, kColDP = 256, kColDQ = 384;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -415,24 +416,36 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
         const uint64_t c2 = ptx::f2(p.scale_log2, p.scale_log2);
         const int r_tok = row / p.group, r_head = row - r_tok * p.group;
+        const uint32_t pair_bar = 1u + uint32_t(warp & 3);  // named barrier of warps w and w + 4: the same rows
+        float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
         uint32_t gs = 0, dqc = 0;
         bool ok = true;
         for (uint32_t kq = 0; ok; ++kq) {
             QWork q;
-            if (!__all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, q))) break;
+            q.n = -1;
+            const bool took = __all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, q));
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
+            if (took && lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
+            if (ptx::bar_red_or(pair_bar, 64, !took)) break;  // leave together: they meet again below
             if (q.n < 0) break;
             const int32_t hk = q.hk, n = q.n;
             const bool real = r_tok < q.ntok;
             const int limit = real ? min(q.nkeys, q.limit0 + (p.causal ? r_tok : 0)) : INT32_MAX;
             const int warp_limit = __reduce_min_sync(~0u, limit);
             const int64_t grow = (int64_t(q.block) * K + hk) * 128 + row;
-            const float nl = p.neg_l[grow], nd = p.neg_d[grow];
-            const uint64_t nl2 = ptx::f2(nl, nl), nd2 = ptx::f2(nd, nd);
+            const float nl = p.neg_l[grow];
+            float nd = p.neg_d[grow];
+            const uint64_t nl2 = ptx::f2(nl, nl);
+            // A walk of one chunk has all of the row's P and dP here, so D = sum P dP is taken from them:
+            // dO.O carries O's rounding to bf16 into every dS of the row, which shows (a sixth of the
+            // error of dQ and dK at 2048 causal tokens) where a row has few keys; over more keys it
+            // averages out.
+            const bool exact = n == 1 && q.c0 == 0 && q.slot < 0;
             for (int32_t j = 0; j < n; ++j) {
                 const uint32_t step = gs + uint32_t(j);
-                if (!__all_sync(~0u, wait_bw(s_full(int(step & 1u)), (step >> 1) & 1u, abort_flag, p))) {
+                // (in an exact walk both warps of a pair meet at its barrier, whatever failed)
+                bool good = __all_sync(~0u, wait_bw(s_full(int(step & 1u)), (step >> 1) & 1u, abort_flag, p));
+                if (!good && !exact) {
                     ok = false;
                     break;
                 }
@@ -456,7 +469,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         pr[2 * i + 1] = ptx::ex2(x1);
                     }
                 }
-                if (!__all_sync(~0u, wait_bw(dp_full, step & 1u, abort_flag, p))) {
+                good = good && __all_sync(~0u, wait_bw(dp_full, step & 1u, abort_flag, p));
+                if (!good && !exact) {
                     ok = false;
                     break;
                 }
@@ -473,6 +487,26 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 pr[i] = 0.0f;
                                 dr[i] = 0u;
                             }
+                    if (exact) {
+                        uint64_t a0 = ptx::f2(0.0f, 0.0f), a1 = a0;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            a0 = ptx::f2_fma(ptx::f2(pr[2 * i], pr[2 * i + 1]),
+                                             ptx::f2(__uint_as_float(dr[2 * i]), __uint_as_float(dr[2 * i + 1])), a0);
+                            a1 = ptx::f2_fma(ptx::f2(pr[2 * i + 2], pr[2 * i + 3]),
+                                             ptx::f2(__uint_as_float(dr[2 * i + 2]), __uint_as_float(dr[2 * i + 3])), a1);
+                        }
+                        float x0, x1;
+                        ptx::f2_split(ptx::f2_add(a0, a1), x0, x1);
+                        xch[h * 128 + row] = x0 + x1;
+                        if (ptx::bar_red_or(pair_bar, 64, !good)) {
+                            ok = false;
+                            break;
+                        }
+                        nd = -(xch[row] + xch[128 + row]);
+                        if (h == 0 && real) p.neg_d[grow] = nd;  // for dK / dV
+                    }
+                    const uint64_t nd2 = ptx::f2(nd, nd);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         float t0, t1;
