@@ -533,6 +533,13 @@ STA_API sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const i
                                     const int32_t* free_count, int32_t* free_count_out, int64_t* slots,
                                     int64_t max_slots, int32_t* cu_new, int32_t* shortage, void* stream);
 
+/* Debug only: with mode 1 a device-side wait of the next calls of
+ * sta_packed_forward, sta_packed_backward and sta_cache_attention runs out on a
+ * barrier that nothing arrives at, every wait having the time limit `limit_ms`
+ * (1..10000): their outputs are left partly written and sta_operator_status
+ * returns TIMEOUT.  Mode 0 (the default): off.  Else INVALID_ARG. */
+STA_API sta_status sta_debug_inject_operator_timeout(int32_t mode, int32_t limit_ms);
+
 /* Synchronise `stream`, then report (and clear) the first asynchronous error of
  * the calls of this part on the current device: CUDA, BOUNDS (bounds, block ids
  * or slots out of range, cut as described) or TIMEOUT.  The device has one

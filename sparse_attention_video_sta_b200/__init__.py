@@ -43,7 +43,7 @@ __all__ = [
     "Pipe", "sta_pipe_create", "sta_backward_raster", "sta_window_pick",
     "sta_packed_forward", "sta_packed_backward", "sta_packed_attention", "sta_packed_attention_backward",
     "StaPackedAttention", "sta_cache_append", "sta_cache_attention", "sta_cache_extend", "CacheStep",
-    "sta_operator_status",
+    "sta_operator_status", "sta_debug_inject_operator_timeout",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -153,8 +153,8 @@ def _check(status: int, what: str) -> None:
 
 _prompt.bind(_lib, _check)
 from ._prompt import (  # noqa: E402  (after the library is loaded)
-    CacheStep, StaPackedAttention, sta_cache_append, sta_cache_attention, sta_cache_extend, sta_operator_status,
-    sta_packed_attention, sta_packed_attention_backward, sta_packed_backward, sta_packed_forward)
+    CacheStep, StaPackedAttention, sta_cache_append, sta_cache_attention, sta_cache_extend,
+    sta_debug_inject_operator_timeout, sta_operator_status, sta_packed_attention, sta_packed_attention_backward, sta_packed_backward, sta_packed_forward)
 
 
 def _geom(latent, tile) -> _Geom:

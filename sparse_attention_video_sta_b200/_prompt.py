@@ -17,12 +17,12 @@ import torch
 __all__ = [
     "sta_packed_forward", "sta_packed_backward", "sta_packed_attention", "sta_packed_attention_backward",
     "StaPackedAttention", "sta_cache_append", "sta_cache_attention", "sta_cache_extend", "CacheStep",
-    "sta_operator_status", "SYMBOLS",
+    "sta_operator_status", "sta_debug_inject_operator_timeout", "SYMBOLS",
 ]
 
 SYMBOLS = (
     "sta_packed_workspace", "sta_packed_forward", "sta_packed_backward", "sta_cache_append", "sta_cache_workspace",
-    "sta_cache_attention", "sta_cache_extend", "sta_operator_status",
+    "sta_cache_attention", "sta_cache_extend", "sta_operator_status", "sta_debug_inject_operator_timeout",
 )
 
 
@@ -62,6 +62,7 @@ def bind(lib, check) -> None:
         "sta_cache_attention": [C, P, vp, vp, i32, i64, R, R, vp, vp, i64, vp],
         "sta_cache_extend": [i32, i32, vp, vp, vp, vp, i32, i64, vp, i32, vp, vp, vp, i64, vp, vp, vp],
         "sta_operator_status": [vp],
+        "sta_debug_inject_operator_timeout": [i32, i32],
     }.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = args, ctypes.c_int
@@ -426,3 +427,8 @@ def sta_operator_status(device=None, stream=None) -> int:
         s = torch.cuda.current_stream() if stream is None else stream
         h = s.cuda_stream if isinstance(s, torch.cuda.Stream) else int(s)
         return int(_lib.sta_operator_status(h))
+
+
+def sta_debug_inject_operator_timeout(mode, limit_ms: int = 50) -> None:
+    """Debug: make a device-side wait of the next packed or cache attention calls run out (``mode`` 0 off, 1 on)."""
+    _check(_lib.sta_debug_inject_operator_timeout(int(mode), int(limit_ms)), "sta_debug_inject_operator_timeout")

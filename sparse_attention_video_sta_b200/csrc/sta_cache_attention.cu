@@ -376,7 +376,8 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 const uint32_t bar = bar0 + 8u * slot_in, dst = ptx::smem_u32(ring + slot_in * 2 * C::kTileBytes);
                 ptx::mbar_arrive_expect_tx(bar, 2 * C::kTileBytes);
                 ptx::tma_load_2d(dst, &tm_k, bar, 0, row);
-                ptx::tma_load_2d(dst + C::kTileBytes, &tm_v, bar, 0, row);
+                if (!a.p.waits.inject)  // (debug: the tile never comes)
+                    ptx::tma_load_2d(dst + C::kTileBytes, &tm_v, bar, 0, row);
             }
             slot_in = slot_in + 1 == S ? 0 : slot_in + 1;
             ++in_flight;
@@ -643,7 +644,10 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         }
     // ---- the CTA's joins: of the unit that its run begins inside of, then of each unit that
     // begins inside of a warp's run and does not end there
-    if (__syncthreads_or(dead)) return;
+    if (__syncthreads_or(dead)) {
+        if (threadIdx.x == 0) a.begins[blockIdx.x].unit0 = -1;  // nothing for the second kernel to join from here
+        return;
+    }
     // (one warp for each row of each such unit)
     const float* parts0 = a.warp_parts + int64_t(blockIdx.x) * kWarps * 2 * kRows * (D + 4);
     // lane i < 16: does warp i's run begin inside of a unit, does it leave one unfinished
@@ -839,7 +843,7 @@ sta_status sta_cache_attention(const sta_cache* c, const sta_packed* p, const in
     a.k_scales = c->k_scales;
     a.v_scales = c->v_scales;
     a.warp_parts = static_cast<float*>(workspace);
-    a.timeout_ns = kOpTimeoutNs;
+    a.timeout_ns = a.p.waits.timeout_ns;
     a.lengths = lengths;
     a.tables = block_tables;
     a.width = table_width;

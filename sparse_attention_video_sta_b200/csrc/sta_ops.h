@@ -19,8 +19,13 @@ cudaError_t op_begin();
 // Device address of the current device's status word (looked up once per device).
 cudaError_t op_status_word(uint32_t** out);
 
-// Time limit of every device-side wait of these operators' kernels.
-constexpr uint64_t kOpTimeoutNs = 2000000000ull;
+// Time limit of every device-side wait of these operators' kernels, and whether a wait is made to
+// run out (sta_debug_inject_operator_timeout).
+struct OpWaits {
+    uint64_t timeout_ns;
+    int32_t inject;
+};
+OpWaits op_waits();
 
 // A token-major bf16 tensor as the kernels address it.
 struct Rows {
@@ -47,6 +52,7 @@ struct PackedProblem {
     int32_t causal, clear_tail;
     float scale;
     uint32_t* status;
+    OpWaits waits;
 };
 
 // Checks shared by the packed calls; fills everything but `status`.

@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cmath>
 #include <mutex>
 
@@ -46,6 +47,8 @@ constexpr float kRescaleRowSum = 65536.0f;
 constexpr int kMaxDevices = 64;
 __device__ uint32_t g_op_status;  // one word per device: kDevTimeout | kDevBounds
 std::mutex g_status_mutex;
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per device-side wait
+std::atomic<int32_t> g_op_inject_ms{0};
 uint32_t* g_status_ptr[kMaxDevices] = {};
 
 // The forward kernel.  One item is one query block (128 rows: tokens x the query
@@ -204,7 +207,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int32_t n_items = p.self ? 0 : p.v.lists->w_q * K;
             uint32_t ring = 0;
             uint32_t q_loads[2] = {0u, 0u};
-            bool ok = true;
+            bool ok = !p.prob.waits.inject || wait_bar(bar_drain(0), 0);  // (arrived at on the way out only)
             auto issue = [&](const CUtensorMap* m, int32_t head, int32_t row) -> bool {
                 const int r = int(ring % S);
                 if (ring >= uint32_t(S) && !wait_bar(bar_empty(r), ((ring / S) - 1) & 1u)) return false;
@@ -667,7 +670,7 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     if (e == cudaSuccess) e = packed::rows_map(&mv, v, p.tokens_k, p.kv_heads, D, 1, 128);
     if (e != cudaSuccess) return e;
     FwdParams fp{view, p, self ? 1 : 0, p.kv_heads, p.group, p.causal, p.tokens_q, o, lse, p.scale, p.scale * 1.4426950408889634f,
-                 uint32_t(p.group * tpb) * 128u, p.status, kOpTimeoutNs};
+                 uint32_t(p.group * tpb) * 128u, p.status, p.waits.timeout_ns};
     constexpr int kSmem = Cfg<D>::kSmemBytes;
     const int64_t items = w.max_wq * p.kv_heads;
     if (short_walks(p, D)) {
@@ -692,6 +695,11 @@ bool self_planned(const PackedProblem& p, const packed::Layout& w) {
 }
 
 }  // namespace
+
+OpWaits op_waits() {
+    const int32_t ms = g_op_inject_ms.load();  // 0: off
+    return ms > 0 ? OpWaits{uint64_t(ms) * 1000000ull, 1} : OpWaits{kTimeoutNs, 0};
+}
 
 cudaError_t op_status_word(uint32_t** out) {
     int dev = -1;
@@ -726,7 +734,7 @@ sta_status packed_problem(const sta_packed* p, bool pointers, PackedProblem* out
             return STA_ERR_INVALID_ARG;
     }
     *out = PackedProblem{p->batch, p->heads, p->kv_heads, group, int32_t(p->tokens_q), int32_t(p->tokens_k),
-                         p->cu_q, p->cu_k, p->causal, p->clear_tail, p->softmax_scale, nullptr};
+                         p->cu_q, p->cu_k, p->causal, p->clear_tail, p->softmax_scale, nullptr, op_waits()};
     return STA_OK;
 }
 
@@ -809,6 +817,12 @@ sta_status sta_packed_backward(const sta_packed* p, const sta_rows* q, const sta
     return op_cuda_status(launch_packed_backward(pp, p->head_dim, rows_of(q), rows_of(k), rows_of(v), rows_of(o),
                                                  rows_of(dout), lse, rows_of(dq), rows_of(dk), rows_of(dv), workspace,
                                                  static_cast<cudaStream_t>(stream)));
+}
+
+sta_status sta_debug_inject_operator_timeout(int32_t mode, int32_t limit_ms) {
+    if (mode < 0 || mode > 1 || limit_ms < 1 || limit_ms > 10000) return STA_ERR_INVALID_ARG;
+    sta::g_op_inject_ms.store(mode == 1 ? limit_ms : 0);
+    return STA_OK;
 }
 
 sta_status sta_operator_status(void* stream) {

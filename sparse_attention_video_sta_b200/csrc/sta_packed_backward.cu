@@ -63,6 +63,7 @@ struct BwdParams {
     uint32_t q_box_bytes;
     uint32_t* status;
     uint64_t timeout_ns;
+    int32_t inject;        // debug: the load thread's first wait runs out
 };
 
 __device__ __forceinline__ bool wait_bw(uint32_t bar, uint32_t parity, volatile int* abort_flag, const BwdParams& p) {
@@ -301,7 +302,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // ------------------------------------------------------------ load
             const int32_t n_items = p.v.lists->w_q * K;
             uint32_t kit = 0, vit = 0, qc = 0;
-            bool ok = true;
+            bool ok = !p.inject || wait_bw(drain, 0, abort_flag, p);  // (arrived at on the way out only)
             for (uint32_t kq = 0; ok; ++kq) {
                 QWork q;
                 if (!put_item(kq, q, p.v.qwalks, &p.v.lists->next_dq, n_items, K, item_full0, item_empty0, item_q, abort_flag, p))
@@ -656,7 +657,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // ------------------------------------------------------------ load
             const int32_t n_items = p.v.lists->w_k * K;
             uint32_t sit = 0, kvc = 0;
-            bool ok = true;
+            bool ok = !p.inject || wait_bw(drain, 0, abort_flag, p);  // (arrived at on the way out only)
             for (uint32_t kq = 0; ok; ++kq) {
                 KWork kb;
                 if (!put_item(kq, kb, p.v.kwalks, &p.v.lists->next_k, n_items, K, item_full0, item_empty0, item_q, abort_flag, p))
@@ -1003,7 +1004,7 @@ cudaError_t launch_bwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     float* neg_l = reinterpret_cast<float*>(ws + w.neg_l);
     float* neg_d = reinterpret_cast<float*>(ws + w.neg_d);
     BwdParams bp{view, p.kv_heads, p.group, p.causal, neg_l, neg_d, dq, dq, p.scale, p.scale * kLog2e,
-                 uint32_t(p.group * tpb) * 128u, p.status, kOpTimeoutNs};
+                 uint32_t(p.group * tpb) * 128u, p.status, p.waits.timeout_ns, p.waits.inject};
     constexpr int kDq = smem_launch(DqCfg<D>::kSmemBytes), kDkv = smem_launch(DkvCfg<D>::kSmemBytes);
     e = cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDq);
     if (e == cudaSuccess)

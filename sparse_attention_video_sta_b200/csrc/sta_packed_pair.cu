@@ -167,7 +167,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             int32_t u2 = early ? next() : 0;
             QWork w1 = p.self ? item_q[0] : fetch(id);
             uint32_t ki = 0, vi = 0, qi = 0;
-            bool ok = true;
+            bool ok = !p.prob.waits.inject || wait_bar(drain, 0);  // (arrived at on the way out only)
             for (uint32_t k = 0; ok; ++k) {
                 const int qe = int(k % kItemQ);
                 if (k > 0 && p.self)

@@ -414,6 +414,22 @@ def test_many_requests(sta):
     ref.check(lse, want, "lse")
 
 
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_clean(sta):
+    lengths, K, bt, d = [3000, 5, 800], 2, 64, 128
+    kc, vc, ks, vs, table = filled_cache(lengths, K, bt, d, seed=3)
+    q = torch.randn(3, 6, d, device="cuda").bfloat16()
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    want = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n)
+    sta.sta_debug_inject_operator_timeout(1, 20)
+    try:
+        sta.sta_cache_attention(q, kc, vc, ks, vs, table, n)
+        assert sta.sta_operator_status() == sta.STA_ERR_TIMEOUT
+    finally:
+        sta.sta_debug_inject_operator_timeout(0)
+    got = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n)
+    assert sta.sta_operator_status() == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("H,K,d,bt", [(6, 2, 128, 16), (8, 1, 64, 64)])
 def test_serving_prompts_and_tokens(sta, H, K, d, bt):

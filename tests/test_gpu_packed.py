@@ -418,3 +418,28 @@ print("fine")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-3000:]
+
+
+@pytest.mark.parametrize("lens,d", [([700, 300], 128), ([60] * 40, 64), ([30, 5], 64), ([4000], 64)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_calls_are_clean(sta, lens, d):
+    """Each kernel's load thread waits on a barrier that nothing arrives at, with a short limit: the kernels end,
+    the status says so, and the same calls give their results again."""
+    q, k, v, do = make(lens, lens, 4, 2, d, seed=16)
+    cu = ref.cu_of(lens)
+
+    def both():
+        o, lse = sta.sta_packed_attention(q, k, v, cu)
+        return (o, lse) + sta.sta_packed_attention_backward(q, k, v, want[0] if want else o, want[1] if want else lse, do, cu)
+    want = None
+    want = both()
+    assert sta.sta_operator_status() == 0
+    sta.sta_debug_inject_operator_timeout(1, 20)
+    try:
+        for call in (lambda: sta.sta_packed_attention(q, k, v, cu),
+                     lambda: sta.sta_packed_attention_backward(q, k, v, want[0], want[1], do, cu)):
+            call()
+            assert sta.sta_operator_status() == sta.STA_ERR_TIMEOUT
+    finally:
+        sta.sta_debug_inject_operator_timeout(0)
+    assert all(torch.equal(a, b) for a, b in zip(both(), want))
+    assert sta.sta_operator_status() == 0

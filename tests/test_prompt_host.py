@@ -128,3 +128,8 @@ def test_extend_is_refused():
                dict(cu=None), dict(sh=None), dict(ln=P + 2)):
         assert ext(**kw) == INV, kw
     assert ext(batch=8193) == UNS and ext(bt=48) == UNS
+
+
+def test_timeout_injection_arguments():
+    f = sta._lib.sta_debug_inject_operator_timeout
+    assert f(2, 50) == INV and f(-1, 50) == INV and f(1, 0) == INV and f(1, 10001) == INV and f(0, 50) == OK
