@@ -1,9 +1,12 @@
-"""Build libsta.so (the C-ABI STA library) in-tree with nvcc for sm_100a."""
+"""Build libsta.so (the C-ABI STA library, nvcc for sm_100a) and _sta_torch.so (checks and
+allocation of the prompt side's calls on PyTorch tensors; host code) in-tree."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -13,6 +16,9 @@ LIB_PATH = os.path.join(PKG_DIR, "libsta.so")
 # The same library with the device-side checks of every plan index compiled in
 # (STA_DEBUG_BOUNDS; see csrc/sta_bounds.cuh).
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libsta_debug.so")
+
+TORCH_PATH = os.path.join(PKG_DIR, "_sta_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "sta_torch.cpp")
 
 SOURCES = ["sta_api.cu", "sta_permute.cu", "sta_forward.cu", "sta_backward.cu", "sta_search.cu", "sta_pipe.cu", "sta_noalloc.cu",
            "sta_packed_lists.cu", "sta_packed.cu", "sta_packed_pair.cu",
@@ -52,8 +58,34 @@ def _compile(path: str, extra, verbose: bool):
     os.replace(tmp, path)
 
 
+def _torch_command(out: str):
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            *[a for i in inc for a in ("-isystem", i)], TORCH_SOURCE, "-o", out, "-L", os.path.join(torch_dir, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
+def _torch_up_to_date() -> bool:
+    return os.path.exists(TORCH_PATH) and all(os.path.getmtime(f) <= os.path.getmtime(TORCH_PATH)
+                                              for f in (TORCH_SOURCE, os.path.join(INCLUDE, "sta.h")))
+
+
+def _build_torch(verbose: bool):
+    tmp = TORCH_PATH + f".tmp{os.getpid()}"
+    cmd = _torch_command(tmp)
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, TORCH_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Build libsta.so (and, with debug=True, also libsta_debug.so)."""
+    """Build libsta.so and _sta_torch.so (and, with debug=True, also libsta_debug.so)."""
+    if force or not _torch_up_to_date():
+        _build_torch(verbose)
     if force or not up_to_date(LIB_PATH):
         _compile(LIB_PATH, [], verbose)
     if debug and (force or not up_to_date(DEBUG_LIB_PATH)):

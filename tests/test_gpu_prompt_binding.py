@@ -1,0 +1,171 @@
+"""The prompt side's compiled binding: what it refuses, the streams it takes, who owns new tensors."""
+import math
+
+import pytest
+import torch
+
+import prompt_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def sta():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    import sparse_attention_video_sta_b200 as s
+    return s
+
+
+def packed_args():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)
+    return dict(q=r(9, 4, 64), k=r(9, 2, 64), v=r(9, 2, 64), o=r(9, 4, 64), lse=torch.zeros(4, 9, device="cuda"),
+                cu_q=ref.cu_of([5, 4]))
+
+
+PACKED = [
+    ("q", lambda t: t.cpu(), "CUDA"), ("q", lambda t: t.float(), "bf16"), ("q", lambda t: t[0], "tokens, heads, d"),
+    ("k", lambda t: t.half(), "bf16"), ("k", lambda t: t.cpu(), "bf16"), ("v", lambda t: t[:, :, :32], "shape"),
+    ("v", lambda t: t[:-1], "shape"), ("k", lambda t: torch.zeros(9, 2, 128, device="cuda", dtype=BF)[..., ::2], "contiguous"),
+    ("k", lambda t: torch.zeros(9, 2, 68, device="cuda", dtype=BF)[..., :64], "multiples of 8"),
+    ("k", lambda t: torch.zeros(9, 2, 72, device="cuda", dtype=BF)[..., 4:68], "aligned"),
+    ("v", lambda t: t[:1].expand(9, -1, -1), "positive"), ("o", lambda t: t[:, :2], "shape"),
+    ("lse", lambda t: t.double(), "fp32"), ("lse", lambda t: t.t().contiguous(), "shape"),
+    ("cu_q", lambda t: t.long(), "Int"), ("cu_q", lambda t: t.cpu(), "cuda"), ("cu_q", lambda t: t[None], "sequences"),
+    ("cu_q", lambda t: t[:0], "sequences"), ("cu_q", lambda t: t.repeat(2)[::2], "contiguous"),
+    ("cu_k", lambda t: ref.cu_of([9]), "shape"),
+    ("workspace", lambda t: torch.empty(1 << 20, device="cuda"), "uint8"),
+    ("workspace", lambda t: torch.empty(1 << 20, dtype=torch.uint8), "uint8"),
+]
+
+
+@pytest.mark.parametrize("name,change,word", PACKED, ids=[f"{n}-{i}" for i, (n, _, _) in enumerate(PACKED)])
+def test_packed_refusals(sta, name, change, word):
+    a = packed_args()
+    a[name] = change(a.get(name))
+    with pytest.raises(ValueError, match=word):
+        sta.sta_packed_forward(**a)
+    if name != "o" and name != "lse" and name != "workspace":
+        b = {n: a[n] for n in a if n not in ("o", "lse")}
+        with pytest.raises(ValueError, match=word):
+            sta.sta_packed_attention(**b)
+    d = packed_args()
+    d[name] = a[name]
+    with pytest.raises(ValueError, match=word):
+        sta.sta_packed_backward(d.pop("q"), d.pop("k"), d.pop("v"), d.pop("o"), d.pop("lse"), torch.zeros(9, 4, 64, device="cuda", dtype=BF),
+                                torch.zeros(9, 4, 64, device="cuda", dtype=BF), torch.zeros(9, 2, 64, device="cuda", dtype=BF),
+                                torch.zeros(9, 2, 64, device="cuda", dtype=BF), d.pop("cu_q"), **d)
+
+
+def test_library_errors_come_through(sta):
+    a = packed_args()
+    a["k"], a["v"] = (torch.zeros(9, 3, 64, device="cuda", dtype=BF) for _ in range(2))  # 4 heads, 3 key heads
+    with pytest.raises(sta.StaError, match="sta_packed_workspace"):
+        sta.sta_packed_forward(**a)
+    a = packed_args()
+    with pytest.raises(ValueError, match="workspace"):
+        sta.sta_packed_backward(a["q"], a["k"], a["v"], a["o"], a["lse"], a["o"], a["o"].clone(), a["k"].clone(),
+                                a["v"].clone(), a["cu_q"], workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(sta.StaError):
+        sta.sta_packed_forward(**packed_args(), softmax_scale=math.nan)
+    with pytest.raises(TypeError):
+        sta.sta_packed_forward(None, *list(packed_args().values())[1:])
+
+
+def cache_args(K=2, d=64, bt=32, blocks=4):
+    codes = [torch.zeros(blocks, K, bt, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.full((blocks, K), 2.0 ** -60, device="cuda") for _ in range(2)]
+    return codes + scales
+
+
+CACHE = [
+    (0, lambda t: t.cpu(), "CUDA"), (0, lambda t: t[0], "CUDA"), (0, lambda t: t.view(torch.int8), "e4m3"),
+    (1, lambda t: t[:-1], "shape"), (1, lambda t: t.transpose(1, 2), "shape"), (2, lambda t: t.double(), "fp32"),
+    (3, lambda t: t[:, :1], "shape"), (3, lambda t: t.t().contiguous().t(), "contiguous"),
+]
+
+
+@pytest.mark.parametrize("which,change,word", CACHE, ids=[f"{n}-{i}" for i, (n, _, _) in enumerate(CACHE)])
+def test_cache_refusals(sta, which, change, word):
+    c = cache_args()
+    c[which] = change(c[which])
+    x = torch.zeros(3, 2, 64, device="cuda", dtype=BF)
+    with pytest.raises(ValueError, match=word):
+        sta.sta_cache_append(x, x, torch.arange(3, device="cuda"), *c)
+    with pytest.raises(ValueError, match=word):
+        sta.sta_cache_attention(x, *c, torch.zeros(3, 1, dtype=torch.int32, device="cuda"),
+                                torch.ones(3, dtype=torch.int32, device="cuda"))
+
+
+def test_cache_argument_refusals(sta):
+    c = cache_args()
+    x = torch.zeros(3, 2, 64, device="cuda", dtype=BF)
+    t, n = torch.zeros(3, 2, dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    slots = torch.arange(3, device="cuda")
+    for k, s in ((x, slots.int()), (x[:2], slots), (x, slots.cpu()), (x.float(), slots), (x, slots[None])):
+        with pytest.raises(ValueError):
+            sta.sta_cache_append(k, x, s, *c)
+    for q, tt, nn, kw in ((x[:2], t, n, {}), (x, t.long(), n, {}), (x, t[:2], n, {}), (x, t[:, :0], n, {}), (x, t[:, 0], n, {}),
+                          (x, t.t().contiguous().t(), n, {}), (x, t, n.long(), {}), (x, t, n[None], {}),
+                          (x, t, n, dict(cu_q=n)), (x, t, n, dict(o=x.float())), (x, t, n, dict(lse=n.float())),
+                          (x, t[:1].expand(3, 2), n, {}), (x.expand(3, 2, 64)[:, :, ::2], t, n, {})):
+        with pytest.raises((ValueError, sta.StaError)):
+            sta.sta_cache_attention(q, *c, tt, nn, **kw)
+    free, count = torch.arange(4, dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
+    for kw in (dict(new_tokens=n[:2]), dict(lengths=n.cpu()), dict(block_tables=t.long()), dict(free_blocks=free.long()),
+               dict(free_count=free), dict(block_tokens=33), dict(block_tokens=-32), dict(max_slots=-1)):
+        a = dict(new_tokens=n, lengths=n, block_tables=t, free_blocks=free, free_count=count, block_tokens=32, max_slots=3)
+        a.update(kw)
+        with pytest.raises((ValueError, sta.StaError)):
+            sta.sta_cache_extend(**a)
+
+
+def test_streams(sta):
+    """A stream object, its raw handle and the current stream give the same; memory that a call on a side stream
+    used is not handed out before that stream is done with it."""
+    a = packed_args()
+    args = (a["q"], a["k"], a["v"], a["cu_q"])
+    want = sta.sta_packed_attention(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, 0):
+        got = sta.sta_packed_attention(*args, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    with torch.cuda.stream(side):
+        got = sta.sta_packed_attention(*args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # outputs dropped while the side stream is still busy: their memory must not be given to the current stream
+    big = torch.zeros(1 << 27, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big.add_(1.0)
+    o, lse = sta.sta_packed_attention(*args, stream=side)
+    p = o.data_ptr()
+    del o
+    assert all(torch.empty_like(a["q"]).data_ptr() != p for _ in range(3)) or side.query()
+    torch.cuda.synchronize()
+
+
+def test_no_grad_history_and_contiguous_outputs(sta):
+    a = packed_args()
+    q = a["q"].transpose(0, 1).contiguous().transpose(0, 1).requires_grad_()
+    o, lse = sta.sta_packed_attention(q, a["k"], a["v"], a["cu_q"])
+    assert o.is_contiguous() and lse.is_contiguous() and not o.requires_grad and o.grad_fn is None
+    c = cache_args()
+    step = sta.sta_cache_extend(torch.ones(2, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                                torch.full((2, 1), -1, dtype=torch.int32, device="cuda"),
+                                torch.arange(4, dtype=torch.int32, device="cuda"),
+                                torch.tensor([4], dtype=torch.int32, device="cuda"), 32, 2)
+    assert isinstance(step, sta.CacheStep) and step.slots.dtype is torch.int64 and int(step.short) == 0
+    x = torch.zeros(2, 2, 64, device="cuda", dtype=BF)
+    sta.sta_cache_append(x, x, step.slots, *c)
+    for cu in (None, torch.zeros(1, dtype=torch.int32, device="cuda")):  # no queries, no sequences
+        o, lse = sta.sta_cache_attention(x[:0], *c, torch.zeros(0, 1, dtype=torch.int32, device="cuda"),
+                                         torch.zeros(0, dtype=torch.int32, device="cuda"), cu)
+        assert o.shape == (0, 2, 64) and lse.shape == (2, 0)
