@@ -61,9 +61,10 @@ uint32_t* g_status_ptr[kMaxDevices] = {};
 //                   V(i), K(i + 3) into the ring
 //   warp 9  (PV)  : O += P_A V_A, then O += P_B V_B as each half's P lands in TMEM
 //   warp 10 (S)   : S(c) = Q K(c)^T into buffer c % 3, once the PVs of chunk c - 3 are done
-//   warp 11 (tail): a sequence's last chunk may end inside its 128 rows; what lies
-//                   behind (the next sequence, or anything) has P = 0, but 0 x inf is
-//                   not 0, so those V rows are overwritten with zeros in shared memory
+//   warp 11 (tail): rows of a V chunk that no row of the block sees (behind the causal diagonal,
+//                   or the sequence's end) have P = 0, but 0 x inf is not 0: they are overwritten
+//                   with zeros in shared memory, and those that only some rows see lose what is
+//                   not finite (scrub_rows)
 //   warps 0-7     : softmax halves and the epilogue
 //
 // Masks: a row sees keys [0, limit).  A chunk wholly below every row's limit
@@ -92,7 +93,8 @@ struct Cfg {
     static constexpr int kNumBars = 4 * kStages + 4 + kSBufs + 2 * kSBufs + kSBufs + 4 + 2 * kItemQ;
     static constexpr int kXchOff = kBarOff + kNumBars * 8;   // [2 halves][128 rows] fp32 exchange
     static constexpr int kMiscOff = kXchOff + 2 * 128 * 4;   // tmem base slot, abort flag
-    static constexpr int kQueueOff = kMiscOff + 16;          // item queue
+    static constexpr int kLostOff = kMiscOff + 16;           // kLostWords
+    static constexpr int kQueueOff = kLostOff + 4 * packed::kLostWords;  // item queue
     static constexpr int kSmemBytes = kQueueOff + kItemQ * int(sizeof(QWork)) + 1024;
     static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     __host__ __device__ static constexpr uint32_t col_s(int buf) { return uint32_t(buf) * 128u; }
@@ -137,6 +139,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    volatile uint32_t* lost = reinterpret_cast<volatile uint32_t*>(smem + C::kLostOff);
     QWork* item_q = reinterpret_cast<QWork*>(smem + C::kQueueOff);
     auto wait_bar = [&](uint32_t bar, uint32_t parity) {
         return wait_bar_limited(bar, parity, abort_flag, p.status, p.timeout_ns);
@@ -174,6 +177,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             ptx::mbar_init(bar_item_empty(q), kItemConsumers);
         }
         *abort_flag = 0;
+        for (int i = 0; i < packed::kLostWords; ++i) lost[i] = 0;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
     }
@@ -196,8 +200,6 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // K(0), K(1), K(2), then V(i), K(i + 3) for i = 0, 1, ...).
     auto entry_k = [](uint32_t c) { return c < uint32_t(NB) ? c : 2u * c - uint32_t(NB - 1); };
     auto entry_v = [](uint32_t i, uint32_t n) { return i + uint32_t(NB) <= n ? uint32_t(NB) + 2u * i : n + i; };
-    // Does the walk's last chunk reach past the sequence's last key?
-    auto ragged = [](const QWork& q) { return (q.c0 + q.n) * 128 > q.nkeys; };
 
     if (warp == kLoadWarp) {
         ptx::regs_dec<kRegsProducer>();
@@ -264,7 +266,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int32_t c = 0; ok && c < n && c < NB; ++c) ok = issue(&tm_k, hk, row0 + c * 128);
                 for (int32_t i = 0; ok && i < n; ++i) {
                     ok = issue(&tm_v, hk, row0 + i * 128);
-                    if (ok && i == n - 1 && ragged(q)) ptx::mbar_arrive(bar_v_tail(int((ring - 1) % S)));
+                    if (ok && i >= first_care(q)) ptx::mbar_arrive(bar_v_tail(int((ring - 1) % S)));
                     if (ok && i + NB < n) ok = issue(&tm_k, hk, row0 + (i + NB) * 128);
                 }
             }
@@ -286,22 +288,26 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             if (lane == 0) ptx::mbar_arrive(bar_item_empty(int(kq % kItemQ)));
             if (q.n < 0) break;
             const uint32_t n = uint32_t(q.n);
-            if (ragged(q)) {
-                const uint32_t e = e0 + entry_v(n - 1, n);
+            bool ok = true;
+            for (uint32_t i = uint32_t(first_care(q)); i < n; ++i) {
+                const uint32_t e = e0 + entry_v(i, n);
                 const int r = int(e % S);
-                if (!__all_sync(~0u, wait_bar(bar_v_tail(r), (tails >> r) & 1u))) break;
+                ok = __all_sync(~0u, wait_bar(bar_v_tail(r), (tails >> r) & 1u) && wait_bar(bar_full(r), (e / S) & 1u));
+                if (!ok) break;
                 tails ^= 1u << r;
-                if (!__all_sync(~0u, wait_bar(bar_full(r), (e / S) & 1u))) break;
-                const int from = q.nkeys - (q.c0 + q.n - 1) * 128;  // rows [from, 128) hold no key
+                const int key = (q.c0 + int(i)) * 128, dead = dead_from(q, p.causal, key);
                 uint8_t* v0 = smem + C::kRingOff + r * C::kKVBytes;
-                for (int i = from * 8 + lane; i < 128 * 8; i += 32)
+                for (int j = dead * 8 + lane; j < 128 * 8; j += 32)
 #pragma unroll
                     for (int cb = 0; cb < C::kColBlocks; ++cb)
-                        *reinterpret_cast<uint4*>(v0 + cb * kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(v0 + cb * kBoxBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                if (packed::scrub_rows<C::kColBlocks>(v0, kBoxBytes, hidden_from(q, key), dead, lane, 32))
+                    lost[kq % packed::kLostWords] = kq + 1;
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar_v_clean(r));
             }
+            if (!ok) break;
             e0 += 2u * n;
         }
     } else if (warp == kPvWarp || warp == kSWarp) {
@@ -333,7 +339,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         const uint32_t gi = g0 + i, bb = gi % uint32_t(NB), e = e0 + entry_v(i, n);
                         uint32_t vaddr;
                         if (!wait_entry(e, vaddr)) { ok = false; break; }
-                        if (i == n - 1 && ragged(q)) {
+                        if (i >= uint32_t(first_care(q))) {
                             const uint32_t r = e % S;
                             if (!wait_bar(bar_v_clean(int(r)), (cleaned >> r) & 1u)) { ok = false; break; }
                             cleaned ^= 1u << r;
@@ -460,13 +466,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (ptx::bar_red_or(pair_bar, 64, !wok || need || i == 0)) {
                     // ---- slow path: the block's first chunk, a rescale, or an abort.
                     // Both warps of the pair take it, exchange this chunk's
-                    // maxima of their rows and agree on the new running max.
+                    // maxima of the rows that need it and agree on the new running max.
+                    // (Of those alone: what a row comes to never depends on other rows.)
                     if (nxt) {
                         ptx::tmem_wait_ld(sr);
                         ptx::tmem_ld64(tS, sr);  // S(g) again: P(g) is not stored yet
                         if (masked) mask_from(sr, limit - kbeg);
                     }
-                    *x_mine = wok ? row_max64(sr) : -INFINITY;
+                    *x_mine = wok && (need || i == 0) ? row_max64(sr) : -INFINITY;
                     if (ptx::bar_red_or(pair_bar, 64, !wok)) {
                         ok = false;
                         break;
@@ -545,10 +552,17 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             uint4* dst = reinterpret_cast<uint4*>(p.o.p + tok * p.o.ts + head * p.o.hs + half * (D / 2));
             // a part: O unnormalised in fp32, and after the rows m (in units of log2) and l
             float* part = p.v.parts + (int64_t(q.slot) * K + q.hk) * (128 * (D + 2));
+            const bool fix = real && lost[kq % packed::kLostWords] == kq + 1;
 #pragma unroll 1
             for (int cb = 0; cb < D / 64; ++cb) {
                 uint32_t orr[32];
                 ptx::tmem_ld32(tOh + cb * 32, orr);  // every lane loads: the access is warp-wide
+                if (fix) {
+                    int lo;
+                    const int seen = lost_seen(q, limit, lo);
+                    packed::restore(orr, p.vals.p + (q.key0 + int64_t(lo)) * p.vals.ts + q.hk * p.vals.hs + half * (D / 2) + cb * 32,
+                                    p.vals.ts, seen);
+                }
                 if (q.slot >= 0) {
                     float4* d4 = reinterpret_cast<float4*>(part + row * D + half * (D / 2) + cb * 32);
                     if (real)
@@ -669,7 +683,7 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     if (e == cudaSuccess) e = packed::rows_map(&mk, k, p.tokens_k, p.kv_heads, D, 1, 128);
     if (e == cudaSuccess) e = packed::rows_map(&mv, v, p.tokens_k, p.kv_heads, D, 1, 128);
     if (e != cudaSuccess) return e;
-    FwdParams fp{view, p, self ? 1 : 0, p.kv_heads, p.group, p.causal, p.tokens_q, o, lse, p.scale, p.scale * 1.4426950408889634f,
+    FwdParams fp{view, p, self ? 1 : 0, p.kv_heads, p.group, p.causal, p.tokens_q, o, v, lse, p.scale, p.scale * 1.4426950408889634f,
                  uint32_t(p.group * tpb) * 128u, p.status, p.waits.timeout_ns};
     constexpr int kSmem = Cfg<D>::kSmemBytes;
     const int64_t items = w.max_wq * p.kv_heads;

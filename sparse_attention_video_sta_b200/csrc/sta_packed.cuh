@@ -157,6 +157,75 @@ cudaError_t launch_lists(const PackedProblem& p, const View& v, bool backward, i
 // (heads innermost), 128-byte swizzle.
 cudaError_t rows_map(CUtensorMap* m, const Rows& r, int64_t tokens, int heads, int d, int box_heads, int box_tokens);
 
+#ifdef __CUDACC__
+// Infinities and NaN where a mask hides them.  In P V a masked pair has P = 0, but 0 x inf and 0 x NaN
+// are NaN, and the tensor core multiplies every pair.  So the rows that some row of the block does
+// not see have their non-finite elements set to zero in shared memory (scrub_rows), and the rows of
+// the result that do see them get them back at the end (restore): adding a non-finite element is
+// what its product would have done.  What is scanned is the causal diagonal of a block alone, and
+// the second half only runs for an item in which the first found something.
+//
+// Elements of a pair of bf16 that are not finite: bit 15 for the low one, 31 for the high one.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// Are there any in rows [from, to) of a block in shared memory (128-byte rows in boxes of `box`
+// bytes)?  `threads` threads share the rows; the answer is the caller's own part.
+template <int kBoxes>
+__device__ __forceinline__ bool any_lost(const uint8_t* blk, int box, int from, int to, int thread, int threads) {
+    uint32_t bad = 0;
+    for (int i = from * 8 + thread; i < to * 8; i += threads)
+#pragma unroll
+        for (int cb = 0; cb < kBoxes; ++cb) {
+            const uint4 x = *reinterpret_cast<const uint4*>(blk + cb * box + i * 16);
+            bad |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
+        }
+    return bad != 0;
+}
+// Sets them to zero (the caller fences the writes for the asynchronous proxy); were there any?
+template <int kBoxes>
+__device__ __forceinline__ bool scrub_rows(uint8_t* blk, int box, int from, int to, int thread, int threads) {
+    bool any = false;
+    for (int i = from * 8 + thread; i < to * 8; i += threads)
+#pragma unroll
+        for (int cb = 0; cb < kBoxes; ++cb) {
+            uint4* at = reinterpret_cast<uint4*>(blk + cb * box + i * 16);
+            uint4 x = *at;
+            const uint4 b = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+            if ((b.x | b.y | b.z | b.w) == 0) continue;
+            x.x &= ~((b.x >> 15) * 0xffffu);
+            x.y &= ~((b.y >> 15) * 0xffffu);
+            x.z &= ~((b.z >> 15) * 0xffffu);
+            x.w &= ~((b.w >> 15) * 0xffffu);
+            *at = x;
+            any = true;
+        }
+    return any;
+}
+// r[i] += src[i] where that is not finite, for `n` rows of N elements `stride` apart.
+template <int N>
+__device__ __forceinline__ void restore(uint32_t (&r)[N], const __nv_bfloat16* src, int64_t stride, int n) {
+    for (int k = 0; k < n; ++k) {
+        const uint4* row = reinterpret_cast<const uint4*>(src + k * stride);
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+            const uint4 v = __ldg(row + j);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t b = not_finite(w[e]);
+                const int at = 8 * j + 2 * e;
+                if (b & 0x8000u) r[at] = __float_as_uint(__uint_as_float(r[at]) + __uint_as_float(w[e] << 16));
+                if (b & 0x80000000u)
+                    r[at + 1] = __float_as_uint(__uint_as_float(r[at + 1]) + __uint_as_float(w[e] & 0xffff0000u));
+            }
+        }
+    }
+}
+// Which items had any: word k % kLostWords holds k + 1.  (Writers are at most the item queue's length
+// ahead of the last reader, so a word is not reused too early.)
+constexpr int kLostWords = 8;
+#endif
+
 // Launch attributes: `pdl`: the kernel may start while its predecessor in the
 // stream ends, and waits for it (griddepcontrol.wait) before it reads memory.
 template <class... P, class... A>

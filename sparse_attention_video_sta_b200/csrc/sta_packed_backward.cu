@@ -15,10 +15,11 @@
 //
 // Masks and rows that are not there.  In a masked chunk P and dS are selected to 0,
 // whatever the products held.  Rows of an operand that a product sums over must be
-// finite as well, since 0 x inf is not 0: K rows behind the sequence's last key (dQ)
+// finite as well, since 0 x inf is not 0: K rows that no query of the block sees (dQ)
 // and Q, dO rows behind a block's last token (dK, dV) are overwritten with zeros in
 // shared memory by the elementwise warps, once the products that only need the other
-// rows have read them.
+// rows have read them; on the causal diagonal the rows that only some see lose what is
+// not finite, and the results that see them get it back (scrub_rows, restore).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -64,6 +65,7 @@ struct BwdParams {
     uint32_t* status;
     uint64_t timeout_ns;
     int32_t inject;        // debug: the load thread's first wait runs out
+    Rows q, k, dout;
 };
 
 __device__ __forceinline__ bool wait_bw(uint32_t bar, uint32_t parity, volatile int* abort_flag, const BwdParams& p) {
@@ -109,14 +111,16 @@ __device__ __forceinline__ void pack64(const float (&x)[64], uint32_t (&pk)[32])
 
 // `kCols` fp32 TMEM columns of this thread's lane, times `mul`, as bf16 to dst; `zero`: zeros
 // instead.  Every lane loads (the access is warp-wide); lanes with `store` write.
-template <int kCols>
-__device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloat16* dst, bool store, bool zero) {
+// `fix(r, column)` changes 32 columns before.
+template <int kCols, class Fix>
+__device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloat16* dst, bool store, bool zero, Fix&& fix) {
     uint4* d4 = reinterpret_cast<uint4*>(dst);
 #pragma unroll 1
     for (int cb = 0; cb < kCols / 32; ++cb) {
         uint32_t r[32];
         ptx::tmem_ld32(taddr + cb * 32, r);
         if (!store) continue;
+        fix(r, cb * 32);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 v;
@@ -130,14 +134,15 @@ __device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloa
 }
 
 // The same as fp32, as they are: a part's sums.
-template <int kCols>
-__device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool store) {
+template <int kCols, class Fix>
+__device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool store, Fix&& fix) {
     float4* d4 = reinterpret_cast<float4*>(dst);
 #pragma unroll 1
     for (int cb = 0; cb < kCols / 32; ++cb) {
         uint32_t r[32];
         ptx::tmem_ld32(taddr + cb * 32, r);
         if (!store) continue;
+        fix(r, cb * 32);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             d4[cb * 8 + j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
@@ -220,7 +225,8 @@ struct DqCfg {
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kQueueOff = kMiscOff + 16;
     static constexpr int kXchOff = kQueueOff + kItemQ * int(sizeof(QWork));  // [2 halves][128 rows]
-    static constexpr int kSmemBytes = kXchOff + 1024 + 1024;
+    static constexpr int kLostOff = kXchOff + 1024;  // kLostWords
+    static constexpr int kSmemBytes = kLostOff + 4 * packed::kLostWords + 1024;
     static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     static constexpr uint32_t kColS0 = 0, kColDP = 256, kColDQ = 384;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -252,6 +258,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t item_full0 = xb + 64, item_empty0 = xb + 64 + 8 * kItemQ;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    volatile uint32_t* lost = reinterpret_cast<volatile uint32_t*>(smem + C::kLostOff);
     QWork* item_q = reinterpret_cast<QWork*>(smem + C::kQueueOff);
 
     if (threadIdx.x == 0) {
@@ -276,6 +283,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ptx::mbar_init(item_empty0 + 8u * q, kItemConsumers);
         }
         *abort_flag = 0;
+        for (int i = 0; i < packed::kLostWords; ++i) lost[i] = 0;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
     }
@@ -458,8 +466,14 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const int key = (q.c0 + j) * 128;  // the chunk's first
                 const int seen = limit - (key + 64 * h);  // keys of this half that the row sees
                 const bool masked = warp_limit < key + 64 * h + 64;
-                if (key + 128 > q.nkeys)  // the sequence's last chunk: S has read K, dQ has not
-                    zero_rows<D>(smem + C::kKOff + (step % KS) * C::kBlk, q.nkeys - key, threadIdx.x);
+                if (key + 128 > q.limit0) {  // keys that some row does not see: S has read K, dQ has not
+                    if (!wait_bw(k_full(int(step % KS)), (step / KS) & 1u, abort_flag, p)) good = false;  // (has been)
+                    uint8_t* kblk = smem + C::kKOff + (step % KS) * C::kBlk;
+                    const int dead = min(128, max(0, (p.causal ? min(q.nkeys, q.limit0 + q.ntok - 1) : q.nkeys) - key));
+                    if (packed::scrub_rows<D / 64>(kblk, kBoxBytes, max(0, q.limit0 - key), dead, threadIdx.x, 256))
+                        lost[kq % packed::kLostWords] = kq + 1;
+                    zero_rows<D>(kblk, dead, threadIdx.x);
+                }
                 float pr[64];
                 {
                     uint32_t sr[64];
@@ -533,14 +547,20 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!__all_sync(~0u, wait_bw(dq_full, dqc & 1u, abort_flag, p))) break;
             ++dqc;
             ptx::tc_fence_after();
+            const bool fix = lost[kq % packed::kLostWords] == kq + 1;
+            const int lo = max(max(q.limit0, 0), q.c0 * 128), seen = min(limit, (q.c0 + n) * 128) - lo;
+            auto put_back = [&](uint32_t (&r)[32], int col) {
+                if (fix)
+                    packed::restore(r, p.k.p + (q.key0 + int64_t(lo)) * p.k.ts + hk * p.k.hs + (D / 2) * h + col, p.k.ts, seen);
+            };
             if (q.slot >= 0)
                 store_part<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h,
-                                  p.v.parts + (int64_t(q.slot) * K + hk) * (128 * D) + row * D + (D / 2) * h, real);
+                                  p.v.parts + (int64_t(q.slot) * K + hk) * (128 * D) + row * D + (D / 2) * h, real, put_back);
             else
                 store_cols<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h, p.scale,
                               p.out_a.p + int64_t(q.tok0 + r_tok) * p.out_a.ts + (hk * p.group + r_head) * p.out_a.hs +
                                   (D / 2) * h,
-                              real, limit <= 0);
+                              real, limit <= 0, put_back);
             ptx::tc_fence_before();
             gs += uint32_t(n);
         }
@@ -574,7 +594,8 @@ struct DkvCfg {
     static constexpr int kNumBars = 2 * kStages + 8 + 2 * kItemQ;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kQueueOff = kMiscOff + 16;
-    static constexpr int kSmemBytes = kQueueOff + kItemQ * int(sizeof(QWork)) + 1024;
+    static constexpr int kLostOff = kQueueOff + kItemQ * int(sizeof(QWork));  // kLostWords
+    static constexpr int kSmemBytes = kLostOff + 4 * packed::kLostWords + 1024;
     static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     static constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 256 + D;
     static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
@@ -605,6 +626,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto stage_off = [&](int r) { return C::kStageOff + r * C::kStageBytes; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    volatile uint32_t* lost = reinterpret_cast<volatile uint32_t*>(smem + C::kLostOff);
     KWork* item_q = reinterpret_cast<KWork*>(smem + C::kQueueOff);
     const int rows_used = (128 / p.group) * p.group;  // rows of a query block's box
 
@@ -626,6 +648,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ptx::mbar_init(item_empty0 + 8u * q, kItemConsumers);
         }
         *abort_flag = 0;
+        for (int i = 0; i < packed::kLostWords; ++i) lost[i] = 0;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
     }
@@ -800,7 +823,19 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const bool ragged = rows < rows_used;
                 // query rows [from, to) of this half see this thread's key
                 const int from = (p.causal ? p.group * max(0, kb.pos + row - limit0 + 1) : 0) - 64 * h, to = rows - 64 * h;
-                const bool masked = ragged || (p.causal && kb.pos + 127 >= limit0);
+                const bool diagonal = p.causal && kb.pos + 127 >= limit0, masked = ragged || diagonal;
+                // rows that do not see every key of the block
+                const int partly = diagonal ? min(rows, p.group * (kb.pos + 128 - limit0)) : 0;
+                if (__any_sync(~0u, packed::any_lost<D / 64>(st + C::kStDO, kBoxBytes, 0, partly, threadIdx.x, 256))) {
+                    // dP must have read them first
+                    if (!__all_sync(~0u, wait_bw(dp_full, step & 1u, abort_flag, p))) {
+                        ok = false;
+                        break;
+                    }
+                    packed::scrub_rows<D / 64>(st + C::kStDO, kBoxBytes, 0, partly, threadIdx.x, 256);
+                    lost[kq % packed::kLostWords] = kq + 1;
+                    ptx::fence_proxy_async_smem();
+                }
                 if (ragged) zero_rows<D>(st + C::kStDO, rows, threadIdx.x);
                 // per-column constants, 16-byte broadcast loads
                 const float4* cl = reinterpret_cast<const float4*>(st + C::kStL) + 16 * h;
@@ -837,6 +872,10 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(p_full);
+                if (packed::scrub_rows<D / 64>(st + C::kStQ, kBoxBytes, 0, partly, threadIdx.x, 256)) {
+                    lost[kq % packed::kLostWords] = kq + 1;
+                    ptx::fence_proxy_async_smem();
+                }
                 if (ragged) zero_rows<D>(st + C::kStQ, rows, threadIdx.x);
                 if (!__all_sync(~0u, wait_bw(dp_full, step & 1u, abort_flag, p))) {
                     ok = false;
@@ -847,10 +886,6 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 {
                     uint32_t dr[64];
                     ptx::tmem_ld64(tdp, dr);
-                    if (masked)
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (i < from || i >= to) dr[i] = 0u;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float4 dd = cd[i];
@@ -868,6 +903,12 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         pk[2 * i] = ptx::pack_bf16x2(t0, t1);
                         pk[2 * i + 1] = ptx::pack_bf16x2(t2, t3);
                     }
+                    if (masked)  // (selected last: dP and D of a row may be anything)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (2 * i < from || 2 * i >= to) pk[i] &= 0xffff0000u;
+                            if (2 * i + 1 < from || 2 * i + 1 >= to) pk[i] &= 0xffffu;
+                        }
                 }
                 ptx::tmem_st32(tdp, pk);
                 ptx::tmem_wait_st();
@@ -881,18 +922,30 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ptx::tc_fence_after();
             const bool real = row < kb.nkeys;
             const int64_t tok = kb.key0 + row;
+            // Tokens whose rows may have lost something and see this thread's key: a token that sees `limit`
+            // keys is the (limit - limit0)-th from the walk's first.
+            const bool fix = n > 0 && lost[kq % packed::kLostWords] == kq + 1;
+            auto put_back = [&](const Rows& x, uint32_t (&r)[32], int col) {
+                if (!fix) return;
+                const QBlock b0 = p.v.qblocks[kb.q0], b1 = p.v.qblocks[kb.q0 + n - 1];
+                const int lo = max(kb.pos + row + 1, b0.limit0), hi = min(kb.pos + 127, b1.limit0 + b1.ntok - 1);
+                for (int t = lo; t <= hi; ++t)
+                    packed::restore(r, x.p + (int64_t(b0.tok0) + t - b0.limit0) * x.ts + hk * p.group * x.hs + (D / 2) * h + col,
+                                    x.hs, p.group);
+            };
+            auto back_q = [&](uint32_t (&r)[32], int col) { put_back(p.q, r, col); };
+            auto back_do = [&](uint32_t (&r)[32], int col) { put_back(p.dout, r, col); };
+            const uint32_t t_dk = tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h;
+            const uint32_t t_dv = tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h;
             if (kb.slot >= 0) {
                 float* part = p.v.parts + (int64_t(kb.slot) * K + hk) * (2 * 128 * D) + row * D + (D / 2) * h;
-                store_part<D / 2>(tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h, part, real);
-                store_part<D / 2>(tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h, part + 128 * D, real);
-                ptx::tc_fence_before();
-                gs += uint32_t(n);
-                continue;
+                store_part<D / 2>(t_dk, part, real, back_q);
+                store_part<D / 2>(t_dv, part + 128 * D, real, back_do);
+            } else {
+                store_cols<D / 2>(t_dv, 1.0f, p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + (D / 2) * h, real, n == 0, back_do);
+                store_cols<D / 2>(t_dk, p.scale, p.out_a.p + tok * p.out_a.ts + hk * p.out_a.hs + (D / 2) * h, real, n == 0,
+                                  back_q);
             }
-            store_cols<D / 2>(tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h, 1.0f,
-                              p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + (D / 2) * h, real, n == 0);
-            store_cols<D / 2>(tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h, p.scale,
-                              p.out_a.p + tok * p.out_a.ts + hk * p.out_a.hs + (D / 2) * h, real, n == 0);
             ptx::tc_fence_before();
             gs += uint32_t(n);
         }
@@ -1004,7 +1057,7 @@ cudaError_t launch_bwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     float* neg_l = reinterpret_cast<float*>(ws + w.neg_l);
     float* neg_d = reinterpret_cast<float*>(ws + w.neg_d);
     BwdParams bp{view, p.kv_heads, p.group, p.causal, neg_l, neg_d, dq, dq, p.scale, p.scale * kLog2e,
-                 uint32_t(p.group * tpb) * 128u, p.status, p.waits.timeout_ns, p.waits.inject};
+                 uint32_t(p.group * tpb) * 128u, p.status, p.waits.timeout_ns, p.waits.inject, q, k, dout};
     constexpr int kDq = smem_launch(DqCfg<D>::kSmemBytes), kDkv = smem_launch(DkvCfg<D>::kSmemBytes);
     e = cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDq);
     if (e == cudaSuccess)

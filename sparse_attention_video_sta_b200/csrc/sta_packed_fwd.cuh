@@ -29,12 +29,27 @@ struct FwdParams {
     int32_t self;  // no lists
     int32_t kv_heads, group, causal, tokens_q;
     Rows o;
+    Rows vals;  // V
     float* lse;
     float scale, scale_log2;
     uint32_t q_box_bytes;  // bytes of one box of a query block: group * (128 / group) rows of 128 bytes
     uint32_t* status;
     uint64_t timeout_ns;
 };
+
+// The chunk of a walk's V from which on its rows need care: those that some row of the block does not
+// see.  Within such a chunk (its first key `key`) rows from `dead` on are seen by none, and are zeroed;
+// those in [hidden, dead) are seen by some, and lose what is not finite.
+__device__ __forceinline__ int32_t first_care(const QWork& q) { return max(0, (max(q.limit0, 0) >> 7) - q.c0); }
+__device__ __forceinline__ int dead_from(const QWork& q, int32_t causal, int key) {
+    return min(128, max(0, (causal ? min(q.nkeys, q.limit0 + q.ntok - 1) : q.nkeys) - key));
+}
+__device__ __forceinline__ int hidden_from(const QWork& q, int key) { return max(0, q.limit0 - key); }
+// Rows [lo, lo + n) of V, from q.key0, that may have lost something and that a row of the result sees.
+__device__ __forceinline__ int lost_seen(const QWork& q, int limit, int& lo) {
+    lo = max(max(q.limit0, 0), q.c0 * 128);
+    return min(limit, (q.c0 + q.n) * 128) - lo;
+}
 
 // Scores of the 64 keys of a half row from index `n` on to -inf.
 __device__ __forceinline__ void mask_from(uint32_t (&sr)[64], int n) {

@@ -60,7 +60,8 @@ struct PairCfg {
     static constexpr int kSlotBars = 2 + 4 * kStages + 5 + 2 * kItemQ;
     static constexpr int kQueueOff = kBarOff + (2 * kSlotBars + 1) / 2 * 16;
     static constexpr int kMiscOff = kQueueOff + 2 * kItemQ * int(sizeof(QWork));  // tmem base slot, abort flag
-    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+    static constexpr int kLostOff = kMiscOff + 16;  // of each slot kLostWords
+    static constexpr int kSmemBytes = kLostOff + 2 * 4 * packed::kLostWords + 1024;
     static constexpr uint32_t kColO = 256;
     static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -92,6 +93,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     auto item_empty = [&](int q) { return xb + 40 + 8u * (kItemQ + q); };
     QWork* item_q = reinterpret_cast<QWork*>(smem + C::kQueueOff) + slot * kItemQ;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile uint32_t* lost = reinterpret_cast<volatile uint32_t*>(smem + C::kLostOff) + slot * packed::kLostWords;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     const uint32_t q_at = base + uint32_t(slot) * C::kSlotBytes, k_at = q_at + C::kBlk, v_at = k_at + S * C::kBlk;
     auto wait_bar = [&](uint32_t bar, uint32_t parity) {
@@ -122,6 +124,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             ptx::mbar_init(item_empty(q), kConsumers);
         }
         if (slot == 0) *abort_flag = 0;
+        for (int i = 0; i < packed::kLostWords; ++i) lost[i] = 0;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
         ptx::prefetch_tensormap(&tm_q);
@@ -290,18 +293,6 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 ptx::tmem_ld64(mS, s0);
                 ptx::tmem_ld64(mS + 64, s1);
                 const int key = (q.c0 + i) * 128;
-                if (key + 128 > q.nkeys) {
-                    // the sequence's last chunk: V rows behind its last key (the V in flight or here is this
-                    // chunk's: the one before was read by a product that s_full has waited for)
-                    const int r = int(g % S);
-                    if (!__all_sync(~0u, wait_bar(v_full(r), (g / S) & 1u))) { ok = false; break; }
-                    uint8_t* v0 = smem + (v_at - base) + r * C::kBlk;
-                    for (int j = (q.nkeys - key) * 8 + row; j < 128 * 8; j += 128)
-#pragma unroll
-                        for (int cb = 0; cb < C::kColBlocks; ++cb)
-                            *reinterpret_cast<uint4*>(v0 + cb * kBoxBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    ptx::fence_proxy_async_smem();
-                }
                 // 32 keys at a time: masked where some row's limit falls in them, left out where every row's has passed
                 const bool cut = key + 128 > least;
                 float mx;
@@ -360,6 +351,21 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     if (key + 96 < most) l += softmax_exp32<32>(s1, c, m, pk);
                 }
                 ptx::tmem_st32(mS + 32, pk);
+                if (i >= first_care(q)) {
+                    // V rows that no row sees, or not every one (the V in flight or here is this chunk's: the
+                    // one before was read by a product that s_full has waited for)
+                    const int r = int(g % S);
+                    if (!__all_sync(~0u, wait_bar(v_full(r), (g / S) & 1u))) { ok = false; break; }
+                    uint8_t* v0 = smem + (v_at - base) + r * C::kBlk;
+                    const int dead = dead_from(q, p.causal, key);
+                    for (int j = dead * 8 + row; j < 128 * 8; j += 128)
+#pragma unroll
+                        for (int cb = 0; cb < C::kColBlocks; ++cb)
+                            *reinterpret_cast<uint4*>(v0 + cb * kBoxBytes + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    if (packed::scrub_rows<C::kColBlocks>(v0, kBoxBytes, hidden_from(q, key), dead, row, 128))
+                        lost[kq % packed::kLostWords] = kq + 1;
+                    ptx::fence_proxy_async_smem();
+                }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -372,12 +378,17 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             const bool none = l == 0.0f;  // no visible key: O = 0, whatever TMEM holds
             const int32_t head = q.hk * p.group + r_head;
             const int64_t tok = q.tok0 + r_tok;
+            const bool fix = real && lost[kq % packed::kLostWords] == kq + 1;
+            int lo;
+            const int seen = lost_seen(q, limit, lo);
+            const __nv_bfloat16* seen_v = p.vals.p + (q.key0 + int64_t(lo)) * p.vals.ts + q.hk * p.vals.hs;
             if (q.slot >= 0) {
                 float* part = p.v.parts + (int64_t(q.slot) * K + q.hk) * (128 * (D + 2));
 #pragma unroll 1
                 for (int cb = 0; cb < D / 32; ++cb) {
                     uint32_t orr[32];
                     ptx::tmem_ld32(mO + cb * 32, orr);
+                    if (fix) packed::restore(orr, seen_v + cb * 32, p.vals.ts, seen);
                     float4* d4 = reinterpret_cast<float4*>(part + row * D + cb * 32);
                     if (real)
 #pragma unroll
@@ -395,6 +406,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 for (int cb = 0; cb < D / 64; ++cb) {  // 64 columns (128 bytes) of the warp's 32 rows at a time
                     uint32_t orr[64];
                     ptx::tmem_ld64(mO + cb * 64, orr);
+                    if (fix) packed::restore(orr, seen_v + cb * 64, p.vals.ts, seen);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         uint32_t pk[4];

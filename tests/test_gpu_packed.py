@@ -443,3 +443,64 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_calls_are_clean(sta, lens
         sta.sta_debug_inject_operator_timeout(0)
     assert all(torch.equal(a, b) for a, b in zip(both(), want))
     assert sta.sta_operator_status() == 0
+
+
+HIDDEN = [  # query lengths, key lengths, heads, key heads, d
+    ([300, 77], [300, 77], 4, 4, 128), ([300, 77], [300, 77], 12, 4, 128), ([260, 9], [260, 9], 16, 2, 64),
+    ([1500], [1500], 6, 2, 128), ([1000, 1000], [1000, 1000], 24, 8, 128), ([4000], [4000], 4, 4, 64),
+    ([50, 200], [333, 120], 8, 2, 128), ([30], [30], 32, 1, 64),
+]
+
+
+def poison(t, head, row, elements):
+    t = t.clone()
+    for c, x in elements:
+        t[row, head, c] = x
+    return t
+
+
+@pytest.mark.parametrize("nq,nk,H,K,d", HIDDEN, ids=lambda x: str(x).replace(" ", ""))
+def test_what_a_causal_mask_hides_does_not_count(sta, nq, nk, H, K, d):
+    """Infinities and NaN in tokens that a query does not see leave its results as they were, bit for bit, and so
+    do those of a query for the keys that it does not see; whoever sees them gets them, in their column."""
+    q, k, v, do = make(nq, nk, H, K, d, seed=31)
+    cq, ck = ref.cu_of(nq), ref.cu_of(nk)
+    G = H // K
+    run = lambda q, k, v, do: (lambda o, l: (o, l) + sta.sta_packed_attention_backward(q, k, v, o, l, do, cq, ck))(
+        *sta.sta_packed_attention(q, k, v, cq, ck))
+    o0, l0, dq0, dk0, dv0 = run(q, k, v, do)
+    odd = [(3, math.inf), (d - 1, math.nan), (17, -math.inf)]
+    cols = [c for c, _ in odd]
+    rest = [c for c in range(d) if c not in cols]
+    hk = K - 1
+    heads = list(range(hk * G, hk * G + G))
+    others = [h for h in range(H) if h not in heads]
+    a, ka = 0, 0
+    for n, m in zip(nq, nk):
+        first = max(0, m - n)  # the first query's own key
+        for t in sorted({0, m // 2, m - 1, max(0, m - 2), min(m - 1, 129)}):
+            sees = max(0, min(n, t - (m - n)))  # queries from this one on see key t
+            rows, before = slice(a + sees, a + n), slice(a, a + sees)
+            o, l, dq, dk, dv = run(q, k, poison(v, hk, ka + t, odd), do)
+            assert torch.equal(l, l0) and torch.equal(o[:, others], o0[:, others])
+            assert torch.equal(o[before], o0[before]) and torch.equal(dq[before], dq0[before])
+            assert torch.equal(o[rows][:, heads][..., rest], o0[rows][:, heads][..., rest])
+            assert not o[rows][:, heads][..., cols].isfinite().any()
+            o, l, dq, dk, dv = run(q, poison(k, hk, ka + t, odd), v, do)
+            assert torch.equal(o[before], o0[before]) and torch.equal(dq[before], dq0[before])
+            assert torch.equal(dq[:, others], dq0[:, others]) and torch.equal(l[:, before], l0[:, before])
+            assert not dq[rows][:, heads].isfinite().any()
+        for i in sorted({0, n // 2, n - 1, min(n - 1, 43)}):
+            seen = max(0, min(m, i + m - n + 1))
+            h = heads[-1]
+            behind, upto = slice(ka + seen, ka + m), slice(ka, ka + seen)
+            _, _, _, dk, dv = run(q, k, v, poison(do, h, a + i, odd))
+            assert torch.equal(dk[behind], dk0[behind]) and torch.equal(dv[behind], dv0[behind])
+            assert torch.equal(dv[upto, hk][:, rest], dv0[upto, hk][:, rest])
+            assert not dv[upto, hk][:, cols].isfinite().any() and not dk[upto, hk].isfinite().any()
+            keep = [x for x in range(K) if x != hk]
+            assert torch.equal(dk[:, keep], dk0[:, keep]) and torch.equal(dv[:, keep], dv0[:, keep])
+            _, _, _, dk, dv = run(poison(q, h, a + i, [(3, math.nan), (8, math.inf)]), k, v, do)
+            assert torch.equal(dk[behind], dk0[behind]) and torch.equal(dv[behind], dv0[behind])
+            assert not dv[upto, hk].isfinite().any() and not dk[upto, hk].isfinite().any()
+        a, ka = a + n, ka + m
