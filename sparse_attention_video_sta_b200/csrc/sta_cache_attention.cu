@@ -181,6 +181,8 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Bit 7 of each byte that is a NaN code of e4m3 (S.1111.111).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
@@ -523,14 +525,17 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 }
             }
             if (__any_sync(~0u, rise)) {
-                // raise the maxima to this tile's, and rescale
+                // raise the maxima of the rows that need it to this tile's, and rescale (of those alone: what a row
+                // comes to does not depend on other rows)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
 #pragma unroll
                         for (int k = 4; k <= 16; k <<= 1) x[nt][i] = fmaxf(x[nt][i], __shfl_xor_sync(~0u, x[nt][i], k));
-                        const float mn = fmaxf(m[nt][i], x[nt][i]), wn = fmaxf(mw[nt][i], x[nt][i] + mt.y);
+                        const bool up = x[nt][i] > m[nt][i] + kRise || x[nt][i] + mt.y > mw[nt][i] + kRise;
+                        const float mn = up ? fmaxf(m[nt][i], x[nt][i]) : m[nt][i];
+                        const float wn = up ? fmaxf(mw[nt][i], x[nt][i] + mt.y) : mw[nt][i];
                         const float cf = ptx::ex2(mw[nt][i] - wn);
                         l[nt][i] *= ptx::ex2(m[nt][i] - mn);
                         m[nt][i] = mn;
@@ -589,6 +594,42 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             phase ^= slot_out == 0 ? 1u : 0u;
             --in_flight;
             if (next < t1) issue(next++);
+            if (masked) {
+                // NaN codes in a tile that not every row sees whole: out of the products; another product counts for
+                // each sum those that its row does see
+                uint32_t bad[4][D / 32], any = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) any |= bad[i][j] = nan_codes(v[i][j]) >> 7;  // 1 in their bytes
+                if (__any_sync(~0u, any != 0u)) {
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            constexpr uint32_t kOne = 0x38;  // 1.0 in e4m3
+                            const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
+                            const uint32_t lo = __byte_perm(bad[0][j], bad[1][j], sel) * kOne,
+                                           hi = __byte_perm(bad[2][j], bad[3][j], sel) * kOne;
+                            const uint32_t is_nan[4] = {ops::e4m3_half2(uint16_t(lo)), ops::e4m3_half2(uint16_t(lo >> 16)),
+                                                        ops::e4m3_half2(uint16_t(hi)), ops::e4m3_half2(uint16_t(hi >> 16))};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                auto sees = [&](int i) { return tok + g + (i >> 1) * 8 < limit[nt][i & 1] ? 1.0f : 0.0f; };
+                                float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma16816(count, is_nan, transpose8x8(half2_of(sees(0), sees(1))),
+                                         transpose8x8(half2_of(sees(2), sees(3))));
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (count[i] > 0.0f) o[nt][2 * j + h][i] = __uint_as_float(0x7fc00000u);
+                            }
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) v[i][j] &= ~(bad[i][j] * 0xffu);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < D / 32; ++j)
 #pragma unroll

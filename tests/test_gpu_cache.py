@@ -331,6 +331,38 @@ def test_attention_never_reads_behind_the_last_token(sta):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("heads,K,d", [(4, 4, 64), (8, 2, 128), (24, 1, 128)])
+@pytest.mark.parametrize("held,drafts", [(9, 9), (40, 6), (2000, 17)])
+def test_attention_drafts_that_a_query_does_not_see_do_not_count(sta, held, drafts, heads, K, d):
+    """NaN in a drafted token's keys or values: the queries before it keep their bits; those that see it have NaN, from
+    its values in that column alone."""
+    lengths, bt = [held, 33], 16
+    kc, vc, ks, vs, table = filled_cache(lengths, K, bt, d, seed=held)
+    lens_q = [drafts, 1]
+    q = torch.randn(drafts + 1, heads, d, generator=torch.Generator("cuda").manual_seed(3), device="cuda").bfloat16()
+    n, cu = torch.tensor(lengths, dtype=torch.int32, device="cuda"), ref.cu_of(lens_q)
+    want, want_lse = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n, cu)
+    hk, c = K - 1, d - 5
+    mine = torch.arange(hk * (heads // K), (hk + 1) * (heads // K), device="cuda")
+    rest = [x for x in range(d) if x != c]
+    for i in {0, drafts // 2, drafts - 1}:
+        pos = held - drafts + i
+        at = (int(table[0, pos // bt]), hk, pos % bt)
+        for code in (0x7f, 0xff):
+            bad = vc.clone()
+            bad.view(torch.uint8)[at + (c,)] = code
+            o, lse = sta.sta_cache_attention(q, kc, bad, ks, vs, table, n, cu)
+            assert torch.equal(lse, want_lse)
+            sees = torch.zeros_like(o, dtype=torch.bool)
+            sees[i:drafts, mine, c] = True
+            assert torch.equal(torch.where(sees, 0, o), torch.where(sees, 0, want)) and bool(o[sees].isnan().all())
+            bad = kc.clone()
+            bad.view(torch.uint8)[at + (c,)] = code
+            o, lse = sta.sta_cache_attention(q, bad, vc, ks, vs, table, n, cu)
+            sees[i:drafts, mine] = True
+            assert torch.equal(torch.where(sees, 0, o), torch.where(sees, 0, want)) and bool(o[sees].isnan().all())
+
+
 def test_attention_blocks_out_of_the_pool_are_not_seen(sta):
     lengths, K, bt, d = [100, 64], 1, 16, 64
     kc, vc, ks, vs, table = filled_cache(lengths, K, bt, d, seed=5)
