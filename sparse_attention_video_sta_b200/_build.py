@@ -65,7 +65,7 @@ def _torch_command(out: str):
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
             *[a for i in inc for a in ("-isystem", i)], TORCH_SOURCE, "-o", out, "-L", os.path.join(torch_dir, "lib"),
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
 def _torch_up_to_date() -> bool:

@@ -441,7 +441,7 @@ sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* 
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
     return op_cuda_status(cudaLaunchKernelEx(&cfg, cache_extend_kernel, p));
 }
 

@@ -7,6 +7,7 @@
 // given the addresses of its entry points, so it serves whichever build of the
 // library the package has loaded.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -109,8 +110,14 @@ float* lse_ptr(const Tensor& lse, const at::Device& dev, int64_t heads, int64_t 
     return static_cast<float*>(lse.data_ptr());
 }
 
+// New memory from the current stream's pool (not through the dispatcher: 0.5 us less for each).
+Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Device& dev) {
+    return Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+}
+Tensor like(const Tensor& t) { return fresh(t.sizes(), t.scalar_type(), t.device()); }
+
 Tensor scratch(const OptTensor& given, int64_t need, const at::Device& dev) {
-    if (!given.has_value()) return need == 0 ? Tensor() : at::empty({need}, at::TensorOptions(dev).dtype(at::kByte));
+    if (!given.has_value()) return need == 0 ? Tensor() : fresh({need}, at::kByte, dev);
     const Tensor& w = *given;
     if (w.device() != dev || w.scalar_type() != at::kByte || !w.is_contiguous() || w.numel() < need)
         bad("workspace must be a contiguous uint8 tensor of at least " + std::to_string(need) + " bytes on " + dev.str());
@@ -132,8 +139,6 @@ sta_packed problem(const Tensor& q, const Tensor& k, const Tensor& cu_q, const O
                       cq, ck, causal ? 1 : 0, clear_tail ? 1 : 0,
                       scale.has_value() ? float(*scale) : float(1.0 / std::sqrt(double(q.size(2))))};
 }
-
-Tensor like(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
 
 void packed_forward(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& o, const Tensor& lse, const Tensor& cu_q,
                     const OptTensor& cu_k, bool causal, const std::optional<double>& scale, bool clear_tail,
@@ -157,7 +162,8 @@ std::tuple<Tensor, Tensor> packed_attention(const Tensor& q, const Tensor& k, co
                                             const OptTensor& cu_k, bool causal, const std::optional<double>& scale,
                                             int64_t stream) {
     if (q.dim() != 3) bad("q must be [tokens, heads, d]");
-    const Tensor o = like(q), lse = at::empty({q.size(1), q.size(0)}, q.options().dtype(at::kFloat));
+    const at::Device dev = cuda_device("q", q);
+    const Tensor o = like(q), lse = fresh({q.size(1), q.size(0)}, at::kFloat, dev);
     packed_forward(q, k, v, o, lse, cu_q, cu_k, causal, scale, true, std::nullopt, stream);
     if (stream >= 0) {
         const On on(q.device(), stream);
@@ -190,6 +196,7 @@ std::tuple<Tensor, Tensor, Tensor> packed_attention_backward(const Tensor& q, co
                                                              const Tensor& lse, const Tensor& dout, const Tensor& cu_q,
                                                              const OptTensor& cu_k, bool causal,
                                                              const std::optional<double>& scale, int64_t stream) {
+    for (const auto& [name, t] : {std::pair{"q", q}, std::pair{"k", k}, std::pair{"v", v}}) cuda_device(name, t);
     const Tensor dq = like(q), dk = like(k), dv = like(v);
     packed_backward(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, causal, scale, true, std::nullopt, stream);
     if (stream >= 0) {
@@ -261,15 +268,15 @@ std::tuple<Tensor, Tensor> cache_attention(const Tensor& q, const Tensor& kc, co
     const int32_t* cp = cu_q.has_value() ? vec<int32_t>("cu_q", *cu_q, dev, B + 1) : nullptr;
     if (cp == nullptr && T != B) bad(std::to_string(T) + " queries for " + std::to_string(B) + " sequences: give cu_q");
     const Tables t = tables(block_tables, B, dev);
-    const bool fresh = !o_given.has_value();
-    const Tensor o = fresh ? like(q) : *o_given;
-    const Tensor lse = lse_given.has_value() ? *lse_given : at::empty({H, T}, q.options().dtype(at::kFloat));
-    const sta_packed p{int32_t(B), int32_t(H), c.kv_heads, int32_t(d), T, 0, cp, nullptr, 1, fresh ? 1 : 0,
+    const bool new_o = !o_given.has_value();
+    const Tensor o = new_o ? fresh(q.sizes(), at::kBFloat16, dev) : *o_given;
+    const Tensor lse = lse_given.has_value() ? *lse_given : fresh({H, T}, at::kFloat, dev);
+    const sta_packed p{int32_t(B), int32_t(H), c.kv_heads, int32_t(d), T, 0, cp, nullptr, 1, new_o ? 1 : 0,
                        scale.has_value() ? float(*scale) : float(1.0 / std::sqrt(double(d)))};
     const sta_rows rq = rows("q", q, dev, T, H, d), ro = rows("o", o, dev, T, H, d);
     float* lsp = lse_ptr(lse, dev, H, T);
     if (T == 0 || B == 0) {
-        if (fresh) {
+        if (new_o) {
             o.zero_();
             lse.fill_(-INFINITY);
         }
@@ -281,7 +288,7 @@ std::tuple<Tensor, Tensor> cache_attention(const Tensor& q, const Tensor& kc, co
     const Tensor w = scratch(workspace, need, dev);
     call("sta_cache_attention", f_cache_attention, &c, &p, lp, t.p, t.width, t.stride, &rq, &ro, lsp, ptr(w), bytes(w), on.handle);
     on.keep(w);
-    if (fresh) on.keep(o);
+    if (new_o) on.keep(o);
     if (!lse_given.has_value()) on.keep(lse);
     return {o, lse};
 }
@@ -302,9 +309,9 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor> cache_extend(const Tensor& ne
     int32_t* cp = vec<int32_t>("free_count", free_count, dev, 1);
     const Tables t = tables(block_tables, B, dev);
     const On on(dev, stream);
-    const at::TensorOptions ints = lengths.options();
-    const Tensor slots = at::empty({std::max<int64_t>(max_slots, 0)}, ints.dtype(at::kLong)), cu = at::empty({B + 1}, ints), brief = at::empty({1}, ints);
-    const Tensor len_out = in_place ? lengths : at::empty({B}, ints), count_out = in_place ? free_count : at::empty({1}, ints);
+    const Tensor slots = fresh({std::max<int64_t>(max_slots, 0)}, at::kLong, dev), cu = fresh({B + 1}, at::kInt, dev),
+                 brief = fresh({1}, at::kInt, dev);
+    const Tensor len_out = in_place ? lengths : fresh({B}, at::kInt, dev), count_out = in_place ? free_count : fresh({1}, at::kInt, dev);
     call("sta_cache_extend", f_cache_extend, int32_t(B), int32_t(block_tokens), np, lp, static_cast<int32_t*>(len_out.data_ptr()), t.p, t.width,
                          t.stride, fp, int32_t(free_blocks.size(0)), cp, static_cast<int32_t*>(count_out.data_ptr()),
                          static_cast<int64_t*>(slots.data_ptr()), max_slots, static_cast<int32_t*>(cu.data_ptr()),
