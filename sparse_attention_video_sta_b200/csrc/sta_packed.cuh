@@ -168,20 +168,9 @@ cudaError_t rows_map(CUtensorMap* m, const Rows& r, int64_t tokens, int heads, i
 // Elements of a pair of bf16 that are not finite: bit 15 for the low one, 31 for the high one.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-// Are there any in rows [from, to) of a block in shared memory (128-byte rows in boxes of `box`
-// bytes)?  `threads` threads share the rows; the answer is the caller's own part.
-template <int kBoxes>
-__device__ __forceinline__ bool any_lost(const uint8_t* blk, int box, int from, int to, int thread, int threads) {
-    uint32_t bad = 0;
-    for (int i = from * 8 + thread; i < to * 8; i += threads)
-#pragma unroll
-        for (int cb = 0; cb < kBoxes; ++cb) {
-            const uint4 x = *reinterpret_cast<const uint4*>(blk + cb * box + i * 16);
-            bad |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
-        }
-    return bad != 0;
-}
-// Sets them to zero (the caller fences the writes for the asynchronous proxy); were there any?
+// Sets those in rows [from, to) of a block in shared memory (128-byte rows in boxes of `box` bytes) to
+// zero; `threads` threads share the rows, and the caller fences the writes for the asynchronous proxy.
+// Were there any, in the caller's own part?
 template <int kBoxes>
 __device__ __forceinline__ bool scrub_rows(uint8_t* blk, int box, int from, int to, int thread, int threads) {
     bool any = false;

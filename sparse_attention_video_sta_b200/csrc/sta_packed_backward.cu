@@ -826,14 +826,26 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const bool diagonal = p.causal && kb.pos + 127 >= limit0, masked = ragged || diagonal;
                 // rows that do not see every key of the block
                 const int partly = diagonal ? min(rows, p.group * (kb.pos + 128 - limit0)) : 0;
-                if (__any_sync(~0u, packed::any_lost<D / 64>(st + C::kStDO, kBoxBytes, 0, partly, threadIdx.x, 256))) {
+                // A Q or dO row that is not finite has an LSE or a D that is not (its products with anything are not;
+                // a row that sees no key has LSE = -inf as well), so those two say whether to look.
+                bool suspect = false;
+                if (partly > 0) {
+                    const float4 l = reinterpret_cast<const float4*>(st + C::kStL)[lane];
+                    const float4 dd = reinterpret_cast<const float4*>(st + C::kStD)[lane];
+                    const float z[4] = {l.x - l.x + (dd.x - dd.x), l.y - l.y + (dd.y - dd.y), l.z - l.z + (dd.z - dd.z),
+                                        l.w - l.w + (dd.w - dd.w)};  // 0, or NaN
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) suspect |= z[i] != 0.0f && 4 * lane + i < partly;
+                    suspect = __any_sync(~0u, suspect);
+                }
+                if (suspect) {
                     // dP must have read them first
                     if (!__all_sync(~0u, wait_bw(dp_full, step & 1u, abort_flag, p))) {
                         ok = false;
                         break;
                     }
-                    packed::scrub_rows<D / 64>(st + C::kStDO, kBoxBytes, 0, partly, threadIdx.x, 256);
-                    lost[kq % packed::kLostWords] = kq + 1;
+                    if (packed::scrub_rows<D / 64>(st + C::kStDO, kBoxBytes, 0, partly, threadIdx.x, 256))
+                        lost[kq % packed::kLostWords] = kq + 1;
                     ptx::fence_proxy_async_smem();
                 }
                 if (ragged) zero_rows<D>(st + C::kStDO, rows, threadIdx.x);
@@ -872,8 +884,9 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(p_full);
-                if (packed::scrub_rows<D / 64>(st + C::kStQ, kBoxBytes, 0, partly, threadIdx.x, 256)) {
-                    lost[kq % packed::kLostWords] = kq + 1;
+                if (suspect) {
+                    if (packed::scrub_rows<D / 64>(st + C::kStQ, kBoxBytes, 0, partly, threadIdx.x, 256))
+                        lost[kq % packed::kLostWords] = kq + 1;
                     ptx::fence_proxy_async_smem();
                 }
                 if (ragged) zero_rows<D>(st + C::kStQ, rows, threadIdx.x);
