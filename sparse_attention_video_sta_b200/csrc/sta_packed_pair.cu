@@ -38,12 +38,13 @@ namespace {
 
 using namespace packed_fwd;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kLoadWarp = 8, kMmaWarp = 10;  // + slot
-constexpr uint32_t kRegsSoftmax = 208, kRegsProducer = 88;
-static_assert(128 * (2 * kRegsSoftmax + kRegsProducer) <= kThreads * 168, "register split exceeds the launch");
+constexpr int kStoreWarp = 12;
+constexpr uint32_t kRegsSoftmax = 184, kRegsProducer = 64, kRegsStore = 80;
+static_assert(128 * (2 * kRegsSoftmax + kRegsProducer + kRegsStore) <= kThreads * 128, "register split exceeds the launch");
 constexpr uint32_t kTmemCols = 512;
-constexpr int kConsumers = 1 + 4;  // of a slot's items: the issuing thread and the softmax warps
+constexpr int kConsumers = 1 + 4 + 4;  // of a slot's items: the issuing thread, the softmax and the storing warps
 // log2 by which scores may pass the running maximum before O and l are rescaled
 constexpr float kRise = 8.0f;
 
@@ -53,8 +54,9 @@ struct PairCfg {
     static constexpr int kBlk = 128 * D * 2;
     static constexpr int kStages = D == 128 ? 1 : 2;  // of K and of V, for each slot
     static constexpr int kSlotBytes = kBlk * (1 + 2 * kStages);
-    static constexpr int kStageOff = 2 * kSlotBytes;  // epilogue: 4 KB for each softmax warp
-    static constexpr int kBarOff = kStageOff + 8 * 4096;
+    static constexpr int kStageOff = 2 * kSlotBytes;  // 4 KB for each storing warp
+    static constexpr int kSumOff = kStageOff + 4 * 4096;  // l of an item's rows: [2 slots][2 items][128] fp32
+    static constexpr int kBarOff = kSumOff + 2 * 2 * 512;
     // of each slot: q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full, p_full,
     // o_full, o_empty, drain, item_full[Q], item_empty[Q]
     static constexpr int kSlotBars = 2 + 4 * kStages + 5 + 2 * kItemQ;
@@ -79,7 +81,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     const uint32_t base = (raw_base + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw_base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slot = warp < 8 ? warp >> 2 : warp & 1;
+    const int slot = warp < 8 ? warp >> 2 : warp & 1;  // (the storing warps serve both)
 
     const uint32_t bar0 = base + C::kBarOff + uint32_t(slot) * (C::kSlotBars * 8);
     const uint32_t q_full = bar0, q_empty = bar0 + 8;
@@ -217,6 +219,129 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 drain_bar(v_full(int(it % S)), (it / S) & 1u, p.timeout_ns);
             if (qi > 0) drain_bar(q_full, (qi - 1) & 1u, p.timeout_ns);
         }
+    } else if (warp >= kStoreWarp) {
+        ptx::regs_dec<kRegsStore>();
+        // ------------------------------------------------------------ O / l -> bf16
+        const int row = threadIdx.x & 127;
+        uint8_t* stage = smem + C::kStageOff + (warp - kStoreWarp) * 4096;
+        const int r_tok = row / p.group, r_head = row - r_tok * p.group;
+        uint32_t done[2] = {0u, 0u};  // items of each slot
+        bool live[2] = {true, true};
+        int32_t steps[2] = {0, 0};  // chunks of the items under way
+        uint64_t since = 0;
+        uint32_t idle = 0;
+        while (live[0] || live[1]) {
+            bool moved = false;
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {
+                if (!live[s]) continue;
+                const uint32_t kq = done[s], b = base + C::kBarOff + uint32_t(s) * (C::kSlotBars * 8) + 16 + 32 * S;
+                const uint32_t o_full_s = b + 16, o_empty_s = b + 24, full = b + 40 + 8u * (kq % kItemQ),
+                               empty = b + 40 + 8u * (kItemQ + kq % kItemQ);
+                if (!__all_sync(~0u, ptx::mbar_test_wait(full, (kq / kItemQ) & 1u))) continue;
+                const QWork* item = reinterpret_cast<const QWork*>(smem + C::kQueueOff) + s * kItemQ + kq % kItemQ;
+                steps[s] = item->n;
+                if (steps[s] < 0) {
+                    live[s] = false;
+                    steps[s] = 0;
+                    continue;
+                }
+                if (!__all_sync(~0u, ptx::mbar_test_wait(o_full_s, kq & 1u))) continue;
+                const QWork q = *item;
+                __syncwarp();
+                moved = true;
+                steps[s] = 0;
+                ++done[s];
+                if (lane == 0) ptx::mbar_arrive(empty);
+                ptx::tc_fence_after();
+                const uint32_t mO = tmem + C::kColO + uint32_t(s) * D + (uint32_t((warp & 3) * 32) << 16);
+                const bool real = r_tok < q.ntok;
+                const int limit = real ? min(q.nkeys, q.limit0 + (p.causal ? r_tok : 0)) : 0;
+                const float l = reinterpret_cast<const float*>(smem + C::kSumOff)[(s * 2 + int(kq & 1u)) * 128 + row];
+                const bool none = l == 0.0f;  // no visible key: O = 0, whatever TMEM holds
+                const int32_t head = q.hk * p.group + r_head;
+                const int64_t tok = q.tok0 + r_tok;
+                const volatile uint32_t* lost_s =
+                    reinterpret_cast<const volatile uint32_t*>(smem + C::kLostOff) + s * packed::kLostWords;
+                const bool fix = real && lost_s[kq % packed::kLostWords] == kq + 1;
+                int lo;
+                const int seen = lost_seen(q, limit, lo);
+                const __nv_bfloat16* seen_v = p.vals.p + (q.key0 + int64_t(lo)) * p.vals.ts + q.hk * p.vals.hs;
+                if (q.slot >= 0) {
+                    float* part = p.v.parts + (int64_t(q.slot) * K + q.hk) * (128 * (D + 2));
+#pragma unroll 1
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        uint32_t orr[32];
+                        ptx::tmem_ld32(mO + cb * 32, orr);
+                        if (fix) packed::restore(orr, seen_v + cb * 32, p.vals.ts, seen);
+                        float4* d4 = reinterpret_cast<float4*>(part + row * D + cb * 32);
+                        if (real)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                d4[j] = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                             : make_float4(__uint_as_float(orr[4 * j]), __uint_as_float(orr[4 * j + 1]),
+                                                           __uint_as_float(orr[4 * j + 2]), __uint_as_float(orr[4 * j + 3]));
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(o_empty_s);
+                } else {
+                    const float inv = none ? 0.0f : 1.0f / l;
+                    const uint64_t inv2 = ptx::f2(inv, inv);
+                    const int64_t out = real ? tok * p.o.ts + head * p.o.hs : -1;  // element offset of this thread's row
+#pragma unroll 1
+                    for (int cb = 0; cb < D / 64; ++cb) {  // 64 columns (128 bytes) of the warp's 32 rows at a time
+#pragma unroll
+                        for (int hc = 0; hc < 2; ++hc) {
+                            uint32_t orr[32];
+                            ptx::tmem_ld32(mO + cb * 64 + hc * 32, orr);
+                            if (fix) packed::restore(orr, seen_v + cb * 64 + hc * 32, p.vals.ts, seen);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t pk[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float o0, o1;
+                                    ptx::f2_split(ptx::f2_mul(ptx::f2(__uint_as_float(orr[8 * j + 2 * e]),
+                                                                      __uint_as_float(orr[8 * j + 2 * e + 1])), inv2),
+                                                  o0, o1);
+                                    pk[e] = none ? 0u : ptx::pack_bf16x2(o0, o1);
+                                }
+                                *reinterpret_cast<uint4*>(stage + lane * 128 + (((hc * 4 + j) ^ (lane & 7)) << 4)) =
+                                    make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            }
+                        }
+                        if (cb == D / 64 - 1) {  // O is read
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(o_empty_s);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int it = 0; it < 8; ++it) {
+                            const int r = it * 4 + (lane >> 3), j = lane & 7;
+                            const int64_t at = __shfl_sync(~0u, out, r);
+                            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ (r & 7)) << 4));
+                            if (at >= 0) *reinterpret_cast<uint4*>(p.o.p + at + cb * 64 + j * 8) = v;
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            // bounded, as every wait; an item may take its chunks' time (some 2 us each)
+            if (moved) {
+                idle = 0;
+            } else {
+                if (__any_sync(~0u, *abort_flag != 0)) break;
+                if (idle++ == 0) since = ptx::globaltimer_ns();
+                if (idle % 64 == 0 && __any_sync(~0u, ptx::globaltimer_ns() - since >
+                                                      p.timeout_ns + uint64_t(int64_t(steps[0]) + steps[1]) * 20000u)) {
+                    *abort_flag = 1;
+                    if (lane == 0) atomicOr(p.status, kDevTimeout);
+                    break;
+                }
+            }
+        }
     } else if (warp >= kMmaWarp) {
         ptx::regs_dec<kRegsProducer>();
         if (lane == 0) {
@@ -269,7 +394,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         const int row = threadIdx.x & 127;
         const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
         const uint32_t mS = tS + lane_addr, mO = tO + lane_addr;
-        uint8_t* stage = smem + C::kStageOff + warp * 4096;
+        float* sums = reinterpret_cast<float*>(smem + C::kSumOff) + slot * 256 + row;
         const float c = p.scale_log2;
         const int r_tok = row / p.group, r_head = row - r_tok * p.group;
         uint32_t g = 0;
@@ -366,76 +491,24 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                         lost[kq % packed::kLostWords] = kq + 1;
                     ptx::fence_proxy_async_smem();
                 }
+                // (read after this chunk's product; the item two before has been stored: this one's first product
+                // waited for the O of the one before)
+                if (i == q.n - 1) sums[(kq & 1u) * 128] = l;
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(p_full);
             }
             if (!ok) break;
-            // ---- epilogue: O / l -> bf16, LSE
-            if (!__all_sync(~0u, wait_bar(o_full, kq & 1u))) break;
-            ptx::tc_fence_after();
-            const bool none = l == 0.0f;  // no visible key: O = 0, whatever TMEM holds
-            const int32_t head = q.hk * p.group + r_head;
-            const int64_t tok = q.tok0 + r_tok;
-            const bool fix = real && lost[kq % packed::kLostWords] == kq + 1;
-            int lo;
-            const int seen = lost_seen(q, limit, lo);
-            const __nv_bfloat16* seen_v = p.vals.p + (q.key0 + int64_t(lo)) * p.vals.ts + q.hk * p.vals.hs;
-            if (q.slot >= 0) {
-                float* part = p.v.parts + (int64_t(q.slot) * K + q.hk) * (128 * (D + 2));
-#pragma unroll 1
-                for (int cb = 0; cb < D / 32; ++cb) {
-                    uint32_t orr[32];
-                    ptx::tmem_ld32(mO + cb * 32, orr);
-                    if (fix) packed::restore(orr, seen_v + cb * 32, p.vals.ts, seen);
-                    float4* d4 = reinterpret_cast<float4*>(part + row * D + cb * 32);
-                    if (real)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            d4[j] = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                         : make_float4(__uint_as_float(orr[4 * j]), __uint_as_float(orr[4 * j + 1]),
-                                                       __uint_as_float(orr[4 * j + 2]), __uint_as_float(orr[4 * j + 3]));
-                }
-                if (real) *reinterpret_cast<float2*>(part + 128 * D + 2 * row) = make_float2(none ? -INFINITY : m * c, l);
-            } else {
-                const float inv = none ? 0.0f : 1.0f / l;
-                const uint64_t inv2 = ptx::f2(inv, inv);
-                const int64_t out = real ? tok * p.o.ts + head * p.o.hs : -1;  // element offset of this thread's row
-#pragma unroll 1
-                for (int cb = 0; cb < D / 64; ++cb) {  // 64 columns (128 bytes) of the warp's 32 rows at a time
-                    uint32_t orr[64];
-                    ptx::tmem_ld64(mO + cb * 64, orr);
-                    if (fix) packed::restore(orr, seen_v + cb * 64, p.vals.ts, seen);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float o0, o1;
-                            ptx::f2_split(ptx::f2_mul(ptx::f2(__uint_as_float(orr[8 * j + 2 * e]),
-                                                              __uint_as_float(orr[8 * j + 2 * e + 1])), inv2),
-                                          o0, o1);
-                            pk[e] = none ? 0u : ptx::pack_bf16x2(o0, o1);
-                        }
-                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int it = 0; it < 8; ++it) {
-                        const int r = it * 4 + (lane >> 3), j = lane & 7;
-                        const int64_t at = __shfl_sync(~0u, out, r);
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ (r & 7)) << 4));
-                        if (at >= 0) *reinterpret_cast<uint4*>(p.o.p + at + cb * 64 + j * 8) = v;
-                    }
-                    __syncwarp();
-                }
-                if (real) p.lse[int64_t(head) * p.tokens_q + tok] = none ? -INFINITY : m * p.scale + logf(l);
+            if (real) {
+                const bool none = l == 0.0f;
+                if (q.slot >= 0)
+                    *reinterpret_cast<float2*>(p.v.parts + (int64_t(q.slot) * K + q.hk) * (128 * (D + 2)) + 128 * D + 2 * row) =
+                        make_float2(none ? -INFINITY : m * c, l);
+                else
+                    p.lse[int64_t(q.hk * p.group + r_head) * p.tokens_q + q.tok0 + r_tok] =
+                        none ? -INFINITY : m * p.scale + logf(l);
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(o_empty);
         }
     }
 
