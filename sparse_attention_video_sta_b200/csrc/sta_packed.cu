@@ -550,7 +550,8 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int32_t head = q.hk * p.group + r_head;
             const int64_t tok = q.tok0 + r_tok;
             uint4* dst = reinterpret_cast<uint4*>(p.o.p + tok * p.o.ts + head * p.o.hs + half * (D / 2));
-            // a part: O unnormalised in fp32, and after the rows m (in units of log2) and l
+            // a part: O unnormalised in fp32, four columns of all rows after four columns (a warp's stores are
+            // whole lines), and behind it of each row m (in units of log2) and l
             float* part = p.v.parts + (int64_t(q.slot) * K + q.hk) * (128 * (D + 2));
             const bool fix = real && lost[kq % packed::kLostWords] == kq + 1;
 #pragma unroll 1
@@ -564,11 +565,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                     p.vals.ts, seen);
                 }
                 if (q.slot >= 0) {
-                    float4* d4 = reinterpret_cast<float4*>(part + row * D + half * (D / 2) + cb * 32);
+                    float4* d4 = reinterpret_cast<float4*>(part) + (half * (D / 8) + cb * 8) * 128 + row;
                     if (real)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            d4[j] = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                            d4[j * 128] = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
                                          : make_float4(__uint_as_float(orr[4 * j]), __uint_as_float(orr[4 * j + 1]),
                                                        __uint_as_float(orr[4 * j + 2]), __uint_as_float(orr[4 * j + 3]));
                     continue;
@@ -626,43 +627,44 @@ __global__ void packed_no_keys_kernel(const PackedProblem p, const packed::View 
 
 // Bound by latency (a few microseconds beside the launch); each part is read once.
 // Joins the parts of split query blocks: O = sum 2^(m_i - m) O_i / l, in the order of the parts.
-// One warp for each row, 8 rows (of blockIdx.y) to a CTA.
+// Eight rows (of blockIdx.y) to a CTA, four columns of a row to a thread.
+constexpr int kJoinRows = 8;
 template <int D>
-__global__ void __launch_bounds__(256) packed_join_kernel(const FwdParams p) {
-    constexpr int E = D / 32;
+__global__ void __launch_bounds__(kJoinRows * D / 4) packed_join_kernel(const FwdParams p) {
     ops::grid_wait();
-    const int lane = threadIdx.x & 31, K = p.kv_heads;
+    const int K = p.kv_heads, row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
     const int64_t n = int64_t(p.v.lists->n_q) * K;
     for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
         const QBlock q = p.v.qblocks[w / K];
         const int hk = int(w % K);
-        if (q.split < 2) continue;
-        const int row = blockIdx.y * 8 + threadIdx.x / 32;
-        if (row < q.ntok * p.group) {
-            auto part = [&](int i) { return p.v.parts + (int64_t(q.slot + i) * K + hk) * (128 * (D + 2)); };
-            float m = -INFINITY, l = 0.0f, x[E] = {};
-            for (int i = lane; i < q.split; i += 32) m = fmaxf(m, part(i)[128 * D + 2 * row]);
-            for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
-            const float mu = m == -INFINITY ? 0.0f : m;
+        if (q.split < 2 || row >= q.ntok * p.group) continue;
+        const float* part = p.v.parts + (int64_t(q.slot) * K + hk) * (128 * (D + 2));
+        const int64_t step = int64_t(K) * (128 * (D + 2));
+        float m = -INFINITY;
 #pragma unroll 4
-            for (int i = 0; i < q.split; ++i) {
-                const float* src = part(i);
-                const float2 st = *reinterpret_cast<const float2*>(src + 128 * D + 2 * row);
-                const float f = ptx::ex2(st.x - mu);
-                l += st.y * f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[e] += src[row * D + lane * E + e] * f;
-            }
-            const bool none = l == 0.0f;
-            const float inv = none ? 0.0f : 1.0f / l;
-            const int64_t tok = q.tok0 + row / p.group;
-            const int head = hk * p.group + row % p.group;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o.p + tok * p.o.ts + head * p.o.hs + lane * E);
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) dst[e] = none ? 0u : ptx::pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
-            if (lane == 0)
-                p.lse[int64_t(head) * p.tokens_q + tok] = none ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+        for (int i = 0; i < q.split; ++i) m = fmaxf(m, part[i * step + 128 * D + 2 * row]);
+        const float mu = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f, x[4] = {};
+#pragma unroll 4
+        for (int i = 0; i < q.split; ++i) {
+            const float* src = part + i * step;
+            const float2 st = *reinterpret_cast<const float2*>(src + 128 * D + 2 * row);
+            const float4 o = reinterpret_cast<const float4*>(src)[c4 * 128 + row];
+            const float f = ptx::ex2(st.x - mu);
+            l += st.y * f;
+            x[0] += o.x * f;
+            x[1] += o.y * f;
+            x[2] += o.z * f;
+            x[3] += o.w * f;
         }
+        const bool none = l == 0.0f;
+        const float inv = none ? 0.0f : 1.0f / l;
+        const int64_t tok = q.tok0 + row / p.group;
+        const int head = hk * p.group + row % p.group;
+        *reinterpret_cast<uint2*>(p.o.p + tok * p.o.ts + head * p.o.hs + c4 * 4) =
+            none ? make_uint2(0u, 0u)
+                 : make_uint2(ptx::pack_bf16x2(x[0] * inv, x[1] * inv), ptx::pack_bf16x2(x[2] * inv, x[3] * inv));
+        if (c4 == 0) p.lse[int64_t(head) * p.tokens_q + tok] = none ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -697,7 +699,7 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     }
     if (e == cudaSuccess && !self && w.split_q) {
         const int64_t blocks = w.max_q * p.kv_heads;
-        e = packed::launch(packed_join_kernel<D>, dim3(unsigned(blocks), 16), 256, 0, stream, true, fp);  // (fewer than 2 SMs' worth)
+        e = packed::launch(packed_join_kernel<D>, dim3(unsigned(blocks), 128 / kJoinRows), kJoinRows * D / 4, 0, stream, true, fp);  // (fewer than 2 SMs' worth)
     }
     return e;
 }

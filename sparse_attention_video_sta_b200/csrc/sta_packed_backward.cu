@@ -133,10 +133,10 @@ __device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloa
     }
 }
 
-// The same as fp32, as they are: a part's sums.
+// The same as fp32, as they are: a part's sums, four columns of all rows after four columns (a warp's
+// stores are whole lines).  `dst`: the part's four columns that `taddr` begins with, this thread's row.
 template <int kCols, class Fix>
-__device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool store, Fix&& fix) {
-    float4* d4 = reinterpret_cast<float4*>(dst);
+__device__ __forceinline__ void store_part(uint32_t taddr, float4* dst, bool store, Fix&& fix) {
 #pragma unroll 1
     for (int cb = 0; cb < kCols / 32; ++cb) {
         uint32_t r[32];
@@ -145,7 +145,7 @@ __device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool stor
         fix(r, cb * 32);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            d4[cb * 8 + j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+            dst[(cb * 8 + j) * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
                                          __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
     }
 }
@@ -555,7 +555,9 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             };
             if (q.slot >= 0)
                 store_part<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h,
-                                  p.v.parts + (int64_t(q.slot) * K + hk) * (128 * D) + row * D + (D / 2) * h, real, put_back);
+                                  reinterpret_cast<float4*>(p.v.parts + (int64_t(q.slot) * K + hk) * (128 * D)) +
+                                      (D / 8) * h * 128 + row,
+                                  real, put_back);
             else
                 store_cols<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h, p.scale,
                               p.out_a.p + int64_t(q.tok0 + r_tok) * p.out_a.ts + (hk * p.group + r_head) * p.out_a.hs +
@@ -951,9 +953,10 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint32_t t_dk = tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h;
             const uint32_t t_dv = tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h;
             if (kb.slot >= 0) {
-                float* part = p.v.parts + (int64_t(kb.slot) * K + hk) * (2 * 128 * D) + row * D + (D / 2) * h;
+                float4* part = reinterpret_cast<float4*>(p.v.parts + (int64_t(kb.slot) * K + hk) * (2 * 128 * D)) +
+                               (D / 8) * h * 128 + row;
                 store_part<D / 2>(t_dk, part, real, back_q);
-                store_part<D / 2>(t_dv, part + 128 * D, real, back_do);
+                store_part<D / 2>(t_dv, part + 128 * D / 4, real, back_do);
             } else {
                 store_cols<D / 2>(t_dv, 1.0f, p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + (D / 2) * h, real, n == 0, back_do);
                 store_cols<D / 2>(t_dk, p.scale, p.out_a.p + tok * p.out_a.ts + hk * p.out_a.hs + (D / 2) * h, real, n == 0,
@@ -1000,14 +1003,15 @@ __global__ void __launch_bounds__(256) packed_sum_kernel(const BwdParams p) {
         if (split < 2) continue;
         constexpr int kPlanes = kKeys ? 2 : 1;
         const int i = blockIdx.y * 256 + threadIdx.x;
-        if (i < rows * (D / 8) * kPlanes) {
-            const int plane = i / (rows * (D / 8)), at = i % (rows * (D / 8)), row = at / (D / 8), col = at % (D / 8) * 8;
+        // a warp: eight rows by four pieces, whole lines of the parts and 64 bytes of a result's row
+        const int plane = i / (128 * D / 8), row = i / D % 16 * 8 + i % 8, col = i / 8 % (D / 8) * 8;
+        if (plane < kPlanes && row < rows) {
             float x[8] = {};
 #pragma unroll 4
             for (int k = 0; k < split; ++k) {
                 const float4* src = reinterpret_cast<const float4*>(
-                    p.v.parts + ((int64_t(slot + k) * K + hk) * kPlanes + plane) * (128 * D) + row * D + col);
-                const float4 a = src[0], b = src[1];
+                    p.v.parts + ((int64_t(slot + k) * K + hk) * kPlanes + plane) * (128 * D)) + col / 4 * 128 + row;
+                const float4 a = src[0], b = src[128];
                 x[0] += a.x;
                 x[1] += a.y;
                 x[2] += a.z;

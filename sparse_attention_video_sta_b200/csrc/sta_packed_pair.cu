@@ -274,11 +274,11 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                         uint32_t orr[32];
                         ptx::tmem_ld32(mO + cb * 32, orr);
                         if (fix) packed::restore(orr, seen_v + cb * 32, p.vals.ts, seen);
-                        float4* d4 = reinterpret_cast<float4*>(part + row * D + cb * 32);
+                        float4* d4 = reinterpret_cast<float4*>(part) + cb * 8 * 128 + row;
                         if (real)
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                d4[j] = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                d4[j * 128] = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
                                              : make_float4(__uint_as_float(orr[4 * j]), __uint_as_float(orr[4 * j + 1]),
                                                            __uint_as_float(orr[4 * j + 2]), __uint_as_float(orr[4 * j + 3]));
                     }
