@@ -8,6 +8,7 @@
 
 #include "sta_ops.h"
 #include "sta_ops.cuh"
+#include "sta_packed.cuh"
 
 namespace sta {
 
@@ -85,6 +86,8 @@ cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* 
     float* scales = is_v ? c.v_scales : c.k_scales;
     const int64_t n_slots = int64_t(c.blocks) * BT;
     const int64_t t0 = int64_t(blockIdx.x) * range, t1 = min(t0 + range, tokens);
+    ops::grid_launch_dependents();
+    ops::grid_wait();
     for (int i = tid; i < range + BT + 2; i += kAppendThreads) {
         const int64_t t = t0 - 1 + i;
         sh_slot[i] = t >= 0 && t < tokens ? slots[t] : -1;
@@ -206,9 +209,8 @@ cudaError_t launch_append(const sta_cache& c, const Rows& k, const Rows& v, int6
     const int range = tokens * c.kv_heads * 2 <= 4096 ? 1 : BT;  // (at most kMaxRange)
     const int64_t gx = (tokens + range - 1) / range;
     if (gx > INT32_MAX) return cudaErrorInvalidValue;
-    cache_append_kernel<D, BT><<<dim3(unsigned(gx), unsigned(c.kv_heads), 2), kAppendThreads, 0, stream>>>(
-        c, k, v, tokens, slots, range, status);
-    return cudaGetLastError();
+    return packed::launch(cache_append_kernel<D, BT>, dim3(unsigned(gx), unsigned(c.kv_heads), 2), kAppendThreads, 0, stream,
+                          true, c, k, v, tokens, slots, range, status);
 }
 
 // ---------------------------------------------------------------- extend
@@ -274,6 +276,8 @@ __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const Exte
     int32_t* s_need = s_back + B + 1;  // blocks needed before it; [B]: all
     const int tid = threadIdx.x, first = tid * per, last = min(first + per, B);
     const int64_t row = int64_t(p.width) * p.bt;  // tokens that a table holds
+    ops::grid_launch_dependents();
+    ops::grid_wait();
     const int32_t count = *p.count;
     bool bad = count < 0 || count > p.pool;
     int64_t add = 0, back = 0, need = 0;
@@ -431,17 +435,19 @@ sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* 
             return op_cuda_status(e);
     // a serving step's few slots and tables need no second CTA
     const unsigned ctas = max_slots > 8 * kExtendThreads || batch > 4 * kExtendThreads / 32 ? kExtendCluster : 1;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kExtendThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return op_cuda_status(cudaLaunchKernelEx(&cfg, cache_extend_kernel, p));
 }
 

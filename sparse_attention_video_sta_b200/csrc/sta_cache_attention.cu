@@ -300,6 +300,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     }
     __syncwarp();
     ops::grid_launch_dependents();
+    ops::grid_wait();
 
     const int64_t total = plan_total(a, plan, blockIdx.x == 0);
     if (a.p.clear_tail && plan.last < a.p.tokens_q) {
@@ -809,7 +810,7 @@ cudaError_t launch_attention(const sta_cache& c, CacheArgs a, int sms, cudaStrea
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(cache_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess)
-        e = packed::launch(cache_attention_kernel<D, NT>, dim3(unsigned(sms)), C::kThreads, C::kSmem, stream, false, mk, mv, a);
+        e = packed::launch(cache_attention_kernel<D, NT>, dim3(unsigned(sms)), C::kThreads, C::kSmem, stream, true, mk, mv, a);
     if (e == cudaSuccess && sms > 1)
         e = packed::launch(cache_join_kernel<D>, dim3(unsigned(sms - 1)), kJoinWarps * 32, 0, stream, true, a);
     return e;

@@ -690,12 +690,12 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     constexpr int kSmem = Cfg<D>::kSmemBytes;
     const int64_t items = w.max_wq * p.kv_heads;
     if (short_walks(p, D)) {
-        e = packed_fwd::launch_forward_pair(D, mq, mk, mv, fp, items, w.sms, !self, stream);
+        e = packed_fwd::launch_forward_pair(D, mq, mk, mv, fp, items, w.sms, stream);
     } else {
         e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e == cudaSuccess)
             e = packed::launch(packed_fwd_kernel<D>, dim3(unsigned(items < w.sms ? items : w.sms)), kThreads, kSmem, stream,
-                               !self, mq, mk, mv, fp);
+                               true, mq, mk, mv, fp);
     }
     if (e == cudaSuccess && !self && w.split_q) {
         const int64_t blocks = w.max_q * p.kv_heads;

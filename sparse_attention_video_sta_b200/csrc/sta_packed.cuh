@@ -215,8 +215,9 @@ __device__ __forceinline__ void restore(uint32_t (&r)[N], const __nv_bfloat16* s
 constexpr int kLostWords = 8;
 #endif
 
-// Launch attributes: `pdl`: the kernel may start while its predecessor in the
-// stream ends, and waits for it (griddepcontrol.wait) before it reads memory.
+// Launch attributes: `pdl`: the kernel may start while its predecessor in the stream
+// ends, whatever that is, and waits for it (griddepcontrol.wait, in every CTA and before
+// any access to global memory, so that its own end says that all before it has ended).
 template <class... P, class... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, bool pdl,
                    A&&... args) {

@@ -203,7 +203,7 @@ __device__ __forceinline__ float softmax_exp32(const uint32_t (&sr)[64], float c
 
 // The kernel for short walks (sta_packed_pair.cu).
 cudaError_t launch_forward_pair(int head_dim, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                const FwdParams& fp, int64_t items, int sms, bool pdl, cudaStream_t stream);
+                                const FwdParams& fp, int64_t items, int sms, cudaStream_t stream);
 
 }  // namespace packed_fwd
 }  // namespace sta

@@ -191,6 +191,7 @@ __device__ void clear_tails(const PackedProblem& p, const Tails& t, int head_dim
 __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProblem p, const View v, int backward,
                                                                 int head_dim, const Tails tails) {
     ops::grid_launch_dependents();
+    ops::grid_wait();
     if (blockIdx.x > 0) {
         clear_tails(p, tails, head_dim);
         return;
@@ -311,8 +312,7 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
 cudaError_t launch_lists(const PackedProblem& p, const View& v, bool backward, int head_dim, const Tails& tails,
                          cudaStream_t stream) {
     const unsigned grid = p.clear_tail && (tails.n > 0 || tails.lse != nullptr) ? 1 + 32 : 1;
-    packed_lists_kernel<<<grid, kThreads, 0, stream>>>(p, v, backward ? 1 : 0, head_dim, tails);
-    return cudaGetLastError();
+    return launch(packed_lists_kernel, dim3(grid), kThreads, 0, stream, true, p, v, backward ? 1 : 0, head_dim, tails);
 }
 
 cudaError_t rows_map(CUtensorMap* m, const Rows& r, int64_t tokens, int heads, int d, int box_heads, int box_tokens) {

@@ -523,20 +523,20 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
 
 template <int D>
 cudaError_t launch_pair(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const FwdParams& fp,
-                        int64_t items, int sms, bool pdl, cudaStream_t stream) {
+                        int64_t items, int sms, cudaStream_t stream) {
     constexpr int kSmem = PairCfg<D>::kSmemBytes;
     cudaError_t e = cudaFuncSetAttribute(packed_fwd_pair_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    return packed::launch(packed_fwd_pair_kernel<D>, dim3(unsigned(items < sms ? items : sms)), kThreads, kSmem, stream, pdl,
+    return packed::launch(packed_fwd_pair_kernel<D>, dim3(unsigned(items < sms ? items : sms)), kThreads, kSmem, stream, true,
                           mq, mk, mv, fp);
 }
 
 }  // namespace
 
 cudaError_t packed_fwd::launch_forward_pair(int head_dim, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                            const FwdParams& fp, int64_t items, int sms, bool pdl, cudaStream_t stream) {
-    return head_dim == 128 ? launch_pair<128>(mq, mk, mv, fp, items, sms, pdl, stream)
-                           : launch_pair<64>(mq, mk, mv, fp, items, sms, pdl, stream);
+                                            const FwdParams& fp, int64_t items, int sms, cudaStream_t stream) {
+    return head_dim == 128 ? launch_pair<128>(mq, mk, mv, fp, items, sms, stream)
+                           : launch_pair<64>(mq, mk, mv, fp, items, sms, stream);
 }
 
 }  // namespace sta
