@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "sta_ops.h"
 #include "sta_ops.cuh"
 #include "sta_packed.cuh"
@@ -215,7 +217,7 @@ cudaError_t launch_append(const sta_cache& c, const Rows& k, const Rows& v, int6
 
 // ---------------------------------------------------------------- extend
 constexpr int kExtendThreads = 1024;
-constexpr int kExtendCluster = 8;
+constexpr unsigned kExtendCluster = 16;
 constexpr int kMaxRequests = 8192;
 
 struct ExtendParams {
@@ -233,29 +235,60 @@ struct ExtendParams {
     int32_t* shortage;
 };
 
-// Sums of `v` over the threads before this one; `total`: over all.
-__device__ int64_t block_scan(int64_t v, int64_t* sh, int64_t& total) {
+// Sums of each of `v` over the threads before this one, in place; `total`: over all.
+constexpr int kSums = 3;
+__device__ void block_scan(int64_t (&v)[kSums], int64_t (*sh)[kSums], int64_t (&total)[kSums]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-    for (int i = 1; i < 32; i <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, x, i);
-        if (lane >= i) x += y;
-    }
-    if (lane == 31) sh[warp] = x;
+    int64_t x[kSums];
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) x[k] = v[k];
+    for (int i = 1; i < 32; i <<= 1)
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) {
+            const int64_t y = __shfl_up_sync(~0u, x[k], i);
+            if (lane >= i) x[k] += y;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) sh[warp][k] = x[k];
     __syncthreads();
-    if (warp == 0) {
-        int64_t s = sh[lane];
+    // every warp sums the warps' totals for itself
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+        int64_t s = sh[lane][k];
         for (int i = 1; i < 32; i <<= 1) {
             const int64_t y = __shfl_up_sync(~0u, s, i);
             if (lane >= i) s += y;
         }
-        sh[lane] = s;
+        total[k] = __shfl_sync(~0u, s, 31);
+        const int64_t before = __shfl_sync(~0u, s, warp > 0 ? warp - 1 : 0);
+        v[k] = (warp > 0 ? before : 0) + x[k] - v[k];
     }
-    __syncthreads();
-    const int64_t before = (warp > 0 ? sh[warp - 1] : 0) + x - v;
-    total = sh[31];
-    __syncthreads();
-    return before;
+}
+
+// The last b in [0, n) with cu[b] <= t, for a rising cu with cu[0] <= t (one warp, the same t in all lanes).
+__device__ int last_at_most(const int32_t* cu, int n, int32_t t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    for (int step = 1024; step > 0; step >>= 5) {  // 32 candidates, `step` apart, at a time; n <= 32 * 1024
+        const int b = lo + lane * step;
+        lo += (__popc(__ballot_sync(~0u, b < n && cu[b] <= t)) - 1) * step;
+    }
+    return lo;
+}
+
+// `n` entries, entry j by lane j % 32 of a warp: put(j, get(j)), four loads on their way at once.
+template <class Get, class Put>
+__device__ void each_of(int n, Get get, Put put) {
+    for (int j0 = threadIdx.x & 31; j0 < n; j0 += 128) {
+        int32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j0 + 32 * i < n) x[i] = get(j0 + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j0 + 32 * i < n) put(j0 + 32 * i, x[i]);
+    }
 }
 
 // One cluster.  Every CTA sums the requests for itself (new tokens, blocks
@@ -263,12 +296,14 @@ __device__ int64_t block_scan(int64_t v, int64_t* sh, int64_t& total) {
 // pushes, meet, and share the tables and slots.  The reads of `len` and `count`
 // come before the cluster's meeting and their writes after it, so the outputs
 // may be the inputs.  Latency-bound: one launch in place of a chain of scans (64 requests, one token
-// each: 18 us a call, nearly all of it the host's; 500 requests with 121000 new tokens: 20 us).
+// each: 8.8 us a call, nearly all of it the host's; 500 requests with 121000 new tokens: 11 us).  Its steps
+// are round trips: loads go four at a time, the three sums share their barriers, and a warp
+// finds the requests of its 128 slots by ballots (a binary search in each thread: 20 us).
 __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const ExtendParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ int32_t sh[];
-    __shared__ int64_t sh_scan[32];
+    __shared__ int64_t sh_scan[32][kSums];
     const int B = p.batch, per = (B + kExtendThreads - 1) / kExtendThreads;
     int32_t* s_len = sh;           // tokens held
     int32_t* s_cu = s_len + B;     // new tokens before this request; [B]: all
@@ -280,7 +315,8 @@ __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const Exte
     ops::grid_wait();
     const int32_t count = *p.count;
     bool bad = count < 0 || count > p.pool;
-    int64_t add = 0, back = 0, need = 0;
+    int64_t sums[kSums] = {0, 0, 0}, totals[kSums];
+    int64_t &add = sums[0], &back = sums[1], &need = sums[2];
     for (int b = first; b < last; ++b) {
         const int64_t n = p.len[b], a = p.add[b];
         if (n < 0 || n > row || n + (a > 0 ? a : 0) > row || n + (a > 0 ? a : 0) > INT32_MAX) bad = true;
@@ -293,10 +329,9 @@ __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const Exte
             need += (n + a + p.bt - 1) / p.bt - held;
         }
     }
-    int64_t all_add, all_back, all_need;
-    int64_t at_add = block_scan(add, sh_scan, all_add);
-    int64_t at_back = block_scan(back, sh_scan, all_back);
-    int64_t at_need = block_scan(need, sh_scan, all_need);
+    block_scan(sums, sh_scan, totals);
+    int64_t at_add = sums[0], at_back = sums[1], at_need = sums[2];
+    const int64_t all_add = totals[0], all_back = totals[1], all_need = totals[2];
     bad = __syncthreads_or(bad) || all_add > p.max_slots || all_add > INT32_MAX || count + all_back > p.pool;
     const int64_t there = count + all_back;
     const int64_t lack = all_need > there ? all_need - there : 0;
@@ -324,45 +359,62 @@ __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const Exte
     const int warp = tid / 32, lane = tid % 32, n_warps = kExtendThreads / 32;
     if (fine && all_back > 0)
         for (int b = rank * n_warps + warp; b < B; b += size * n_warps)
-            for (int j = lane; j < s_back[b + 1] - s_back[b]; j += 32)
-                p.free_blocks[count + s_back[b] + j] = p.tables[b * p.stride + j];
+            each_of(s_back[b + 1] - s_back[b], [&](int j) { return p.tables[b * p.stride + j]; },
+                    [&](int j, int32_t x) { p.free_blocks[count + s_back[b] + j] = x; });
     cluster.sync();  // the stack is whole, and every CTA has read the lengths and the count
     if (fine)
         for (int b = rank * n_warps + warp; b < B; b += size * n_warps) {
             const int held = (s_len[b] + p.bt - 1) / p.bt;
-            for (int j = lane; j < s_need[b + 1] - s_need[b]; j += 32)
-                p.tables[b * p.stride + held + j] = p.free_blocks[there - 1 - s_need[b] - j];
+            each_of(s_need[b + 1] - s_need[b], [&](int j) { return p.free_blocks[there - 1 - s_need[b] - j]; },
+                    [&](int j, int32_t x) { p.tables[b * p.stride + held + j] = x; });
         }
     const int32_t n_new = fine ? s_cu[B] : 0;
-    // four slots to a thread: one search, four table entries on their way at once
-    for (int64_t t0 = (rank * kExtendThreads + tid) * 4; t0 < p.max_slots; t0 += size * kExtendThreads * 4) {
-        int b = 0;
-        if (t0 < n_new) {
-            int hi = B - 1;  // the last request whose tokens begin at or before t0
-            while (b < hi) {
-                const int mid = (b + hi + 1) / 2;
-                if (s_cu[mid] <= t0)
-                    b = mid;
-                else
-                    hi = mid - 1;
-            }
+    // a warp takes 128 slots: the requests of its first and last by ballots, those between them in each
+    // lane; four entries of the tables on their way at once
+    for (int64_t t0 = (rank * n_warps + warp) * 128; t0 < p.max_slots; t0 += size * n_warps * 128) {
+        int64_t* out = p.slots + t0 + lane;
+        const int room = int(min(p.max_slots - t0, int64_t(128))) - lane;
+        const int have = t0 < n_new ? min(n_new - int32_t(t0), 128) : 0, first = int32_t(have > 0 ? t0 : 0);
+        int b0 = 0, b1 = 0;
+        if (have > 0) {
+            b0 = b1 = last_at_most(s_cu, B, first);
+            if (s_cu[b0 + 1] < first + have) b1 = last_at_most(s_cu, B, first + have - 1);
         }
         int32_t blk[4], off[4];
+        if (b0 == b1) {  // the usual one: all of one request
+            const int held = (s_len[b0] + p.bt - 1) >> p.bt_log2, pos0 = s_len[b0] + first - s_cu[b0] + lane;
+            const int32_t* table = p.tables + b0 * p.stride;
+            const int32_t* popped = p.free_blocks + (there - 1 - s_need[b0]) + held;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            blk[i] = -1;
-            off[i] = 0;
-            if (t0 + i < n_new) {
-                while (b < B - 1 && s_cu[b + 1] <= t0 + i) ++b;
-                const int held = (s_len[b] + p.bt - 1) >> p.bt_log2, pos = s_len[b] + int(t0 + i - s_cu[b]), j = pos >> p.bt_log2;
-                blk[i] = j < held ? p.tables[b * p.stride + j] : p.free_blocks[there - 1 - s_need[b] - (j - held)];
-                off[i] = pos & (p.bt - 1);
+            for (int i = 0; i < 4; ++i) {
+                const int j = (pos0 + 32 * i) >> p.bt_log2;
+                off[i] = (pos0 + 32 * i) & (p.bt - 1);
+                blk[i] = lane + 32 * i < have ? *(j < held ? table + j : popped - j) : -1;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = first + lane + 32 * i;
+                blk[i] = -1;
+                off[i] = 0;
+                if (lane + 32 * i < have) {
+                    int b = b0, hi = b1;
+                    while (b < hi) {
+                        const int mid = (b + hi + 1) / 2;
+                        if (s_cu[mid] <= t)
+                            b = mid;
+                        else
+                            hi = mid - 1;
+                    }
+                    const int held = (s_len[b] + p.bt - 1) >> p.bt_log2, pos = s_len[b] + t - s_cu[b], j = pos >> p.bt_log2;
+                    blk[i] = j < held ? p.tables[b * p.stride + j] : p.free_blocks[there - 1 - s_need[b] - (j - held)];
+                    off[i] = pos & (p.bt - 1);
+                }
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (t0 + i < p.max_slots)
-                p.slots[t0 + i] = blk[i] >= 0 && blk[i] < p.pool ? int64_t(blk[i]) * p.bt + off[i] : -1;
+            if (32 * i < room) out[32 * i] = uint32_t(blk[i]) < uint32_t(p.pool) ? int64_t(blk[i]) * p.bt + off[i] : -1;
     }
     if (rank == 0) {
         for (int b = tid; b <= B; b += kExtendThreads) p.cu[b] = fine ? s_cu[b] : 0;
@@ -376,6 +428,35 @@ __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const Exte
             *p.shortage = bad ? -1 : int32_t(lack > INT32_MAX ? INT32_MAX : lack);
         }
     }
+}
+
+// A cluster of 16 where the device has one (the SMs of a GPC; 500 requests, 121000 new tokens: 11 us, with 8
+// CTAs 14.6); asked once for each device.  (The kernel's attribute belongs to the device as well.)
+cudaError_t extend_cluster(unsigned* ctas) {
+    constexpr int kDevices = 64;
+    static std::atomic<unsigned> known[kDevices];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    unsigned n = dev < kDevices ? known[dev].load() : 0u;
+    if (n == 0) {
+        cudaError_t e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = *ctas;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(*ctas);
+        cfg.blockDim = dim3(kExtendThreads);
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, cache_extend_kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        n = fit > 0 ? *ctas : 8u;
+        if (dev < kDevices) known[dev].store(n);
+    }
+    *ctas = n;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -427,26 +508,29 @@ sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* 
     if (cudaError_t e = op_begin(); e != cudaSuccess) return op_cuda_status(e);
     ExtendParams p{batch, block_tokens, block_tokens == 16 ? 4 : block_tokens == 32 ? 5 : block_tokens == 64 ? 6 : 7, table_width, pool, table_stride, max_slots, new_tokens, lengths, lengths_out,
                    block_tables, free_blocks, free_count, free_count_out, slots, cu_new, shortage};
-    const size_t smem = size_t(4 * batch + 3) * sizeof(int32_t);
-    if (smem > 48 * 1024)
-        if (cudaError_t e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 int(smem));
-            e != cudaSuccess)
-            return op_cuda_status(e);
-    // a serving step's few slots and tables need no second CTA
-    const unsigned ctas = max_slots > 8 * kExtendThreads || batch > 4 * kExtendThreads / 32 ? kExtendCluster : 1;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kExtendThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = size_t(4 * batch + 3) * sizeof(int32_t);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
+    if (cfg.dynamicSmemBytes > 48 * 1024)
+        if (cudaError_t e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 int(cfg.dynamicSmemBytes));
+            e != cudaSuccess)
+            return op_cuda_status(e);
+    // a serving step's few slots and tables need no second CTA
+    unsigned ctas = 1;
+    if (max_slots > 8 * kExtendThreads || batch > 4 * kExtendThreads / 32) {
+        ctas = kExtendCluster;
+        if (cudaError_t e = extend_cluster(&ctas); e != cudaSuccess) return op_cuda_status(e);
+    }
+    attr[1].val.clusterDim.x = ctas;
+    cfg.gridDim = dim3(ctas);
     cfg.numAttrs = ctas > 1 ? 2 : 1;
     return op_cuda_status(cudaLaunchKernelEx(&cfg, cache_extend_kernel, p));
 }

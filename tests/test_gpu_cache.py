@@ -525,3 +525,38 @@ def test_serving_prompts_and_tokens(sta, H, K, d, bt):
             ref.check(lse[:, :sum(rows)], want, "lse")
     assert sta.sta_operator_status() == 0
     del graph
+
+
+def test_extend_the_largest_tables(sta):
+    """The most requests a step may have, with slots enough for every CTA, against a plain loop."""
+    B, bt, width = 8192, 16, 4
+    r = random.Random(5)
+    lengths = [r.randint(0, 40) for _ in range(B)]
+    new = [r.choice((-1, 0, 1, 1, 3, 20)) for _ in range(B)]
+    pool = sum(-(-n // bt) for n in lengths) + 8192
+    ids = list(range(pool))
+    r.shuffle(ids)
+    table = [[-1] * width for _ in range(B)]
+    for b, n in enumerate(lengths):
+        for j in range(-(-n // bt)):
+            table[b][j] = ids.pop()
+    free = ids + [-1] * (pool - len(ids))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    t, f = i32(table), i32(free)
+    step = sta.sta_cache_extend(i32(new), i32(lengths), t, f, i32([len(ids)]), bt, sum(max(n, 0) for n in new) + 500)
+    for b, n in enumerate(new):
+        if n < 0:
+            ids += table[b][:-(-lengths[b] // bt)]
+    slots, held = [], []
+    for b, n in enumerate(new):
+        for pos in range(lengths[b], lengths[b] + max(n, 0)):
+            if pos % bt == 0:
+                table[b][pos // bt] = ids.pop()
+            slots.append(table[b][pos // bt] * bt + pos % bt)
+        held.append(0 if n < 0 else lengths[b] + n)
+    assert int(step.short) == 0 and int(step.free_count) == len(ids) and step.lengths.tolist() == held
+    assert step.slots.tolist() == slots + [-1] * 500 and f[:len(ids)].tolist() == ids
+    assert step.cu_new.tolist() == [0] + [sum(max(n, 0) for n in new[:i + 1]) for i in range(B)]
+    got = t.tolist()
+    for b, n in enumerate(held):
+        assert got[b][:-(-n // bt)] == table[b][:-(-n // bt)]
