@@ -46,7 +46,7 @@ struct CacheArgs {
     int64_t stride;
     Rows q, o;
     float* lse;
-    float* warp_parts;  // [CTAs][warps][2][row_tile][D + 4]: O, m, l, mw
+    float* warp_parts;  // [CTAs][warps][row_tile][D + 4]: O, m, l, mw
     float* cta_parts;   // [CTAs][2][row_tile][D + 4]
     Unit* begins;       // [CTAs]: the unit that a CTA's run begins inside of
     int64_t* head;      // tiles of all units, CTAs that take part
@@ -159,14 +159,20 @@ __device__ int32_t plan_locate(const CacheArgs& a, const PlanShared& sh, int64_t
     }
 }
 
-// CTAs that take part, and the first tile of CTA i of them (or of warp i of a CTA's).
+// CTAs that take part; the runs of the CTAs, or of a CTA's warps.
 __device__ __forceinline__ int64_t plan_ctas(int64_t total, int64_t most) {
     const int64_t some = (total + 2 * kMinTiles - 1) / (2 * kMinTiles);
     return some < most ? some : most;
 }
-__device__ __forceinline__ int64_t plan_first(int64_t total, int64_t parts, int64_t i) {
-    return total / parts * i + total % parts * i / parts;
+// n / d for n >= 0, d > 0: in 32 bits where they fit (a 64-bit division is some hundred instructions).
+__device__ __forceinline__ int64_t divide(int64_t n, int32_t d) {
+    return n <= int64_t(UINT32_MAX) ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
 }
+struct Runs {
+    int64_t each, more;  // tiles of a run; the first `more` have one more
+    __device__ Runs(int64_t total, int32_t parts) : each(divide(total, parts)), more(total - each * parts) {}
+    __device__ int64_t first(int64_t i) const { return each * i + min(i, more); }
+};
 
 // D += A B, m16n8k16, fp16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -286,6 +292,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     constexpr int kSteps = D / 16;    // k-steps of K Q^T, 16-row tiles of O^T
     extern __shared__ uint8_t smem_raw[];
     __shared__ PlanShared plan;
+    __shared__ bool part0_kept[kWarps];  // in the ring
     __shared__ Unit ends[kWarps][2];  // each warp's parts: of the unit that it begins inside of, of its last
     const uint32_t raw_base = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -319,14 +326,19 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         a.head[1] = ctas;
     }
     if (blockIdx.x >= ctas) return;
-    const int64_t cta_begin = plan_first(total, ctas, blockIdx.x), cta_end = plan_first(total, ctas, blockIdx.x + 1);
+    const Runs cta_runs(total, int32_t(ctas));
+    const int64_t cta_begin = cta_runs.first(blockIdx.x), cta_end = cta_runs.first(blockIdx.x + 1);
     const int64_t n_tiles = cta_end - cta_begin, some = (n_tiles + kMinTiles - 1) / kMinTiles;
     const int warps = int(some < kWarps ? some : kWarps);  // that have a run
-    const int64_t begin = cta_begin + (warp < warps ? plan_first(n_tiles, warps, warp) : n_tiles);
-    const int64_t end = cta_begin + (warp < warps ? plan_first(n_tiles, warps, warp + 1) : n_tiles);
+    const Runs runs(n_tiles, warps);
+    const int64_t begin = cta_begin + (warp < warps ? runs.first(warp) : n_tiles);
+    const int64_t end = cta_begin + (warp < warps ? runs.first(warp + 1) : n_tiles);
     if (lane < 2) ends[warp][lane].unit0 = -1;
     __syncwarp();
-    float* my_parts = a.warp_parts + (int64_t(blockIdx.x) * kWarps + warp) * 2 * kRows * (D + 4);
+    // A part of what a run ends with stays in the warp's ring, which no copy fills any more; one of a unit
+    // that ends inside of the run goes to the workspace.
+    static_assert(S * 2 * C::kTileBytes >= kRows * (D + 4) * 4, "a part fits into a ring");
+    float* my_part0 = a.warp_parts + (int64_t(blockIdx.x) * kWarps + warp) * kRows * (D + 4);
     int64_t at = begin, before = 0;
     int32_t b = at < end ? plan_locate(a, plan, at, &before) : 0;
     uint32_t slot_in = 0, slot_out = 0, phase = 0;  // this warp's ring: next slot to fill, to read, its phase
@@ -342,7 +354,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             ++b;
             continue;
         }
-        const int unit = int(in_seq / sq.tiles), first = int(in_seq % sq.tiles);
+        const int unit = int(divide(in_seq, sq.tiles)), first = int(in_seq - int64_t(unit) * sq.tiles);
         const int rt = unit / K, hk = unit % K;
         const int last = int(min(int64_t(sq.tiles), first + (end - at)));
         at += last - first;
@@ -667,7 +679,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     const int row = rt * kRows + r;
                     store_row<D / 8>(a, sq.q0 + row / G, hk * G + row % G, g * (D / 8), y, m[nt][i], l[nt][i], mw[nt][i]);
                 } else {
-                    float* dst = my_parts + (which * kRows + r) * (D + 4);
+                    float* dst = (at == end ? reinterpret_cast<float*>(ring) : my_part0) + r * (D + 4);
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j)
                         *reinterpret_cast<float4*>(dst + g * (D / 8) + 4 * j) =
@@ -676,6 +688,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 }
             }
         if (lane == 0 && !whole) ends[warp][which] = Unit{unit0, unit0 + sq.tiles, sq.q0, rows, rt * kRows, hk * G};
+        if (lane == 0 && which == 0) part0_kept[warp] = at == end;
     }
     // After a wait that ran out: the copies still in flight land before the CTA leaves (bounded).
     if (dead)
@@ -691,7 +704,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         return;
     }
     // (one warp for each row of each such unit)
-    const float* parts0 = a.warp_parts + int64_t(blockIdx.x) * kWarps * 2 * kRows * (D + 4);
+    const float* parts0 = a.warp_parts + int64_t(blockIdx.x) * kWarps * kRows * (D + 4);
     // lane i < 16: does warp i's run begin inside of a unit, does it leave one unfinished
     const int64_t began = lane < warps ? ends[lane][0].unit0 : -1, left = lane < warps ? ends[lane][1].unit0 : -1;
     const uint32_t starts = __ballot_sync(~0u, left >= 0) << 1 | (__shfl_sync(~0u, began, 0) >= 0 ? 1u : 0u);
@@ -709,7 +722,11 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             if (turn % kWarps != warp) continue;
             float x[D / 32], jm, jl, jw;
             join_row<D>(0, w1 - w0, 1, [&](int64_t c) {
-                return parts0 + (((w0 + c) * 2 + (c == 0 && !early ? 1 : 0)) * kRows + r) * (D + 4);
+                const int v = w0 + int(c);
+                const float* from = (c == 0 && !early) || part0_kept[v]
+                                        ? reinterpret_cast<const float*>(smem + v * S * 2 * C::kTileBytes)
+                                        : parts0 + int64_t(v) * kRows * (D + 4);
+                return from + r * (D + 4);
             }, x, jm, jl, jw);
             if (done) {
                 const int row = u.row0 + r;
@@ -735,15 +752,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
     constexpr int E = D / 32;
     __shared__ alignas(16) float sh[kJoinWarps * (D + 4)];
     ops::grid_wait();
-    const int64_t total = a.head[0], ctas = a.head[1];
     const int64_t i = int64_t(blockIdx.x) + 1;
+    const int64_t total = a.head[0], ctas = a.head[1];
+    const Unit u = a.begins[i];  // (on its way with the others)
     if (i >= ctas) return;
-    const Unit u = a.begins[i];
-    if (u.unit0 < 0 || plan_first(total, ctas, i - 1) > u.unit0) return;
+    const Runs runs(total, int32_t(ctas));
+    if (u.unit0 < 0 || runs.first(i - 1) > u.unit0) return;
     int64_t lo = i + 1, hi = ctas;  // the first CTA from i + 1 on whose run begins behind the unit
     while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
-        if (plan_first(total, ctas, mid) < u.unit1)
+        if (runs.first(mid) < u.unit1)
             lo = mid + 1;
         else
             hi = mid;
@@ -802,7 +820,7 @@ cudaError_t launch_attention(const sta_cache& c, CacheArgs a, int sms, cudaStrea
     const int64_t n_rows = int64_t(c.blocks) * c.kv_heads * c.block_tokens;
     CUtensorMap mk, mv;
     a.row_tile = C::kRows;
-    a.cta_parts = a.warp_parts + int64_t(sms) * 2 * C::kWarps * C::kRows * (D + 4);
+    a.cta_parts = a.warp_parts + int64_t(sms) * C::kWarps * C::kRows * (D + 4);
     a.begins = reinterpret_cast<Unit*>(a.cta_parts + int64_t(sms) * 2 * C::kRows * (D + 4));
     a.head = reinterpret_cast<int64_t*>(a.begins + sms);
     cudaError_t e = codes_map(&mk, c.k_codes, n_rows, D, kTile);
@@ -855,8 +873,8 @@ sta_status sta_cache_workspace(const sta_cache* c, const sta_packed* p, int64_t*
     if (bytes == nullptr) return STA_ERR_INVALID_ARG;
     if (sta_status st = cache_problem(c, p, false, &pp); st != STA_OK) return st;
     const int sms = packed::sm_count_or_b200();
-    // parts of an SM: its warps' (12 of 8 rows, 8 of 16; d = 64: 12 of 16) and its own
-    const int64_t rows = (c->head_dim == 128 ? 128 + 16 : 192 + 16) * 2;
+    // parts of an SM: its warps' (12 of 8 rows, 8 of 16; d = 64: 12 of 16) and its own two
+    const int64_t rows = (c->head_dim == 128 ? 128 : 192) + 2 * 16;
     *bytes = sms * (rows * (c->head_dim + 4) * 4 + int64_t(sizeof(Unit))) + 16;
     return STA_OK;
 }
