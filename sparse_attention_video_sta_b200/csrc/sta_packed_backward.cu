@@ -39,10 +39,14 @@ using packed::KWork;
 using packed::QBlock;
 using packed::QWork;
 
-constexpr int kThreads = 320;  // warps 0-7 elementwise, 8 load, 9 MMA
-constexpr int kLoadWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kEwWarps = 8;
+// Warps 0-15 elementwise: four to an SM sub-partition, 32 columns of a row to a thread (8 warps
+// of 64 columns leave the round trips of a step uncovered: EWFIG); 16 load, 17 MMA.
+constexpr int kEwWarps = 16;
+constexpr int kEwThreads = kEwWarps * 32;
+constexpr int kParts = kEwWarps / 4;  // of a row's 128 columns
+constexpr int kLoadWarp = kEwWarps;
+constexpr int kMmaWarp = kEwWarps + 1;
+constexpr int kThreads = kEwThreads + 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kBoxBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16)
@@ -104,61 +108,50 @@ __device__ __forceinline__ bool get_item(uint32_t k, uint32_t full0, const Work*
     return true;
 }
 
-__device__ __forceinline__ void pack64(const float (&x)[64], uint32_t (&pk)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) pk[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
-}
-
-// `kCols` fp32 TMEM columns of this thread's lane, times `mul`, as bf16 to dst; `zero`: zeros
+// 32 fp32 TMEM columns of this thread's lane, times `mul`, as bf16 to dst; `zero`: zeros
 // instead.  Every lane loads (the access is warp-wide); lanes with `store` write.
-// `fix(r, column)` changes 32 columns before.
-template <int kCols, class Fix>
+// `fix(r)` changes them before.
+template <class Fix>
 __device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloat16* dst, bool store, bool zero, Fix&& fix) {
     uint4* d4 = reinterpret_cast<uint4*>(dst);
-#pragma unroll 1
-    for (int cb = 0; cb < kCols / 32; ++cb) {
-        uint32_t r[32];
-        ptx::tmem_ld32(taddr + cb * 32, r);
-        if (!store) continue;
-        fix(r, cb * 32);
+    uint32_t r[32];
+    ptx::tmem_ld32(taddr, r);
+    if (!store) return;
+    fix(r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint4 v;
-            v.x = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 0]) * mul, __uint_as_float(r[8 * j + 1]) * mul);
-            v.y = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 2]) * mul, __uint_as_float(r[8 * j + 3]) * mul);
-            v.z = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 4]) * mul, __uint_as_float(r[8 * j + 5]) * mul);
-            v.w = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 6]) * mul, __uint_as_float(r[8 * j + 7]) * mul);
-            d4[cb * 4 + j] = zero ? make_uint4(0u, 0u, 0u, 0u) : v;
-        }
+    for (int j = 0; j < 4; ++j) {
+        uint4 v;
+        v.x = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 0]) * mul, __uint_as_float(r[8 * j + 1]) * mul);
+        v.y = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 2]) * mul, __uint_as_float(r[8 * j + 3]) * mul);
+        v.z = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 4]) * mul, __uint_as_float(r[8 * j + 5]) * mul);
+        v.w = ptx::pack_bf16x2(__uint_as_float(r[8 * j + 6]) * mul, __uint_as_float(r[8 * j + 7]) * mul);
+        d4[j] = zero ? make_uint4(0u, 0u, 0u, 0u) : v;
     }
 }
 
 // The same as fp32, as they are: a part's sums, four columns of all rows after four columns (a warp's
 // stores are whole lines).  `dst`: the part's four columns that `taddr` begins with, this thread's row.
-template <int kCols, class Fix>
+template <class Fix>
 __device__ __forceinline__ void store_part(uint32_t taddr, float4* dst, bool store, Fix&& fix) {
-#pragma unroll 1
-    for (int cb = 0; cb < kCols / 32; ++cb) {
-        uint32_t r[32];
-        ptx::tmem_ld32(taddr + cb * 32, r);
-        if (!store) continue;
-        fix(r, cb * 32);
+    uint32_t r[32];
+    ptx::tmem_ld32(taddr, r);
+    if (!store) return;
+    fix(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            dst[(cb * 8 + j) * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                         __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-    }
+    for (int j = 0; j < 8; ++j)
+        dst[j * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                   __uint_as_float(r[4 * j + 3]));
 }
 
-// A-operand column of K-step kk of a bf16 matrix that the two elementwise warpgroups wrote
-// into TMEM: warpgroup h packs its 64 columns into columns [64 h, 64 h + 32).
-__device__ __forceinline__ uint32_t a_col(int kk) { return uint32_t((kk >> 2) * 64 + (kk & 3) * 8); }
+// A-operand column of K-step kk of a bf16 matrix that the elementwise warpgroups wrote into
+// TMEM: warpgroup h packs its 32 columns into columns [32 h, 32 h + 16).
+__device__ __forceinline__ uint32_t a_col(int kk) { return uint32_t((kk >> 1) * 32 + (kk & 1) * 8); }
 
 // Rows [from, 128) of a 128-row block in shared memory to zero (128-byte rows in D / 64 boxes;
-// the swizzle permutes within rows), by the 256 elementwise threads, visible to tcgen05.
+// the swizzle permutes within rows), by the elementwise threads, visible to tcgen05.
 template <int D>
 __device__ __forceinline__ void zero_rows(uint8_t* blk, int from, int thread) {
-    for (int i = from * 8 + thread; i < 128 * 8; i += 256)
+    for (int i = from * 8 + thread; i < 128 * 8; i += kEwThreads)
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb)
             *reinterpret_cast<uint4*>(blk + cb * kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -224,8 +217,7 @@ struct DqCfg {
     static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 8 + 2 * kItemQ;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kQueueOff = kMiscOff + 16;
-    static constexpr int kXchOff = kQueueOff + kItemQ * int(sizeof(QWork));  // [2 halves][128 rows]
-    static constexpr int kLostOff = kXchOff + 1024;  // kLostWords
+    static constexpr int kLostOff = kQueueOff + kItemQ * int(sizeof(QWork));  // kLostWords
     static constexpr int kSmemBytes = kLostOff + 4 * packed::kLostWords + 1024;
     static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
     static constexpr uint32_t kColS0 = 0, kColDP = 256, kColDQ = 384;
@@ -424,13 +416,15 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
     } else {
         // ------------------------------------------------------- elementwise
-        const int h = warp >> 2;  // column half
+        const int h = warp >> 2;  // which 32 columns
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
         const uint64_t c2 = ptx::f2(p.scale_log2, p.scale_log2);
         const int r_tok = row / p.group, r_head = row - r_tok * p.group;
-        const uint32_t pair_bar = 1u + uint32_t(warp & 3);  // named barrier of warps w and w + 4: the same rows
-        float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
+        const uint32_t rows_bar = 1u + uint32_t(warp & 3);  // named barrier of the kParts warps with the same rows
+        // [kParts][128 rows], over the query block: S and dP have read it where this is used, and the next one
+        // is copied in after dQ
+        float* xch = reinterpret_cast<float*>(smem + C::kQOff);
         uint32_t gs = 0, dqc = 0;
         bool ok = true;
         for (uint32_t kq = 0; ok; ++kq) {
@@ -439,7 +433,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const bool took = __all_sync(~0u, get_item(kq, item_full0, item_q, abort_flag, p, q));
             __syncwarp();
             if (took && lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
-            if (ptx::bar_red_or(pair_bar, 64, !took)) break;  // leave together: they meet again below
+            if (ptx::bar_red_or(rows_bar, 32 * kParts, !took)) break;  // leave together: they meet again below
             if (q.n < 0) break;
             const int32_t hk = q.hk, n = q.n;
             const bool real = r_tok < q.ntok;
@@ -456,7 +450,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const bool exact = n == 1 && q.c0 == 0 && q.slot < 0;
             for (int32_t j = 0; j < n; ++j) {
                 const uint32_t step = gs + uint32_t(j);
-                // (in an exact walk both warps of a pair meet at its barrier, whatever failed)
+                // (in an exact walk the warps of the same rows meet at their barrier, whatever failed)
                 bool good = __all_sync(~0u, wait_bw(s_full(int(step & 1u)), (step >> 1) & 1u, abort_flag, p));
                 if (!good && !exact) {
                     ok = false;
@@ -464,22 +458,22 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 ptx::tc_fence_after();
                 const int key = (q.c0 + j) * 128;  // the chunk's first
-                const int seen = limit - (key + 64 * h);  // keys of this half that the row sees
-                const bool masked = warp_limit < key + 64 * h + 64;
+                const int seen = limit - (key + 32 * h);  // keys of this part that the row sees
+                const bool masked = warp_limit < key + 32 * h + 32;
                 if (key + 128 > q.limit0) {  // keys that some row does not see: S has read K, dQ has not
                     if (!wait_bw(k_full(int(step % KS)), (step / KS) & 1u, abort_flag, p)) good = false;  // (has been)
                     uint8_t* kblk = smem + C::kKOff + (step % KS) * C::kBlk;
                     const int dead = min(128, max(0, (p.causal ? min(q.nkeys, q.limit0 + q.ntok - 1) : q.nkeys) - key));
-                    if (packed::scrub_rows<D / 64>(kblk, kBoxBytes, max(0, q.limit0 - key), dead, threadIdx.x, 256))
+                    if (packed::scrub_rows<D / 64>(kblk, kBoxBytes, max(0, q.limit0 - key), dead, threadIdx.x, kEwThreads))
                         lost[kq % packed::kLostWords] = kq + 1;
                     zero_rows<D>(kblk, dead, threadIdx.x);
                 }
-                float pr[64];
+                float pr[32];
                 {
-                    uint32_t sr[64];
-                    ptx::tmem_ld64(tmem + lane_addr + C::kColS0 + (step & 1u) * 128u + 64u * h, sr);
+                    uint32_t sr[32];
+                    ptx::tmem_ld32(tmem + lane_addr + C::kColS0 + (step & 1u) * 128u + 32u * h, sr);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         float x0, x1;
                         ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
                                                   c2, nl2),
@@ -494,14 +488,14 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t tdp = tmem + lane_addr + C::kColDP + 64u * h;
-                uint32_t pk[32];
+                const uint32_t tdp = tmem + lane_addr + C::kColDP + 32u * h;
+                uint32_t pk[16];
                 {
-                    uint32_t dr[64];
-                    ptx::tmem_ld64(tdp, dr);
+                    uint32_t dr[32];
+                    ptx::tmem_ld32(tdp, dr);
                     if (masked)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < 32; ++i)
                             if (i >= seen) {
                                 pr[i] = 0.0f;
                                 dr[i] = 0u;
@@ -509,7 +503,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (exact) {
                         uint64_t a0 = ptx::f2(0.0f, 0.0f), a1 = a0;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < 16; i += 2) {
                             a0 = ptx::f2_fma(ptx::f2(pr[2 * i], pr[2 * i + 1]),
                                              ptx::f2(__uint_as_float(dr[2 * i]), __uint_as_float(dr[2 * i + 1])), a0);
                             a1 = ptx::f2_fma(ptx::f2(pr[2 * i + 2], pr[2 * i + 3]),
@@ -518,16 +512,17 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         float x0, x1;
                         ptx::f2_split(ptx::f2_add(a0, a1), x0, x1);
                         xch[h * 128 + row] = x0 + x1;
-                        if (ptx::bar_red_or(pair_bar, 64, !good)) {
+                        if (ptx::bar_red_or(rows_bar, 32 * kParts, !good)) {
                             ok = false;
                             break;
                         }
-                        nd = -(xch[row] + xch[128 + row]);
+                        nd = -((xch[row] + xch[128 + row]) + (xch[256 + row] + xch[384 + row]));
                         if (h == 0 && real) p.neg_d[grow] = nd;  // for dK / dV
+                        ptx::fence_proxy_async_smem();
                     }
                     const uint64_t nd2 = ptx::f2(nd, nd);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         float t0, t1;
                         ptx::f2_split(ptx::f2_mul(ptx::f2(pr[2 * i], pr[2 * i + 1]),
                                                   ptx::f2_add(ptx::f2(__uint_as_float(dr[2 * i]),
@@ -537,7 +532,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         pk[i] = ptx::pack_bf16x2(t0, t1);
                     }
                 }
-                ptx::tmem_st32(tdp, pk);
+                ops::tmem_st16(tdp, pk);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -549,20 +544,20 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ptx::tc_fence_after();
             const bool fix = lost[kq % packed::kLostWords] == kq + 1;
             const int lo = max(max(q.limit0, 0), q.c0 * 128), seen = min(limit, (q.c0 + n) * 128) - lo;
-            auto put_back = [&](uint32_t (&r)[32], int col) {
-                if (fix)
-                    packed::restore(r, p.k.p + (q.key0 + int64_t(lo)) * p.k.ts + hk * p.k.hs + (D / 2) * h + col, p.k.ts, seen);
-            };
-            if (q.slot >= 0)
-                store_part<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h,
-                                  reinterpret_cast<float4*>(p.v.parts + (int64_t(q.slot) * K + hk) * (128 * D)) +
-                                      (D / 8) * h * 128 + row,
-                                  real, put_back);
-            else
-                store_cols<D / 2>(tmem + lane_addr + C::kColDQ + uint32_t(D / 2) * h, p.scale,
-                              p.out_a.p + int64_t(q.tok0 + r_tok) * p.out_a.ts + (hk * p.group + r_head) * p.out_a.hs +
-                                  (D / 2) * h,
-                              real, limit <= 0, put_back);
+            if (h < D / 32) {  // 32 of the D columns for each warpgroup
+                auto put_back = [&](uint32_t (&r)[32]) {
+                    if (fix)
+                        packed::restore(r, p.k.p + (q.key0 + int64_t(lo)) * p.k.ts + hk * p.k.hs + 32 * h, p.k.ts, seen);
+                };
+                const uint32_t t_dq = tmem + lane_addr + C::kColDQ + 32u * h;
+                if (q.slot >= 0)
+                    store_part(t_dq, reinterpret_cast<float4*>(p.v.parts + (int64_t(q.slot) * K + hk) * (128 * D)) + 8 * h * 128 + row,
+                               real, put_back);
+                else
+                    store_cols(t_dq, p.scale,
+                               p.out_a.p + int64_t(q.tok0 + r_tok) * p.out_a.ts + (hk * p.group + r_head) * p.out_a.hs + 32 * h,
+                               real, limit <= 0, put_back);
+            }
             ptx::tc_fence_before();
             gs += uint32_t(n);
         }
@@ -797,7 +792,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else {
         // ------------------------------------------------------- elementwise
-        const int h = warp >> 2;  // query-column half
+        const int h = warp >> 2;  // which 32 query columns
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
         const uint64_t c2 = ptx::f2(p.scale_log2, p.scale_log2);
@@ -823,8 +818,8 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 uint8_t* st = smem + stage_off(r);
                 const int32_t limit0 = p.v.qblocks[kb.q0 + j].limit0, rows = p.v.qblocks[kb.q0 + j].ntok * p.group;
                 const bool ragged = rows < rows_used;
-                // query rows [from, to) of this half see this thread's key
-                const int from = (p.causal ? p.group * max(0, kb.pos + row - limit0 + 1) : 0) - 64 * h, to = rows - 64 * h;
+                // query rows [from, to) of this part see this thread's key
+                const int from = (p.causal ? p.group * max(0, kb.pos + row - limit0 + 1) : 0) - 32 * h, to = rows - 32 * h;
                 const bool diagonal = p.causal && kb.pos + 127 >= limit0, masked = ragged || diagonal;
                 // rows that do not see every key of the block
                 const int partly = diagonal ? min(rows, p.group * (kb.pos + 128 - limit0)) : 0;
@@ -846,22 +841,22 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         ok = false;
                         break;
                     }
-                    if (packed::scrub_rows<D / 64>(st + C::kStDO, kBoxBytes, 0, partly, threadIdx.x, 256))
+                    if (packed::scrub_rows<D / 64>(st + C::kStDO, kBoxBytes, 0, partly, threadIdx.x, kEwThreads))
                         lost[kq % packed::kLostWords] = kq + 1;
                     ptx::fence_proxy_async_smem();
                 }
                 if (ragged) zero_rows<D>(st + C::kStDO, rows, threadIdx.x);
                 // per-column constants, 16-byte broadcast loads
-                const float4* cl = reinterpret_cast<const float4*>(st + C::kStL) + 16 * h;
-                const float4* cd = reinterpret_cast<const float4*>(st + C::kStD) + 16 * h;
-                const uint32_t ts = tmem + lane_addr + C::kColS + 64u * h;
-                float pr[64];
-                uint32_t pk[32];
+                const float4* cl = reinterpret_cast<const float4*>(st + C::kStL) + 8 * h;
+                const float4* cd = reinterpret_cast<const float4*>(st + C::kStD) + 8 * h;
+                const uint32_t ts = tmem + lane_addr + C::kColS + 32u * h;
+                float pr[32];
+                uint32_t pk[16];
                 {
-                    uint32_t sr[64];
-                    ptx::tmem_ld64(ts, sr);
+                    uint32_t sr[32];
+                    ptx::tmem_ld32(ts, sr);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const float4 l = cl[i];
                         float x0, x1, x2, x3;
                         ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1])),
@@ -878,16 +873,17 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 if (masked)
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
+                    for (int i = 0; i < 32; ++i)
                         if (i < from || i >= to) pr[i] = 0.0f;
-                pack64(pr, pk);
-                ptx::tmem_st32(ts, pk);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = ptx::pack_bf16x2(pr[2 * i], pr[2 * i + 1]);
+                ops::tmem_st16(ts, pk);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(p_full);
                 if (suspect) {
-                    if (packed::scrub_rows<D / 64>(st + C::kStQ, kBoxBytes, 0, partly, threadIdx.x, 256))
+                    if (packed::scrub_rows<D / 64>(st + C::kStQ, kBoxBytes, 0, partly, threadIdx.x, kEwThreads))
                         lost[kq % packed::kLostWords] = kq + 1;
                     ptx::fence_proxy_async_smem();
                 }
@@ -897,12 +893,12 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t tdp = tmem + lane_addr + C::kColDP + 64u * h;
+                const uint32_t tdp = tmem + lane_addr + C::kColDP + 32u * h;
                 {
-                    uint32_t dr[64];
-                    ptx::tmem_ld64(tdp, dr);
+                    uint32_t dr[32];
+                    ptx::tmem_ld32(tdp, dr);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const float4 dd = cd[i];
                         float t0, t1, t2, t3;
                         ptx::f2_split(ptx::f2_mul(ptx::f2(pr[4 * i], pr[4 * i + 1]),
@@ -920,12 +916,12 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     if (masked)  // (selected last: dP and D of a row may be anything)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             if (2 * i < from || 2 * i >= to) pk[i] &= 0xffff0000u;
                             if (2 * i + 1 < from || 2 * i + 1 >= to) pk[i] &= 0xffffu;
                         }
                 }
-                ptx::tmem_st32(tdp, pk);
+                ops::tmem_st16(tdp, pk);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -940,27 +936,30 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // Tokens whose rows may have lost something and see this thread's key: a token that sees `limit`
             // keys is the (limit - limit0)-th from the walk's first.
             const bool fix = n > 0 && lost[kq % packed::kLostWords] == kq + 1;
-            auto put_back = [&](const Rows& x, uint32_t (&r)[32], int col) {
+            // 32 columns of dV or dK for each warpgroup, or (d = 64: four 32s in all) of one of them
+            const int col = D == 128 ? 32 * h : 32 * (h & 1);
+            const bool with_dv = D == 128 || h < 2, with_dk = D == 128 || h >= 2;
+            auto put_back = [&](const Rows& x, uint32_t (&r)[32]) {
                 if (!fix) return;
                 const QBlock b0 = p.v.qblocks[kb.q0], b1 = p.v.qblocks[kb.q0 + n - 1];
                 const int lo = max(kb.pos + row + 1, b0.limit0), hi = min(kb.pos + 127, b1.limit0 + b1.ntok - 1);
                 for (int t = lo; t <= hi; ++t)
-                    packed::restore(r, x.p + (int64_t(b0.tok0) + t - b0.limit0) * x.ts + hk * p.group * x.hs + (D / 2) * h + col,
+                    packed::restore(r, x.p + (int64_t(b0.tok0) + t - b0.limit0) * x.ts + hk * p.group * x.hs + col,
                                     x.hs, p.group);
             };
-            auto back_q = [&](uint32_t (&r)[32], int col) { put_back(p.q, r, col); };
-            auto back_do = [&](uint32_t (&r)[32], int col) { put_back(p.dout, r, col); };
-            const uint32_t t_dk = tmem + lane_addr + C::kColDK + uint32_t(D / 2) * h;
-            const uint32_t t_dv = tmem + lane_addr + C::kColDV + uint32_t(D / 2) * h;
+            auto back_q = [&](uint32_t (&r)[32]) { put_back(p.q, r); };
+            auto back_do = [&](uint32_t (&r)[32]) { put_back(p.dout, r); };
+            const uint32_t t_dk = tmem + lane_addr + C::kColDK + uint32_t(col), t_dv = tmem + lane_addr + C::kColDV + uint32_t(col);
             if (kb.slot >= 0) {
                 float4* part = reinterpret_cast<float4*>(p.v.parts + (int64_t(kb.slot) * K + hk) * (2 * 128 * D)) +
-                               (D / 8) * h * 128 + row;
-                store_part<D / 2>(t_dk, part, real, back_q);
-                store_part<D / 2>(t_dv, part + 128 * D / 4, real, back_do);
+                               col / 4 * 128 + row;
+                if (with_dk) store_part(t_dk, part, real, back_q);
+                if (with_dv) store_part(t_dv, part + 128 * D / 4, real, back_do);
             } else {
-                store_cols<D / 2>(t_dv, 1.0f, p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + (D / 2) * h, real, n == 0, back_do);
-                store_cols<D / 2>(t_dk, p.scale, p.out_a.p + tok * p.out_a.ts + hk * p.out_a.hs + (D / 2) * h, real, n == 0,
-                                  back_q);
+                if (with_dv)
+                    store_cols(t_dv, 1.0f, p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + col, real, n == 0, back_do);
+                if (with_dk)
+                    store_cols(t_dk, p.scale, p.out_a.p + tok * p.out_a.ts + hk * p.out_a.hs + col, real, n == 0, back_q);
             }
             ptx::tc_fence_before();
             gs += uint32_t(n);
