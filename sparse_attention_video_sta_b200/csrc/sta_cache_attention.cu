@@ -266,7 +266,7 @@ __device__ __forceinline__ void join_row(int64_t s, int64_t n, int share, const 
 // which fp16 and fp32 bear and which makes rescaling O rare.  Q is scaled by a power of two
 // for each row into fp16's range.
 // HBM-bound: 2 D bytes for each token and key head.  64 requests of 500-8000 tokens, 24 / 8 heads, d = 128
-// (313 MB): 77 us a call, 4.0 TB/s; the copies alone, without the products, take 70 (the
+// (313 MB): 72.5 us a call, 4.3 TB/s; the copies alone, without the products, take 70 (the
 // plan, the first copies' latency, the joins and 5.4 TB/s of 2 KB boxes).
 template <int D, int NT>
 struct Cfg {
@@ -837,7 +837,7 @@ cudaError_t launch_attention(const sta_cache& c, CacheArgs a, int sms, cudaStrea
 // Query rows of a unit, from the mean number of rows that a sequence has (its own are known
 // on the device only): units of 16 rows widen the codes once for both halves.  (Units of 32
 // leave 8 warps of 250 registers: 7 requests of 3000-30000 tokens with 1-6 drafted ones,
-// 16 / 2 heads, d = 64, take 54 us, units of 16 take 41.)
+// 16 / 2 heads, d = 64, took 54 us, units of 16 took 41 then and take 36 now.)
 template <int D>
 cudaError_t launch_attention(const sta_cache& c, const CacheArgs& a, int sms, cudaStream_t stream) {
     const int64_t rows = int64_t(a.p.tokens_q) * a.p.group / a.p.batch;

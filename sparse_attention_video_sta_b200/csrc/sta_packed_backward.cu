@@ -39,8 +39,9 @@ using packed::KWork;
 using packed::QBlock;
 using packed::QWork;
 
-// Warps 0-15 elementwise: four to an SM sub-partition, 32 columns of a row to a thread (8 warps
-// of 64 columns leave the round trips of a step uncovered: EWFIG); 16 load, 17 MMA.
+// Warps 0-15 elementwise: four to an SM sub-partition, 32 columns of a row to a thread (8 warps of 64
+// columns cover less of a step's round trips: six sequences of 342-2047 tokens, 16 / 2 heads, d = 64, forward
+// and backward 171 us against 168); 16 load, 17 MMA.
 constexpr int kEwWarps = 16;
 constexpr int kEwThreads = kEwWarps * 32;
 constexpr int kParts = kEwWarps / 4;  // of a row's 128 columns
@@ -575,7 +576,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // ---------------------------------------------------------------- dK / dV
 // Four products for each query block (S^T, dP^T, dV, dK).  8192 causal tokens, 24 / 8 heads, d = 128:
 // 725 us, 1.14 PFLOP/s of products, tensor pipe active 66 %; S^T, dP^T, dV and dK fill TMEM, so a block's
-// exponentials wait for its scores, which wait for the block before.
+// exponentials (1650 of a step's 3550 cycles) wait for its scores, which wait for the P of the block before to
+// be read (750).
 template <int D>
 struct DkvCfg {
     static constexpr int kBlk = 128 * D * 2;
@@ -590,7 +592,8 @@ struct DkvCfg {
     // ds_full, dkv_full, drain, item_full[Q], item_empty[Q]
     static constexpr int kNumBars = 2 * kStages + 8 + 2 * kItemQ;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kQueueOff = kMiscOff + 16;
+    static constexpr int kBlockOff = kMiscOff + 16;  // of each stage: limit0 and tokens of its query block
+    static constexpr int kQueueOff = kBlockOff + (8 * kStages + 15) / 16 * 16;
     static constexpr int kLostOff = kQueueOff + kItemQ * int(sizeof(QWork));  // kLostWords
     static constexpr int kSmemBytes = kLostOff + 4 * packed::kLostWords + 1024;
     static_assert(kQueueOff % 16 == 0, "queue entries are 16-byte aligned");
@@ -624,6 +627,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     volatile uint32_t* lost = reinterpret_cast<volatile uint32_t*>(smem + C::kLostOff);
+    int2* blocks = reinterpret_cast<int2*>(smem + C::kBlockOff);
     KWork* item_q = reinterpret_cast<KWork*>(smem + C::kQueueOff);
     const int rows_used = (128 / p.group) * p.group;  // rows of a query block's box
 
@@ -688,13 +692,18 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 load_block<D>(base + C::kKOff, &tm_k, kv_full, hk, kb.key0);
                 load_block<D>(base + C::kVOff, &tm_v, kv_full, hk, kb.key0);
                 ++kvc;
+                QBlock next{};  // (fetched a step ahead, while the stage is waited for)
+                if (kb.n > 0) next = p.v.qblocks[kb.q0];
                 for (int32_t j = 0; j < kb.n; ++j) {
+                    const QBlock qb = next;
+                    if (j + 1 < kb.n) next = p.v.qblocks[kb.q0 + j + 1];
                     const int r = int(sit % NS);
                     if (sit >= uint32_t(NS) && !wait_bw(st_empty(r), ((sit / NS) - 1) & 1u, abort_flag, p)) {
                         ok = false;
                         break;
                     }
-                    const int32_t tok = p.v.qblocks[kb.q0 + j].tok0;
+                    const int32_t tok = qb.tok0;
+                    blocks[r] = make_int2(qb.limit0, qb.ntok);
                     const int64_t row = (int64_t(kb.q0 + j) * K + hk) * 128;
                     const uint32_t st = base + stage_off(r);
                     ptx::mbar_arrive_expect_tx(st_full(r), 2 * (D / 64) * p.q_box_bytes + 1024);
@@ -816,7 +825,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 ptx::tc_fence_after();
                 uint8_t* st = smem + stage_off(r);
-                const int32_t limit0 = p.v.qblocks[kb.q0 + j].limit0, rows = p.v.qblocks[kb.q0 + j].ntok * p.group;
+                const int32_t limit0 = blocks[r].x, rows = blocks[r].y * p.group;
                 const bool ragged = rows < rows_used;
                 // query rows [from, to) of this part see this thread's key
                 const int from = (p.causal ? p.group * max(0, kb.pos + row - limit0 + 1) : 0) - 32 * h, to = rows - 32 * h;

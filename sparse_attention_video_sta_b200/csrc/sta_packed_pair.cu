@@ -9,17 +9,18 @@
 // other's exponentials.  The price is that an item's own steps follow one another, S(i + 1)
 // after P(i) V: P lies over S, and TMEM holds two S and two O.
 //
-//   warps 0-3, 4-7 : softmax and epilogue of slot 0, 1 (a thread for each row)
+//   warps 0-3, 4-7 : softmax of slot 0, 1 (a thread for each row)
 //   warps 8, 9     : loads of slot 0, 1
 //   warps 10, 11   : S = Q K^T and O += P V of slot 0, 1
+//   warps 12-15    : O / l of both slots, whichever is done, to memory, while the softmax goes on
 //
-// Masks and rows that are not there: as in sta_packed.cu; the V rows behind a sequence's last key
-// are cleared by the softmax warpgroup before it hands over its P.
-// Measured: 20736 queries of two videos on 226 and 100 text keys, 24 heads, d = 128: 115 us (152 one item
-// at a time; the tensors alone are 40 us of HBM).  Of an item's 13800 cycles its own steps are
-// 5500 of softmax, 4100 of epilogue and 3000 of waiting for loads and products: with two warps to
-// an SM sub-partition (TMEM holds no third S and O) these round trips are what bounds it.
-// The epilogue turns each warp's 32 rows through shared memory, so that a store instruction
+// Masks and rows that are not there: as in sta_packed.cu; V rows that no row of the block sees are
+// cleared by the softmax warpgroup before it hands over its P.
+// Measured: 20736 queries of two videos on 226 and 100 text keys, 24 heads, d = 128: 103 us (152 one item
+// at a time; 117 with the softmax warps storing O themselves; the tensors alone are 40 us of HBM).  No unit
+// is busy for more than a third of the time: an item's steps follow one another (loads, product, maximum,
+// exponentials, product), and TMEM holds no third S and O.
+// The storing warps turn their 32 rows through shared memory, so that a store instruction
 // writes 128 bytes of four rows, not 16 of 32.
 #include <cuda.h>
 #include <cuda_bf16.h>
