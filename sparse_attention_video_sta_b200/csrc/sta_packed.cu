@@ -670,10 +670,10 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) packed_join_kernel(const Fw
 
 // Are the walks short enough for two items at a time (sta_packed_pair.cu)?  By the mean number of
 // keys of a sequence; 16384 tokens, pair / one at a time, us: d = 128, 24 / 8 heads, causal, sequences
-// of 256: 107 / 140, 512: 137 / 152, 1024: 194 / 191, 4096: 537 / 441; 24 / 24 heads, not causal, 512: 169 / 174,
-// 1024: 291 / 263; d = 64, 16 / 2 heads, causal, 1024: 115 / 143, 2048: 189 / 225, 4096: 324 / 323, 8192: 611 / 550.
+// of 256: 103 / 145, 512: 140 / 157, 768: 169 / 173, 1024: 203 / 195, 4096: 577 / 470; 24 / 24 heads, not causal,
+// 512: 162 / 198, 1024: 294 / 297; d = 64, 16 / 2 heads, causal, 1024: 118 / 124, 2048: 193 / 180, 4096: 330 / 278.
 bool short_walks(const PackedProblem& p, int head_dim) {
-    return p.tokens_k <= int64_t(p.batch) * (head_dim == 128 ? 768 : 3500);
+    return p.tokens_k <= int64_t(p.batch) * (head_dim == 128 ? 768 : 1500);
 }
 
 template <int D>

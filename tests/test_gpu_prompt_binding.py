@@ -169,3 +169,47 @@ def test_no_grad_history_and_contiguous_outputs(sta):
         o, lse = sta.sta_cache_attention(x[:0], *c, torch.zeros(0, 1, dtype=torch.int32, device="cuda"),
                                          torch.zeros(0, dtype=torch.int32, device="cuda"), cu)
         assert o.shape == (0, 2, 64) and lse.shape == (2, 0)
+
+
+def test_captured_between_other_work_and_over_two_streams(sta):
+    """Kernels that start while the one before ends, in a graph: after another library's kernels and copies, after
+    events, and on two streams that meet again; replayed with new inputs, against eager calls."""
+    a = packed_args()
+    c = cache_args(blocks=8)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    new, lengths, free, count = i32([5, 4]), i32([0, 0]), torch.arange(8, dtype=torch.int32, device="cuda"), i32([8])
+    src = torch.randn(9, 4, 64, device="cuda")
+    q, k = torch.empty(9, 4, 64, device="cuda", dtype=BF), torch.empty(9, 2, 64, device="cuda", dtype=BF)
+
+    def step(side):
+        q.copy_(src)
+        k.copy_(src[:, :2] * 0.5)
+        o, lse = sta.sta_packed_attention(q, k, k, a["cu_q"])
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            table = torch.full((2, 2), -1, dtype=torch.int32, device="cuda")
+            f = free.clone()
+            s = sta.sta_cache_extend(new, lengths, table, f, count, 32, 9)
+            sta.sta_cache_append(k, k, s.slots, *c)
+        grads = sta.sta_packed_attention_backward(q, k, k, o, lse, o * 2, a["cu_q"])
+        here.wait_stream(side)
+        got = sta.sta_cache_attention(q, *c, table, s.lengths, a["cu_q"])
+        return (o, lse, *grads, *got, got[0] + 1)
+    side = torch.cuda.Stream()
+    want = []
+    inputs = [torch.randn(9, 4, 64, device="cuda") for _ in range(3)]
+    for x in inputs:
+        src.copy_(x)
+        want.append([t.clone() for t in step(side)])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(side)
+    for x, w in list(zip(inputs, want)) * 3:
+        src.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, r) for p, r in zip(out, w))
+    assert sta.sta_operator_status() == 0
+    del g
