@@ -427,10 +427,10 @@ STA_API sta_status sta_packed_workspace(const sta_packed* p, int32_t backward, i
  *   workspace, workspace_bytes: device, 256-byte aligned, at least
  *             sta_packed_workspace bytes; need not be initialised
  * Scores, softmax statistics and O accumulate in fp32; P enters P V as bf16.
- * A masked key's score never counts, whatever it holds, and the rows of other
- * sequences and behind the last one are never mixed in; only a non-finite V
- * row can reach the other queries of its own sequence's 128-key block (0 x
- * inf).  Every sequence being empty, or batch 0, is not an error.
+ * What a query does not see never counts, whatever it holds (infinities and
+ * NaN in K or V behind the causal diagonal, in other sequences or behind the
+ * last one): a query's results are the same bits as without it.  Every sequence
+ * being empty, or batch 0, is not an error.
  * Errors: INVALID_ARG (null, misaligned or short buffers, bad sizes, strides
  * or scale), UNSUPPORTED (head_dim, more than 128 query heads to a key head,
  * sizes past 2^31 - 1 rows of work), CUDA. */
@@ -442,8 +442,9 @@ STA_API sta_status sta_packed_forward(const sta_packed* p, const sta_rows* q, co
  * a key head are summed over its query heads in fp32).  o and lse as written
  * by the forward for the same problem; dout, dq like q, dk, dv like k; the
  * outputs are distinct from every input.  Every row of every sequence is
- * written, a key that no query sees with zeros.  P and dS enter the products as
- * bf16 with fp32 accumulation.  No atomics on results. */
+ * written, a key that no query sees with zeros; what a query does not see, and
+ * the queries that do not see a key, never count, as in the forward.  P and dS
+ * enter the products as bf16 with fp32 accumulation.  No atomics on results. */
 STA_API sta_status sta_packed_backward(const sta_packed* p, const sta_rows* q, const sta_rows* k, const sta_rows* v,
                                        const sta_rows* o, const sta_rows* dout, const float* lse, const sta_rows* dq,
                                        const sta_rows* dk, const sta_rows* dv, void* workspace,
@@ -492,7 +493,8 @@ STA_API sta_status sta_cache_append(const sta_cache* c, const sta_rows* k, const
  * Query i of nq sees the first lengths[b] - nq + i + 1 tokens.  Products with
  * K and V are of fp16 operands (the codes exactly, Q scaled by a power of two
  * for each row, P rounded) with fp32 accumulation.  What a block holds behind
- * its sequence's last token is never mixed in.  Tokens of a block whose id is
+ * its sequence's last token is never mixed in, nor what a query does not see (NaN
+ * codes of later queries' tokens).  Tokens of a block whose id is
  * outside the pool are not seen, nor are tokens past table_width blocks; both
  * are reported by sta_operator_status as BOUNDS.  The keys are split over the
  * GPU and joined in a fixed order.  Workspace: sta_cache_workspace bytes,

@@ -560,3 +560,34 @@ def test_extend_the_largest_tables(sta):
     got = t.tolist()
     for b, n in enumerate(held):
         assert got[b][:-(-n // bt)] == table[b][:-(-n // bt)]
+
+
+def test_extend_over_a_cluster_first_called_inside_a_capture():
+    """A fresh process captures a step of many slots (a cluster of CTAs) before any other call."""
+    code = """
+import torch
+import sparse_attention_video_sta_b200 as sta
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+new, n, free, count = i32([9000, 3, -1]), i32([5, 0, 40]), torch.arange(700, dtype=torch.int32, device="cuda"), i32([600])
+table = torch.arange(100, 100 + 3 * 600, dtype=torch.int32, device="cuda").view(3, 600) % 700
+torch.cuda.synchronize()
+def run():
+    t, f = table.clone(), free.clone()
+    return (t, f) + tuple(sta.sta_cache_extend(new, n, t, f, count, 16, 20000))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+want = run()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and int(want[-1]) == 0 and int((want[2] >= 0).sum()) == 9003
+del graph
+print("fine")
+"""
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-3000:]
