@@ -15,35 +15,33 @@ constexpr int kThreads = 1024;
 constexpr int kBins = 1024;     // walks are ordered by min(steps, kBins - 1), falling
 constexpr int kNear = 1024;     // up to this many sequences the bounds stay in shared memory
 
+// Inclusive scans of two values over the CTA's threads with `op`: one barrier, every warp joins the
+// warps' totals for itself; two buffers in turn, so that the next scan need not wait for its readers.
 struct Scan {
-    int32_t sh[32];
+    int2 (*sh)[32];
+    int turn;
 };
-
-// Inclusive scan over the CTA's threads with `op`.
 template <class Op>
-__device__ int32_t scan(int32_t v, Scan& s, const Op& op) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ int2 warp_scan(int2 v, const Op& op) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
-        const int32_t y = __shfl_up_sync(~0u, v, i);
-        if (lane >= i) v = op(v, y);
+        const int32_t x = __shfl_up_sync(~0u, v.x, i), y = __shfl_up_sync(~0u, v.y, i);
+        if (lane >= i) v = make_int2(op(v.x, x), op(v.y, y));
     }
-    if (lane == 31) s.sh[warp] = v;
+    return v;
+}
+template <class Op>
+__device__ int2 scan(int2 v, Scan& s, const Op& op) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_scan(v, op);
+    if (lane == 31) s.sh[s.turn][warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        int32_t x = s.sh[lane];
-#pragma unroll
-        for (int i = 1; i < 32; i <<= 1) {
-            const int32_t y = __shfl_up_sync(~0u, x, i);
-            if (lane >= i) x = op(x, y);
-        }
-        s.sh[lane] = x;
-    }
-    __syncthreads();
-    if (warp > 0) v = op(v, s.sh[warp - 1]);
-    const int32_t r = v;
-    __syncthreads();
-    return r;
+    const int2 all = warp_scan(s.sh[s.turn][lane], op);
+    s.turn ^= 1;
+    const int from = warp > 0 ? warp - 1 : 0;
+    const int32_t x = __shfl_sync(~0u, all.x, from), y = __shfl_sync(~0u, all.y, from);
+    return warp > 0 ? make_int2(op(v.x, x), op(v.y, y)) : v;
 }
 
 // The sequence that block e belongs to: the last b with first[b] <= e.
@@ -116,8 +114,9 @@ __device__ int32_t make_walks(int32_t n, int32_t kv_heads, bool split, int32_t s
         for (int e0 = 0; e0 < n; e0 += kThreads) {
             const int e = e0 + threadIdx.x;
             const int32_t w = e < n ? work(e) : 0, parts = e < n ? (w > cap ? (w + cap - 1) / cap : 1) : 0;
-            const int32_t at = walks + scan(parts, s, add_) - parts;
-            const int32_t more = parts > 1 ? parts : 0, slot = slots + scan(more, s, add_) - more;
+            const int32_t more = parts > 1 ? parts : 0;
+            const int2 upto = scan(make_int2(parts, more), s, add_);
+            const int32_t at = walks + upto.x - parts, slot = slots + upto.y - more;
             if (threadIdx.x == kThreads - 1) {
                 sh_end[0] = at + parts;
                 sh_end[1] = slot + more;
@@ -142,7 +141,7 @@ __device__ int32_t make_walks(int32_t n, int32_t kv_heads, bool split, int32_t s
     }
     __syncthreads();
     const int32_t mine = bins[threadIdx.x];
-    const int32_t upto = scan(mine, s, add_);
+    const int32_t upto = scan(make_int2(mine, 0), s, add_).x;
     bins[threadIdx.x] = upto - mine;
     __syncthreads();
     for (int i = threadIdx.x; i < walks; i += kThreads) {
@@ -196,7 +195,8 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
         clear_tails(p, tails, head_dim);
         return;
     }
-    __shared__ Scan s;
+    __shared__ int2 sh_scan[2][32];
+    Scan s{sh_scan, 0};
     __shared__ int32_t bins[kBins];
     __shared__ int32_t near_[4][kNear + 1];
     __shared__ int32_t near_work[kNearBlocks];
@@ -209,8 +209,14 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
     // ---- bounds cut to the tensors and made rising; blocks counted
     int32_t cq = 0, ck = 0, nbq = 0, nbk = 0;  // carried over passes of 1024 sequences
     bool cut = false;
+    int32_t rq = INT32_MIN, rk = INT32_MIN;  // this thread's bounds (the first pass's are on their way with the starts)
+    auto fetch = [&](int i) {
+        rq = i < B ? p.cu_q[i + 1] : INT32_MIN;
+        rk = i < B ? p.cu_k[i + 1] : INT32_MIN;
+    };
     if (B > 0) {
         const int32_t a = p.cu_q[0], b = p.cu_k[0];
+        fetch(tid);
         cq = max(0, min(a, p.tokens_q));
         ck = max(0, min(b, p.tokens_k));
         cut = a != cq || b != ck;
@@ -222,8 +228,9 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
     }
     for (int i0 = 0; i0 < B; i0 += kThreads) {
         const int i = i0 + tid;
-        const int32_t rq = i < B ? p.cu_q[i + 1] : INT32_MIN, rk = i < B ? p.cu_k[i + 1] : INT32_MIN;
-        const int32_t hq = max(cq, scan(min(rq, p.tokens_q), s, max_)), hk = max(ck, scan(min(rk, p.tokens_k), s, max_));
+        if (i0 > 0) fetch(i);
+        const int2 top = scan(make_int2(min(rq, p.tokens_q), min(rk, p.tokens_k)), s, max_);
+        const int32_t hq = max(cq, top.x), hk = max(ck, top.y);
         cut |= i < B && (rq != hq || rk != hk);
         if (i < B) {
             bound[0][i + 1] = hq;
@@ -231,8 +238,8 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
         }
         __syncthreads();
         const int32_t nq = i < B ? hq - bound[0][i] : 0, nk = i < B ? hk - bound[1][i] : 0;
-        const int32_t bq = nbq + scan((nq + tpb - 1) / tpb, s, add_);
-        const int32_t bk = backward ? nbk + scan((nk + kRows - 1) / kRows, s, add_) : 0;
+        const int2 blocks = scan(make_int2((nq + tpb - 1) / tpb, (nk + kRows - 1) / kRows), s, add_);
+        const int32_t bq = nbq + blocks.x, bk = backward ? nbk + blocks.y : 0;
         if (i < B) {
             bound[2][i + 1] = bq;
             bound[3][i + 1] = bk;
