@@ -92,7 +92,7 @@ __device__ int32_t make_walks(int32_t n, int32_t kv_heads, bool split, int32_t s
             mine += __shfl_xor_sync(~0u, mine, i);
             most = max(most, __shfl_xor_sync(~0u, most, i));
         }
-        if (threadIdx.x % 32 == 0) {
+        if (threadIdx.x % 32 == 0 && most > 0) {
             atomicAdd(&sh_total, mine);
             atomicMax(&sh_most, most);
         }
