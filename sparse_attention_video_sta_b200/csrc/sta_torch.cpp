@@ -116,6 +116,14 @@ Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Device& dev) 
 }
 Tensor like(const Tensor& t) { return fresh(t.sizes(), t.scalar_type(), t.device()); }
 
+// `n` elements of a new vector from `at` on.
+Tensor part(const Tensor& t, int64_t at, int64_t n) {
+    auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+    impl->set_storage_offset(at);
+    impl->set_sizes_contiguous({n});
+    return Tensor(std::move(impl));
+}
+
 Tensor scratch(const OptTensor& given, int64_t need, const at::Device& dev) {
     if (!given.has_value()) return need == 0 ? Tensor() : fresh({need}, at::kByte, dev);
     const Tensor& w = *given;
@@ -309,18 +317,16 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor> cache_extend(const Tensor& ne
     int32_t* cp = vec<int32_t>("free_count", free_count, dev, 1);
     const Tables t = tables(block_tables, B, dev);
     const On on(dev, stream);
-    const Tensor slots = fresh({std::max<int64_t>(max_slots, 0)}, at::kLong, dev), cu = fresh({B + 1}, at::kInt, dev),
-                 brief = fresh({1}, at::kInt, dev);
-    const Tensor len_out = in_place ? lengths : fresh({B}, at::kInt, dev), count_out = in_place ? free_count : fresh({1}, at::kInt, dev);
+    // the small ones lie in one allocation
+    const Tensor slots = fresh({std::max<int64_t>(max_slots, 0)}, at::kLong, dev), small = fresh({2 * B + 3}, at::kInt, dev);
+    const Tensor cu = part(small, 0, B + 1), brief = part(small, B + 1, 1);
+    const Tensor len_out = in_place ? lengths : part(small, B + 3, B), count_out = in_place ? free_count : part(small, B + 2, 1);
     call("sta_cache_extend", f_cache_extend, int32_t(B), int32_t(block_tokens), np, lp, static_cast<int32_t*>(len_out.data_ptr()), t.p, t.width,
                          t.stride, fp, int32_t(free_blocks.size(0)), cp, static_cast<int32_t*>(count_out.data_ptr()),
                          static_cast<int64_t*>(slots.data_ptr()), max_slots, static_cast<int32_t*>(cu.data_ptr()),
                          static_cast<int32_t*>(brief.data_ptr()), on.handle);
-    for (const Tensor& x : {slots, cu, brief}) on.keep(x);
-    if (!in_place) {
-        on.keep(len_out);
-        on.keep(count_out);
-    }
+    on.keep(slots);
+    on.keep(small);
     return {slots, cu, len_out, count_out, brief};
 }
 
