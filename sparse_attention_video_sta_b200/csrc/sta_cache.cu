@@ -296,7 +296,7 @@ __device__ void each_of(int n, Get get, Put put) {
 // pushes, meet, and share the tables and slots.  The reads of `len` and `count`
 // come before the cluster's meeting and their writes after it, so the outputs
 // may be the inputs.  Latency-bound: one launch in place of a chain of scans (64 requests, one token
-// each: 8.8 us a call, nearly all of it the host's; 500 requests with 121000 new tokens: 11 us).  Its steps
+// each: 6.6 us a call, nearly all of it the host's; 500 requests with 121000 new tokens: 11 us).  Its steps
 // are round trips: loads go four at a time, the three sums share their barriers, and a warp
 // finds the requests of its 128 slots by ballots (a binary search in each thread: 20 us).
 __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const ExtendParams p) {

@@ -142,6 +142,7 @@ __device__ __forceinline__ void self_items(const PackedProblem& p, QWork* items,
         w.slot = -1;
         w.hk = u % p.kv_heads;
         if (lane == 0) items[i] = w;
+        if (!any) break;  // (an end)
     }
     __syncwarp();
 }

@@ -150,10 +150,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
 
     if (warp >= kLoadWarp && warp < kLoadWarp + 2) {
         ptx::regs_dec<kRegsProducer>();
-        if (p.self) {
-            self_items(p.prob, item_q, id, ids);
-            if (p.prob.clear_tail && slot == 0) self_clear(p.prob, D, p.o, p.lse);
-        }
+        if (p.self) self_items(p.prob, item_q, id, ids);
         if (lane == 0) {
             // ------------------------------------------------------------ load
             const int32_t n_items = p.self ? 0 : p.v.lists->w_q * K;
@@ -220,6 +217,8 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 drain_bar(v_full(int(it % S)), (it / S) & 1u, p.timeout_ns);
             if (qi > 0) drain_bar(q_full, (qi - 1) & 1u, p.timeout_ns);
         }
+        __syncwarp();
+        if (p.self && p.prob.clear_tail && slot == 0) self_clear(p.prob, D, p.o, p.lse);
     } else if (warp >= kStoreWarp) {
         ptx::regs_dec<kRegsStore>();
         // ------------------------------------------------------------ O / l -> bf16
