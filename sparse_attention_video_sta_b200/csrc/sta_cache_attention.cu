@@ -370,7 +370,8 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         const int t0 = first, t1 = last;
         const int rows = min(kRows, sq.nq * G - rt * kRows);
         // keys that row r sees: the first raw - nq + token + 1; never more than the table holds
-        auto limit_of = [&](int r) { return min(sq.len, sq.raw - sq.nq + (rt * kRows + r) / G + 1); };
+        const uint32_t uG = uint32_t(G);  // (an unsigned division is half a signed one's instructions)
+        auto limit_of = [&](int r) { return min(sq.len, sq.raw - sq.nq + int(uint32_t(rt * kRows + r) / uG) + 1); };
         const int least = limit_of(0);  // the smallest limit of the rows
 
         // ---- pages: lane i holds page `p0 + i` of the warp's run; the copies run ahead of the tiles, so the
@@ -417,8 +418,8 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * 8 + g, row = rt * kRows + r;
             const bool have = r < rows;
-            const __nv_bfloat16* src =
-                a.q.p + int64_t(sq.q0 + (have ? row / G : 0)) * a.q.ts + (hk * G + (have ? row % G : 0)) * a.q.hs;
+            const uint32_t tok = have ? uint32_t(row) / uG : 0u, head = have ? uint32_t(row) - tok * uG : 0u;
+            const __nv_bfloat16* src = a.q.p + int64_t(sq.q0 + int(tok)) * a.q.ts + (hk * G + int(head)) * a.q.hs;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 q_raw[nt][i] = make_uint4(0u, 0u, 0u, 0u);

@@ -42,6 +42,7 @@ using namespace packed_fwd;
 constexpr int kThreads = 512;
 constexpr int kLoadWarp = 8, kMmaWarp = 10;  // + slot
 constexpr int kStoreWarp = 12;
+// (20736 queries on text keys: 102 us so; 176 / 64 / 96: 109, 192 / 48 / 80: 119, 192 / 56 / 72: 108.)
 constexpr uint32_t kRegsSoftmax = 184, kRegsProducer = 64, kRegsStore = 80;
 static_assert(128 * (2 * kRegsSoftmax + kRegsProducer + kRegsStore) <= kThreads * 128, "register split exceeds the launch");
 constexpr uint32_t kTmemCols = 512;
