@@ -270,8 +270,8 @@ __device__ __forceinline__ void join_row(int64_t s, int64_t n, int share, const 
 // which fp16 and fp32 bear and which makes rescaling O rare.  Q is scaled by a power of two
 // for each row into fp16's range.
 // HBM-bound: 2 D bytes for each token and key head.  64 requests of 500-8000 tokens, 24 / 8 heads, d = 128
-// (313 MB): 72.5 us a call, 4.3 TB/s; the copies alone, without the products, take 70 (the
-// plan, the first copies' latency, the joins and 5.4 TB/s of 2 KB boxes).
+// (313 MB): 71 us a call, 4.4 TB/s: the plan, the first copies' latency, the joins and 5.4 TB/s of
+// 2 KB boxes between them (leaving the products out saved 7 of 77 us when it took that).
 template <int D, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;
