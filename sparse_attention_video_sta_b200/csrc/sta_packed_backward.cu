@@ -130,7 +130,13 @@ __device__ __forceinline__ void store_cols(uint32_t taddr, float mul, __nv_bfloa
     }
 }
 
-// The same as fp32, as they are: a part's sums, four columns of all rows after four columns (a warp's
+// 32 columns of zeros.
+__device__ __forceinline__ void zero_cols(__nv_bfloat16* dst) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(dst)[j] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// As store_cols, but fp32 as they are: a part's sums, four columns of all rows after four columns (a warp's
 // stores are whole lines).  `dst`: the part's four columns that `taddr` begins with, this thread's row.
 template <class Fix>
 __device__ __forceinline__ void store_part(uint32_t taddr, float4* dst, bool store, Fix&& fix) {
@@ -687,13 +693,13 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!put_item(kq, kb, p.v.kwalks, &p.v.lists->next_k, n_items, K, item_full0, item_empty0, item_q, abort_flag, p))
                     break;
                 const int32_t hk = kb.hk;
+                if (kb.n == 0) continue;  // no query sees these keys: the elementwise warps write their zeros
                 if (!wait_bw(kv_empty, (kvc & 1u) ^ 1u, abort_flag, p)) break;
                 ptx::mbar_arrive_expect_tx(kv_full, 2 * C::kBlk);
                 load_block<D>(base + C::kKOff, &tm_k, kv_full, hk, kb.key0);
                 load_block<D>(base + C::kVOff, &tm_v, kv_full, hk, kb.key0);
                 ++kvc;
-                QBlock next{};  // (fetched a step ahead, while the stage is waited for)
-                if (kb.n > 0) next = p.v.qblocks[kb.q0];
+                QBlock next = p.v.qblocks[kb.q0];  // (fetched a step ahead, while the stage is waited for)
                 for (int32_t j = 0; j < kb.n; ++j) {
                     const QBlock qb = next;
                     if (j + 1 < kb.n) next = p.v.qblocks[kb.q0 + j + 1];
@@ -732,6 +738,9 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
                 if (kb.n < 0) break;
                 const int32_t n = kb.n;
+                // No commit without an arrival of every elementwise warp before it: dkv_full is waited for by
+                // parity, and several such items in a row would run phases ahead of a warp that still stores.
+                if (n == 0) continue;
                 if (!wait_bw(kv_full, kvc & 1u, abort_flag, p)) break;
                 ++kvc;
                 ptx::tc_fence_after();
@@ -762,10 +771,8 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     ptx::mma_commit(dp_full);
                 };
-                if (n > 0) {
-                    ok = issue_s(0);
-                    if (ok) issue_dp(0);
-                }
+                ok = issue_s(0);
+                if (ok) issue_dp(0);
                 for (int32_t j = 0; ok && j < n; ++j) {
                     const uint32_t it = gs + uint32_t(j);
                     const uint32_t st = base + stage_off(int(it % NS));
@@ -814,6 +821,15 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (lane == 0) ptx::mbar_arrive(item_empty0 + 8u * (kq % kItemQ));
             if (kb.n < 0) break;
             const int32_t hk = kb.hk, n = kb.n;
+            // 32 columns of dV or dK for each warpgroup, or (d = 64: four 32s in all) of one of them
+            const int col = D == 128 ? 32 * h : 32 * (h & 1);
+            const bool with_dv = D == 128 || h < 2, with_dk = D == 128 || h >= 2;
+            auto row_of = [&](const Rows& x) { return x.p + int64_t(kb.key0 + row) * x.ts + hk * x.hs + col; };
+            if (n == 0) {  // zeros, and nothing to wait for (such walks are whole)
+                if (with_dv && row < kb.nkeys) zero_cols(row_of(p.out_b));
+                if (with_dk && row < kb.nkeys) zero_cols(row_of(p.out_a));
+                continue;
+            }
             for (int32_t j = 0; j < n; ++j) {
                 const uint32_t step = gs + uint32_t(j);
                 const int r = int(step % NS);
@@ -941,13 +957,9 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ++kvc;
             ptx::tc_fence_after();
             const bool real = row < kb.nkeys;
-            const int64_t tok = kb.key0 + row;
             // Tokens whose rows may have lost something and see this thread's key: a token that sees `limit`
             // keys is the (limit - limit0)-th from the walk's first.
-            const bool fix = n > 0 && lost[kq % packed::kLostWords] == kq + 1;
-            // 32 columns of dV or dK for each warpgroup, or (d = 64: four 32s in all) of one of them
-            const int col = D == 128 ? 32 * h : 32 * (h & 1);
-            const bool with_dv = D == 128 || h < 2, with_dk = D == 128 || h >= 2;
+            const bool fix = lost[kq % packed::kLostWords] == kq + 1;
             auto put_back = [&](const Rows& x, uint32_t (&r)[32]) {
                 if (!fix) return;
                 const QBlock b0 = p.v.qblocks[kb.q0], b1 = p.v.qblocks[kb.q0 + n - 1];
@@ -965,10 +977,8 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (with_dk) store_part(t_dk, part, real, back_q);
                 if (with_dv) store_part(t_dv, part + 128 * D / 4, real, back_do);
             } else {
-                if (with_dv)
-                    store_cols(t_dv, 1.0f, p.out_b.p + tok * p.out_b.ts + hk * p.out_b.hs + col, real, n == 0, back_do);
-                if (with_dk)
-                    store_cols(t_dk, p.scale, p.out_a.p + tok * p.out_a.ts + hk * p.out_a.hs + col, real, n == 0, back_q);
+                if (with_dv) store_cols(t_dv, 1.0f, row_of(p.out_b), real, false, back_do);
+                if (with_dk) store_cols(t_dk, p.scale, row_of(p.out_a), real, false, back_q);
             }
             ptx::tc_fence_before();
             gs += uint32_t(n);

@@ -504,3 +504,24 @@ def test_what_a_causal_mask_hides_does_not_count(sta, nq, nk, H, K, d):
             assert torch.equal(dk[behind], dk0[behind]) and torch.equal(dv[behind], dv0[behind])
             assert not dv[upto, hk].isfinite().any() and not dk[upto, hk].isfinite().any()
         a, ka = a + n, ka + m
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,K,d", [(8, 8, 128), (8, 4, 64)])
+def test_many_keys_that_no_query_sees(sta, H, K, d, causal):
+    """A sequence of keys without queries, more than five of its key blocks to an SM, beside one with both: its dK and
+    dV are zeros, written to rows far apart, the other's are its own, and no wait runs out."""
+    lens_q, lens_k = [300, 0], [300, 24000 * 8 // K]
+    q, k, v, do = make(lens_q, lens_k, H, K, d, seed=41)
+    cq, ck, scale = ref.cu_of(lens_q), ref.cu_of(lens_k), 0.1
+    want = ref.packed(q, k[:300], v[:300], [300], [300], causal, scale, do)
+    o, lse = sta.sta_packed_attention(q, k, v, cq, ck, causal=causal, softmax_scale=scale)
+    for _ in range(3):
+        out = torch.full((2, k.shape[0], 4 * K, d), math.nan, dtype=torch.bfloat16, device="cuda")
+        dk, dv, dq = out[0, :, :K], out[1, :, K:2 * K], torch.empty_like(q)
+        sta.sta_packed_backward(q, k, v, o, lse, do, dq, dk, dv, cq, ck, causal=causal, softmax_scale=scale)
+        assert sta.sta_operator_status() == 0
+        for name, t in (("dq", dq), ("dk", dk[:300]), ("dv", dv[:300])):
+            ref.check(t, want, name)
+        for t in (dk, dv):
+            assert not bool(t[300:].any())
