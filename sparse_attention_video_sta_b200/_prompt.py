@@ -7,6 +7,12 @@ the outputs' and scratch's allocation and the calls into libsta are compiled
 token-major, ``[tokens, heads, d]``, with free token and head strides
 (multiples of 8 elements), so the parts of one fused projection are taken as
 they are.
+
+``stream`` (a ``torch.cuda.Stream`` or a raw handle; default the current one)
+is the stream of a call's kernels and, for new tensors and scratch, of their
+memory: the caller sees to it that this stream is behind what made the inputs
+and in front of what reads the results.  New tensors may be dropped on the
+current stream.
 """
 from __future__ import annotations
 

@@ -213,3 +213,110 @@ def test_captured_between_other_work_and_over_two_streams(sta):
         assert all(torch.equal(p, r) for p, r in zip(out, w))
     assert sta.sta_operator_status() == 0
     del g
+
+
+def calls_with_new_memory(sta):
+    """Each call that allocates outputs or scratch, as f(stream) -> tensors."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)
+    lens = [100, 37] * 20  # more than the forward plans without scratch
+    q, k, v, do, cu = r(sum(lens), 4, 64), r(sum(lens), 2, 64), r(sum(lens), 2, 64), r(sum(lens), 4, 64), ref.cu_of(lens)
+    o, lse = sta.sta_packed_attention(q, k, v, cu)
+    o2, lse2, dq, dk, dv = (torch.empty_like(t) for t in (o, lse, q, k, v))
+    c = cache_args(blocks=200)
+    c[0].view(torch.uint8).copy_((torch.rand(c[0].shape, generator=g, device="cuda") * 100).byte())
+    c[1].copy_(c[0])
+    c[2].fill_(0.01), c[3].fill_(0.01)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.arange(200, dtype=torch.int32, device="cuda").view(2, 100)
+    n, free, count = i32([3000, 777]), torch.arange(90, dtype=torch.int32, device="cuda"), i32([90])
+    new, held, wide = i32([5] * 40), i32([0] * 40), torch.zeros(40, 2, dtype=torch.int32, device="cuda")
+    stock = [(wide.clone(), free.clone()) for _ in range(9)]  # (a call changes them)
+
+    def extend(stream):
+        t, f = stock.pop()
+        return tuple(sta.sta_cache_extend(new, held, t, f, count, 32, 300, stream=stream))
+    return [
+        lambda s: sta.sta_packed_attention(q, k, v, cu, stream=s),
+        lambda s: sta.sta_packed_forward(q, k, v, o2, lse2, cu, stream=s),
+        lambda s: sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu, stream=s),
+        lambda s: sta.sta_packed_backward(q, k, v, o, lse, do, dq, dk, dv, cu, stream=s),
+        lambda s: sta.sta_cache_attention(q[:2], *c, table, n, stream=s),
+        extend,
+    ]
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_new_memory_of_a_call_on_another_stream(sta, which):
+    """Blocks that the current stream has given back while work on them is queued there are not what a call on
+    another stream computes in; and its new tensors, dropped on the current stream, outlast what that has queued."""
+    call = calls_with_new_memory(sta)[which]
+    side, raw = torch.cuda.Stream(), torch.cuda.current_stream()
+    want = [t.clone() for t in call(None)]
+    call(side)
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        spots = [torch.empty(n, dtype=torch.uint8, device="cuda")
+                 for n in [t.numel() * t.element_size() for t in want] + [1 << i for i in range(9, 25)]]
+        used = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in spots]
+        torch.cuda._sleep(400_000_000)
+        for t in spots:
+            t.fill_(0x7f)
+        del spots, t
+        got = call(stream)
+        side.synchronize()
+        assert not raw.query()
+        if which in (0, 2, 4, 5):
+            for t in got:
+                a = t.data_ptr()
+                assert not any(a < hi and lo < a + t.numel() * t.element_size() for lo, hi in used)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    if which in (0, 2, 4, 5):
+        torch.cuda._sleep(400_000_000)
+        kept, p = got[0].clone(), got[0].data_ptr()
+        del got, t
+        with torch.cuda.stream(side):
+            assert all(torch.empty_like(want[0]).data_ptr() != p for _ in range(3)) or raw.query()
+            torch.empty_like(want[0]).fill_(7.0)
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want[0])
+
+
+def test_the_default_stream_from_another_one(sta):
+    """stream=0 while another stream is the current one, and the current stream is what it was afterwards."""
+    a = packed_args()
+    args = (a["q"], a["k"], a["v"], a["cu_q"])
+    want = sta.sta_packed_attention(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = sta.sta_packed_attention(*args, stream=0)
+        assert torch.cuda.current_stream() == side
+        with pytest.raises(ValueError):
+            sta.sta_packed_attention(a["q"], a["k"][:-1], a["v"], a["cu_q"], stream=0)
+        assert torch.cuda.current_stream() == side
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_captured_calls_on_a_stream_that_joined_the_capture(sta):
+    """A call with `stream=` inside a capture, on a stream forked from the captured one: its memory is the graph's,
+    and replays beside eager work on the same streams give the eager results."""
+    calls = calls_with_new_memory(sta)
+    want = [[t.clone() for t in calls[i](None)] for i in (0, 2, 4)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = [calls[i](side) for i in (0, 2, 4)]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        g.replay()
+        other = [calls[i](side) for i in (0, 2, 4)]
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, want, other):
+            assert all(torch.equal(x, y) and torch.equal(z, y) for x, y, z in zip(a, b, c))
+    assert sta.sta_operator_status() == 0
+    del g
