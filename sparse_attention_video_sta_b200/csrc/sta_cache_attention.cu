@@ -850,7 +850,7 @@ cudaError_t launch_attention(const sta_cache& c, CacheArgs a, int sms, cudaStrea
 // 16 / 2 heads, d = 64, took 54 us, units of 16 took 41 then and take 36 now.)
 template <int D>
 cudaError_t launch_attention(const sta_cache& c, const CacheArgs& a, int sms, cudaStream_t stream) {
-    const int64_t rows = int64_t(a.p.tokens_q) * a.p.group / a.p.batch;
+    const int64_t rows = a.p.batch > 0 ? int64_t(a.p.tokens_q) * a.p.group / a.p.batch : 0;
     return rows <= 8 ? launch_attention<D, 1>(c, a, sms, stream) : launch_attention<D, 2>(c, a, sms, stream);
 }
 
@@ -897,9 +897,9 @@ sta_status sta_cache_attention(const sta_cache* c, const sta_packed* p, const in
     if (sta_status st = cache_problem(c, p, true, &a.p); st != STA_OK) return st;
     if (table_width < 1 || table_stride < table_width) return STA_ERR_INVALID_ARG;
     if (int64_t(table_width) * c->block_tokens > INT32_MAX) return STA_ERR_UNSUPPORTED;
-    if (a.p.batch == 0 || a.p.tokens_q == 0) return STA_OK;
-    for (const void* x : {(const void*)lengths, (const void*)block_tables, (const void*)lse})
-        if (x == nullptr || reinterpret_cast<uintptr_t>(x) % 4 != 0) return STA_ERR_INVALID_ARG;
+    if (a.p.tokens_q == 0 || (a.p.batch == 0 && a.p.clear_tail == 0)) return STA_OK;
+    auto bad = [](const void* x) { return x == nullptr || reinterpret_cast<uintptr_t>(x) % 4 != 0; };
+    if (bad(lse) || (a.p.batch > 0 && (bad(lengths) || bad(block_tables)))) return STA_ERR_INVALID_ARG;
     if (!rows_ok(q, a.p.tokens_q) || !rows_ok(o, a.p.tokens_q)) return STA_ERR_INVALID_ARG;
     int64_t need = 0;
     if (sta_status st = sta_cache_workspace(c, p, &need); st != STA_OK) return st;

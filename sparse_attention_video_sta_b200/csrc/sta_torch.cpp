@@ -273,22 +273,19 @@ std::tuple<Tensor, Tensor> cache_attention(const Tensor& q, const Tensor& kc, co
     if (cp == nullptr && T != B) bad(std::to_string(T) + " queries for " + std::to_string(B) + " sequences: give cu_q");
     const Tables t = tables(block_tables, B, dev);
     const On on(dev, stream);
-    const bool new_o = !o_given.has_value();
+    const bool new_o = !o_given.has_value(), new_lse = !lse_given.has_value();
     const Tensor o = new_o ? fresh(q.sizes(), at::kBFloat16, dev) : *o_given;
-    const Tensor lse = lse_given.has_value() ? *lse_given : fresh({H, T}, at::kFloat, dev);
-    const sta_packed p{int32_t(B), int32_t(H), c.kv_heads, int32_t(d), T, 0, cp, nullptr, 1, new_o ? 1 : 0,
+    const Tensor lse = new_lse ? fresh({H, T}, at::kFloat, dev) : *lse_given;
+    // (the call clears the rows of no sequence in both or in neither)
+    const sta_packed p{int32_t(B), int32_t(H), c.kv_heads, int32_t(d), T, 0, cp, nullptr, 1, new_o && new_lse ? 1 : 0,
                        scale.has_value() ? float(*scale) : float(1.0 / std::sqrt(double(d)))};
     const sta_rows rq = rows("q", q, dev, T, H, d), ro = rows("o", o, dev, T, H, d);
     float* lsp = lse_ptr(lse, dev, H, T);
     if (new_o) on.keep(o);
-    if (!lse_given.has_value()) on.keep(lse);
-    if (T == 0 || B == 0) {
-        if (new_o) {
-            o.zero_();
-            lse.fill_(-INFINITY);
-        }
-        return {o, lse};
-    }
+    if (new_lse) on.keep(lse);
+    if (T == 0) return {o, lse};
+    if (new_o && !new_lse) o.zero_();
+    if (new_lse && !new_o) lse.fill_(-INFINITY);
     int64_t need = 0;
     call("sta_cache_workspace", f_cache_workspace, &c, &p, &need);
     const Tensor w = scratch(workspace, need, dev);

@@ -591,3 +591,34 @@ print("fine")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-3000:]
+
+
+@pytest.mark.parametrize("side", [False, True])
+@pytest.mark.parametrize("given", [(), ("o",), ("lse",), ("o", "lse")], ids=lambda g: "-".join(g) or "none")
+@pytest.mark.parametrize("lens_q", [[2, 3], [0, 0], []])
+def test_rows_of_no_sequence_in_given_and_new_outputs(sta, lens_q, given, side):
+    """Given tensors keep the rows behind the last query, new ones have zeros and -inf there, in every mixture and
+    without any sequence."""
+    B = len(lens_q)
+    kc, vc, ks, vs, table = filled_cache([50, 20], 1, 16, 64, seed=6)
+    q = torch.randn(9, 2, 64, device="cuda").bfloat16()
+    n, cu = torch.tensor([50, 20][:B], dtype=torch.int32, device="cuda"), ref.cu_of(lens_q)
+    args, used = (q, kc, vc, ks, vs, table[:B], n), sum(lens_q)
+    want = sta.sta_cache_attention(*args, cu_q=cu)
+    # memory that is handed out again holds something else than zeros and -inf
+    for t in [torch.full_like(q, 3.0), torch.full((2, 9), 3.0, device="cuda")]:
+        del t
+    kw = {"o": torch.full_like(q, 7.0), "lse": torch.full((2, 9), 7.0, device="cuda")}
+    kw = {name: t for name, t in kw.items() if name in given}
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream() if side else None
+    if side:
+        with torch.cuda.stream(s):
+            torch.full_like(q, 3.0), torch.full((2, 9), 3.0, device="cuda")
+    o, lse = sta.sta_cache_attention(*args, cu_q=cu, stream=s, **kw)
+    torch.cuda.synchronize()
+    assert sta.sta_operator_status() == 0
+    assert torch.equal(o[:used], want[0][:used]) and torch.equal(lse[:, :used], want[1][:, :used])
+    assert bool((o[used:] == (7.0 if "o" in given else 0.0)).all())
+    assert bool((lse[:, used:] == (7.0 if "lse" in given else -math.inf)).all())
+    assert all(t is kw[name] for name, t in (("o", o), ("lse", lse)) if name in kw)

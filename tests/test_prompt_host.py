@@ -133,3 +133,13 @@ def test_extend_is_refused():
 def test_timeout_injection_arguments():
     f = sta._lib.sta_debug_inject_operator_timeout
     assert f(2, 50) == INV and f(-1, 50) == INV and f(1, 0) == INV and f(1, 10001) == INV and f(0, 50) == OK
+
+
+def test_cache_attention_without_sequences():
+    """Nothing to clear: no pointer is read.  Rows to clear: the outputs are checked, lengths and tables are not."""
+    r, L = rows(), sta._lib
+    att = lambda clear, q=r, o=r, lse=P, ws=P: L.sta_cache_attention(  # noqa: E731
+        cache(), packed(batch=0, tokens_q=5, cu_q=P, clear_tail=clear), None, None, 4, 4, q, o, lse, ws, 1 << 40, None)
+    assert att(0) == OK and att(0, q=None, o=None, lse=None, ws=None) == OK
+    for kw in (dict(q=None), dict(o=rows(data=P + 8)), dict(lse=None), dict(lse=P + 2), dict(ws=None), dict(ws=P + 16)):
+        assert att(1, **kw) == INV, kw
