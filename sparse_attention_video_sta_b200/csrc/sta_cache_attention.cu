@@ -21,6 +21,7 @@ namespace {
 // times what 1 us of HBM latency needs).
 constexpr int kTile = 16;      // tokens of a tile: in one block, whatever the block size
 constexpr int kPlanWarps = 8;  // warps that sum the sequences
+constexpr int kMostWarps = 12;
 constexpr int kMinTiles = 4;   // a warp takes no fewer tiles, a CTA no fewer than two warps' worth
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -65,13 +66,18 @@ struct Sequence {
     int32_t units;       // row tiles * key heads
 };
 
-__device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b, bool* cut) {
+// Bound i cut to the queries.
+__device__ __forceinline__ int32_t bound(const CacheArgs& a, int i) { return max(0, min(a.p.cu_q[i], a.p.tokens_q)); }
+
+// Sequence b; `top`: the largest bound before its own (0 will do where the bounds do not fall: they are
+// made rising, as in the packed calls, so that no two sequences write the same rows).
+__device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b, int32_t top, bool* cut) {
     Sequence s;
     s.q0 = b;
     s.nq = 1;
     if (a.p.cu_q != nullptr) {
         const int32_t c0 = a.p.cu_q[b], c1 = a.p.cu_q[b + 1];
-        s.q0 = max(0, min(c0, a.p.tokens_q));
+        s.q0 = max(top, min(c0, a.p.tokens_q));
         s.nq = max(s.q0, min(c1, a.p.tokens_q)) - s.q0;
         *cut |= c0 != s.q0 || c1 != s.q0 + s.nq;
     }
@@ -87,33 +93,95 @@ struct PlanShared {
     int64_t scan[kPlanWarps];
     int64_t upto[kPlanWarps * 32];  // tiles of the sequences up to and with b (at most 256 sequences)
     int32_t last;     // end of the last sequence's queries
+    int32_t tops[kPlanWarps];
+    bool fall;        // a bound is below one before it
+    int32_t top[kMostWarps];  // then each warp's, before its next sequence
 };
+
+// Inclusive maxima over a warp's lanes.
+__device__ __forceinline__ int32_t warp_tops(int32_t v) {
+    const int lane = threadIdx.x & 31;
+    for (int i = 1; i < 32; i <<= 1) {
+        const int32_t y = __shfl_up_sync(~0u, v, i);
+        if (lane >= i) v = max(v, y);
+    }
+    return v;
+}
+
+// Bounds that fall (reported): this thread's tiles once more, the bounds made rising, 256 sequences at a time.
+__device__ __forceinline__ int64_t plan_falling(const CacheArgs& a, PlanShared& sh) {
+    const int warp = threadIdx.x / 32;
+    int64_t n = 0;
+    int32_t carry = 0;
+    for (int b0 = 0; b0 < a.p.batch; b0 += kPlanWarps * 32) {
+        const int b = b0 + int(threadIdx.x);
+        const bool mine = warp < kPlanWarps && b < a.p.batch;
+        int32_t top = warp_tops(mine ? bound(a, b) : 0);
+        __syncthreads();
+        if (warp < kPlanWarps && threadIdx.x % 32 == 31) sh.tops[warp] = top;
+        __syncthreads();
+        top = max(top, carry);
+        for (int i = 0; i < kPlanWarps; ++i) {
+            if (i < warp) top = max(top, sh.tops[i]);
+            carry = max(carry, sh.tops[i]);
+        }
+        if (mine) {
+            bool cut = false;
+            const Sequence s = sequence(a, b, top, &cut);
+            n += int64_t(s.tiles) * s.units;
+        }
+    }
+    return n;
+}
+
+// The largest of the bounds before and of sequence b (one warp).
+__device__ __forceinline__ int32_t top_upto(const CacheArgs& a, int b) {
+    int32_t top = 0;
+    for (int i = threadIdx.x & 31; i <= b; i += 32) top = max(top, bound(a, i));
+    return __reduce_max_sync(~0u, top);
+}
 
 // Tiles of all units; the last query row.  (The first 8 warps sum; every thread calls.)
 __device__ int64_t plan_total(const CacheArgs& a, PlanShared& sh, bool report) {
     int64_t n = 0;
     int32_t last = 0;
     bool cut = false;
-    if (threadIdx.x == 0) sh.last = 0;
+    if (threadIdx.x == 0) {
+        sh.last = 0;
+        sh.fall = false;
+    }
     __syncthreads();
-    if (threadIdx.x < kPlanWarps * 32) {
+    if (threadIdx.x < kPlanWarps * 32)
         for (int b = threadIdx.x; b < a.p.batch; b += kPlanWarps * 32) {
-            const Sequence s = sequence(a, b, &cut);
+            const Sequence s = sequence(a, b, 0, &cut);
             n += int64_t(s.tiles) * s.units;
             last = max(last, s.q0 + s.nq);
         }
+    auto share = [&] {  // sums up to and with this thread in its warp; the warp's for the others
         const int lane = threadIdx.x & 31;
         for (int i = 1; i < 32; i <<= 1) {
             const int64_t y = __shfl_up_sync(~0u, n, i);
             if (lane >= i) n += y;
         }
+        if (lane == 31) sh.scan[threadIdx.x / 32] = n;
+    };
+    if (threadIdx.x < kPlanWarps * 32) {
+        share();
         last = __reduce_max_sync(~0u, last);
-        if (lane == 31) {
-            sh.scan[threadIdx.x / 32] = n;
-            atomicMax(&sh.last, last);
+        if (threadIdx.x % 32 == 0) atomicMax(&sh.last, last);
+    }
+    if (__syncthreads_or(cut)) {
+        if (report && threadIdx.x == 0) atomicOr(a.p.status, kDevBounds);
+        bool fall = false;
+        if (a.p.cu_q != nullptr && threadIdx.x < kPlanWarps * 32)
+            for (int b = threadIdx.x; b < a.p.batch; b += kPlanWarps * 32) fall |= bound(a, b + 1) < bound(a, b);
+        if (__syncthreads_or(fall)) {
+            if (threadIdx.x == 0) sh.fall = true;
+            n = plan_falling(a, sh);
+            if (threadIdx.x < kPlanWarps * 32) share();
+            __syncthreads();
         }
     }
-    if (__syncthreads_or(cut) && report && threadIdx.x == 0) atomicOr(a.p.status, kDevBounds);
     int64_t total = 0;
     for (int i = 0; i < kPlanWarps; ++i) {
         if (i < int(threadIdx.x / 32)) n += sh.scan[i];
@@ -136,11 +204,17 @@ __device__ int32_t plan_locate(const CacheArgs& a, const PlanShared& sh, int64_t
             return b;
         }
     int64_t carry = 0;
+    int32_t carry_top = 0;
     for (int b0 = 0;; b0 += 32) {
         bool cut = false;
         int64_t v = 0;
+        int32_t top = 0;
+        if (sh.fall) {
+            top = max(carry_top, warp_tops(b0 + lane < a.p.batch ? bound(a, b0 + lane) : 0));
+            carry_top = __shfl_sync(~0u, top, 31);
+        }
         if (b0 + lane < a.p.batch) {
-            const Sequence s = sequence(a, b0 + lane, &cut);
+            const Sequence s = sequence(a, b0 + lane, top, &cut);
             v = int64_t(s.tiles) * s.units;
         }
         int64_t x = v;
@@ -285,6 +359,7 @@ struct Cfg {
     static constexpr int kBarOff = kRing;
     static constexpr int kSmem = kBarOff + kWarps * kStages * 8 + 1024;
     static_assert(kSmem <= 224 * 1024, "shared memory budget");
+    static_assert(kWarps >= kPlanWarps && kWarps <= kMostWarps, "the plan's warps");
 };
 
 template <int D, int NT>
@@ -327,7 +402,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     int64_t ctas = plan_ctas(total, gridDim.x);
     if (a.p.batch == 1) {  // a unit to a CTA, and nothing for the second kernel to join
         bool cut = false;
-        const Sequence sq = sequence(a, 0, &cut);
+        const Sequence sq = sequence(a, 0, 0, &cut);
         if (sq.units > 0 && sq.units <= int64_t(gridDim.x) && sq.tiles <= kWarps * kAlone) ctas = sq.units;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -350,17 +425,27 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     float* my_part0 = a.warp_parts + (int64_t(blockIdx.x) * kWarps + warp) * kRows * (D + 4);
     int64_t at = begin, before = 0;
     int32_t b = at < end ? plan_locate(a, plan, at, &before) : 0;
+    if (plan.fall && at < end) {
+        const int32_t top = top_upto(a, b);
+        if (lane == 0) plan.top[warp] = top;
+        __syncwarp();
+    }
     uint32_t slot_in = 0, slot_out = 0, phase = 0;  // this warp's ring: next slot to fill, to read, its phase
     uint32_t in_flight = 0;
     bool dead = false;
 
     while (at < end) {
         bool cut = false;
-        const Sequence sq = sequence(a, b, &cut);
+        const Sequence sq = sequence(a, b, plan.fall ? plan.top[warp] : 0, &cut);
         const int64_t in_seq = at - before;
         if (in_seq >= int64_t(sq.tiles) * sq.units) {
             before += int64_t(sq.tiles) * sq.units;
             ++b;
+            if (plan.fall) {
+                __syncwarp();
+                if (lane == 0) plan.top[warp] = sq.q0 + sq.nq;
+                __syncwarp();
+            }
             continue;
         }
         const int unit = int(divide(in_seq, sq.tiles)), first = int(in_seq - int64_t(unit) * sq.tiles);

@@ -622,3 +622,35 @@ def test_rows_of_no_sequence_in_given_and_new_outputs(sta, lens_q, given, side):
     assert bool((o[used:] == (7.0 if "o" in given else 0.0)).all())
     assert bool((lse[:, used:] == (7.0 if "lse" in given else -math.inf)).all())
     assert all(t is kw[name] for name, t in (("o", o), ("lse", lse)) if name in kw)
+
+
+@pytest.mark.parametrize("heads,K,d", [(4, 2, 64), (24, 8, 128), (16, 1, 64)])
+@pytest.mark.parametrize("batch", [1, 2, 3, 64, 256, 257, 700, 1500])
+def test_attention_bounds_that_fall_are_cut_and_reported(sta, batch, heads, K, d):
+    """Bounds of the queries that fall or leave the tensors: the call is the one with the bounds made rising, and says
+    BOUNDS; no row is written by two sequences."""
+    r = random.Random(batch + heads)
+    T = 2 * batch + 5
+    lengths = [r.randint(0, 60) for _ in range(batch - 1)] + [2500]
+    kc, vc, ks, vs, table = filled_cache(lengths, K, 16, d, seed=9)
+    q = torch.randn(T, heads, d, generator=torch.Generator("cuda").manual_seed(1), device="cuda").bfloat16()
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    steady = [min(T, 2 * i) for i in range(batch + 1)]
+    for trial in range(4):
+        bad = list(steady)
+        for i in ([batch] if trial == 0 else [r.randint(1, batch) for _ in range(1 + batch // 5)]):
+            bad[i] = r.choice([-7, 0, 1, T, T + 9, 2 ** 31 - 1, -2 ** 31, r.randint(0, T), max(0, bad[i - 1] - 1)])
+        if trial == 1:
+            bad[1:] = bad[:0:-1]
+        cut, top = [], 0
+        for c in bad:
+            top = max(top, min(c, T))
+            cut.append(top)
+        cu, want_cu = (torch.tensor(c, dtype=torch.int32, device="cuda") for c in (bad, cut))
+        for given in (False, True):
+            kw = [dict(o=torch.full_like(q, 7.0), lse=torch.full((heads, T), 7.0, device="cuda")) if given else {} for _ in range(2)]
+            want = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n, cu_q=want_cu, **kw[0])
+            assert sta.sta_operator_status() == 0
+            got = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n, cu_q=cu, **kw[1])
+            assert sta.sta_operator_status() == (sta.STA_ERR_BOUNDS if bad != cut else 0)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
