@@ -400,7 +400,8 @@ typedef struct {
  * every key); a query that sees none gives O = 0, LSE = -inf and no gradient.
  * Bounds that decrease or reach past the tensors are cut to them on the device
  * (nothing is read or written outside) and reported by
- * sta_operator_status as BOUNDS. */
+ * sta_operator_status as BOUNDS; so is a first bound above 0, whose rows before
+ * the first sequence then belong to none, like those behind the last. */
 typedef struct {
     int32_t batch;            /* sequences, >= 0 */
     int32_t heads, kv_heads;  /* heads a multiple of kv_heads, at most 128 query heads to a key head */
@@ -410,7 +411,7 @@ typedef struct {
     const int32_t* cu_q;      /* device [batch + 1] */
     const int32_t* cu_k;      /* device [batch + 1]; may be cu_q itself */
     int32_t causal;           /* 0 or 1 */
-    int32_t clear_tail;       /* output rows behind the last sequence: 0 left as they were, 1 zeros (lse: -inf) */
+    int32_t clear_tail;       /* output rows of no sequence (behind the last): 0 left as they were, 1 zeros (lse: -inf) */
     float softmax_scale;      /* finite and > 0 */
 } sta_packed;
 

@@ -97,7 +97,8 @@ def sta_packed_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: tor
     ``q`` ``[tokens, heads, d]`` and ``k``, ``v`` ``[tokens_k, kv_heads, d]`` in bf16; sequence ``b`` has the
     query rows ``cu_q[b] : cu_q[b + 1]`` and the key rows ``cu_k[b] : cu_k[b + 1]`` (``cu_k`` defaults to
     ``cu_q``; int32, on the device, read by the kernels).  With ``causal`` a sequence's last query sees
-    every key.  Rows behind the last sequence are left as they were, or zeroed with ``clear_tail``."""
+    every key.  Rows behind the last sequence are left as they were, or zeroed with ``clear_tail``; so are those
+    before the first, though bounds that do not begin at 0 are reported (``sta_operator_status``)."""
     _torch.packed_forward(q, k, v, o, lse, cu_q, cu_k, causal, softmax_scale, clear_tail, workspace, _raw(stream))
     return o, lse
 

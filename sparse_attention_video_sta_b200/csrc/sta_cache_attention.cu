@@ -92,7 +92,7 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b, int32_t 
 struct PlanShared {
     int64_t scan[kPlanWarps];
     int64_t upto[kPlanWarps * 32];  // tiles of the sequences up to and with b (at most 256 sequences)
-    int32_t last;     // end of the last sequence's queries
+    int32_t first, last;  // the first sequence's first query, the end of the last one's queries
     int32_t tops[kPlanWarps];
     bool fall;        // a bound is below one before it
     int32_t top[kMostWarps];  // then each warp's, before its next sequence
@@ -147,13 +147,17 @@ __device__ int64_t plan_total(const CacheArgs& a, PlanShared& sh, bool report) {
     int32_t last = 0;
     bool cut = false;
     if (threadIdx.x == 0) {
-        sh.last = 0;
+        sh.first = sh.last = 0;
         sh.fall = false;
     }
     __syncthreads();
     if (threadIdx.x < kPlanWarps * 32)
         for (int b = threadIdx.x; b < a.p.batch; b += kPlanWarps * 32) {
             const Sequence s = sequence(a, b, 0, &cut);
+            if (b == 0) {
+                sh.first = s.q0;
+                cut |= s.q0 != 0;
+            }
             n += int64_t(s.tiles) * s.units;
             last = max(last, s.q0 + s.nq);
         }
@@ -389,12 +393,13 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     ops::grid_wait();
 
     const int64_t total = plan_total(a, plan, blockIdx.x == 0);
-    if (a.p.clear_tail && plan.last < a.p.tokens_q) {
-        const int32_t tail = a.p.tokens_q - plan.last, parts = D / 8;
-        for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < int64_t(tail) * a.p.heads * parts;
+    if (a.p.clear_tail && plan.last - plan.first < a.p.tokens_q) {  // rows of no sequence
+        const int32_t none = plan.first + a.p.tokens_q - plan.last, parts = D / 8;
+        for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < int64_t(none) * a.p.heads * parts;
              i += int64_t(gridDim.x) * kThreads) {
             const int64_t row = i / parts;
-            const int32_t tok = plan.last + int32_t(row / a.p.heads), h = int32_t(row % a.p.heads);
+            const int32_t nth = int32_t(row / a.p.heads), h = int32_t(row % a.p.heads);
+            const int32_t tok = nth < plan.first ? nth : plan.last + nth - plan.first;
             *reinterpret_cast<uint4*>(a.o.p + tok * a.o.ts + h * a.o.hs + i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
             if (i % parts == 0) a.lse[int64_t(h) * a.p.tokens_q + tok] = -INFINITY;
         }

@@ -112,7 +112,7 @@ __device__ __forceinline__ void self_items(const PackedProblem& p, QWork* items,
         const int32_t y = __shfl_up_sync(~0u, h, 1);
         from = lane == 0 ? start : y;
         n = h - from;
-        const bool cut = c0 != start || (lane < p.batch && c != h);
+        const bool cut = c0 != 0 || (lane < p.batch && c != h);
         if (__any_sync(~0u, cut) && lane == 0 && id == 0) atomicOr(p.status, kDevBounds);
     };
     int32_t q0, nq, key0, nk;
@@ -147,16 +147,18 @@ __device__ __forceinline__ void self_items(const PackedProblem& p, QWork* items,
     __syncwarp();
 }
 
-// Zero the rows behind the last sequence (one warp of each CTA).
+// Zero the rows of no sequence: behind the last, and before the first (one warp of each CTA).
 __device__ __forceinline__ void self_clear(const PackedProblem& p, int head_dim, const Rows& o, float* lse) {
     const int lane = threadIdx.x & 31;
     int32_t last = max(0, min(p.cu_q[lane <= p.batch ? lane : 0], p.tokens_q));
+    const int32_t first = __shfl_sync(~0u, last, 0);
     if (p.batch == kSelfBatch) last = max(last, min(p.cu_q[kSelfBatch], p.tokens_q));
     last = __reduce_max_sync(~0u, last);
-    const int32_t tail = p.tokens_q - last, parts = head_dim / 8;
-    for (int64_t i = int64_t(blockIdx.x) * 32 + lane; i < int64_t(tail) * p.heads * parts; i += int64_t(gridDim.x) * 32) {
+    const int32_t none = first + p.tokens_q - last, parts = head_dim / 8;
+    for (int64_t i = int64_t(blockIdx.x) * 32 + lane; i < int64_t(none) * p.heads * parts; i += int64_t(gridDim.x) * 32) {
         const int64_t row = i / parts;
-        const int32_t tok = last + int32_t(row / p.heads), h = int32_t(row % p.heads);
+        const int32_t nth = int32_t(row / p.heads), h = int32_t(row % p.heads);
+        const int32_t tok = nth < first ? nth : last + nth - first;
         *reinterpret_cast<uint4*>(o.p + tok * o.ts + h * o.hs + i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
         if (i % parts == 0) lse[int64_t(h) * p.tokens_q + tok] = -INFINITY;
     }

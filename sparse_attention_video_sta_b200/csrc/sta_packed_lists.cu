@@ -155,33 +155,41 @@ __device__ int32_t make_walks(int32_t n, int32_t kv_heads, bool split, int32_t s
 }
 static_assert(kBins == kThreads, "one bin for each thread in the scan");
 
-// Zero the rows behind the last sequence (block 0 builds the lists meanwhile).
+// Zero the rows of no sequence: behind the last, and before the first (block 0 builds the lists meanwhile).
 __device__ void clear_tails(const PackedProblem& p, const Tails& t, int head_dim) {
     // the last bound as block 0 cuts it: the running maximum of the clamped bounds
-    __shared__ int32_t last[2];
-    if (threadIdx.x < 2) last[threadIdx.x] = 0;
+    __shared__ int32_t first[2], last[2];
+    if (threadIdx.x < 2) first[threadIdx.x] = last[threadIdx.x] = 0;
     __syncthreads();
     for (int i = threadIdx.x; p.batch > 0 && i <= p.batch; i += blockDim.x) {
-        atomicMax(&last[0], min(p.cu_q[i], p.tokens_q));
-        atomicMax(&last[1], min(p.cu_k[i], p.tokens_k));
+        const int32_t q = min(p.cu_q[i], p.tokens_q), k = min(p.cu_k[i], p.tokens_k);
+        if (i == 0) {
+            first[0] = max(q, 0);
+            first[1] = max(k, 0);
+        }
+        atomicMax(&last[0], q);
+        atomicMax(&last[1], k);
     }
     __syncthreads();
     const int64_t id = int64_t(blockIdx.x - 1) * blockDim.x + threadIdx.x, step = int64_t(gridDim.x - 1) * blockDim.x;
     for (int i = 0; i < t.n; ++i) {
-        const int32_t from = t.is_q[i] ? last[0] : last[1], tokens = t.is_q[i] ? p.tokens_q : p.tokens_k;
-        const int32_t parts = head_dim / 8;
-        const int64_t n = int64_t(tokens - from) * t.heads[i] * parts;
+        const int32_t before = t.is_q[i] ? first[0] : first[1], from = t.is_q[i] ? last[0] : last[1];
+        const int32_t tokens = t.is_q[i] ? p.tokens_q : p.tokens_k, parts = head_dim / 8;
+        const int64_t n = int64_t(before + tokens - from) * t.heads[i] * parts;
         for (int64_t j = id; j < n; j += step) {
             const int64_t row = j / parts;
-            const int32_t tok = from + int32_t(row / t.heads[i]), h = int32_t(row % t.heads[i]);
+            const int32_t nth = int32_t(row / t.heads[i]), h = int32_t(row % t.heads[i]);
+            const int64_t tok = nth < before ? nth : from + nth - before;
             *reinterpret_cast<uint4*>(t.r[i].p + tok * t.r[i].ts + h * t.r[i].hs + (j % parts) * 8) =
                 make_uint4(0u, 0u, 0u, 0u);
         }
     }
     if (t.lse != nullptr) {
-        const int64_t tail = p.tokens_q - last[0];
-        for (int64_t j = id; j < tail * p.heads; j += step)
-            t.lse[(j / tail) * p.tokens_q + last[0] + j % tail] = -INFINITY;
+        const int64_t none = first[0] + p.tokens_q - last[0];
+        for (int64_t j = id; j < none * p.heads; j += step) {
+            const int64_t nth = j % none;
+            t.lse[(j / none) * p.tokens_q + (nth < first[0] ? nth : last[0] + nth - first[0])] = -INFINITY;
+        }
     }
 }
 
@@ -219,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) packed_lists_kernel(const PackedProb
         fetch(tid);
         cq = max(0, min(a, p.tokens_q));
         ck = max(0, min(b, p.tokens_k));
-        cut = a != cq || b != ck;
+        cut = a != 0 || b != 0;  // (rows before the first sequence are no one's)
     }
     if (tid == 0) {
         bound[0][0] = cq;

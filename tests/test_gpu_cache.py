@@ -654,3 +654,27 @@ def test_attention_bounds_that_fall_are_cut_and_reported(sta, batch, heads, K, d
             got = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n, cu_q=cu, **kw[1])
             assert sta.sta_operator_status() == (sta.STA_ERR_BOUNDS if bad != cut else 0)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("batch", [1, 2, 300])
+@pytest.mark.parametrize("given", [False, True])
+def test_queries_before_the_first_sequence_are_no_ones(sta, batch, given):
+    """A first bound above 0 is reported; the rows before it are zeros in new tensors, left alone in given ones."""
+    lengths, lens_q = [5 + i % 40 for i in range(batch)], [1 + i % 3 for i in range(batch)]
+    kc, vc, ks, vs, table = filled_cache(lengths, 2, 16, 64, seed=6)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    first, tail = 4, 3
+    q = torch.randn(first + sum(lens_q) + tail, 8, 64, device="cuda").bfloat16()
+    cu = ref.cu_of(lens_q)
+    rows = slice(first, first + sum(lens_q))
+    want = attention_reference(q[rows], kc, vc, ks, vs, table, lengths, lens_q, 0.125, 16)
+    kw = dict(o=torch.full_like(q, 7.0), lse=torch.full((8, q.shape[0]), 7.0, device="cuda")) if given else {}
+    for t in [torch.full_like(q, 3.0), torch.full((8, q.shape[0]), 3.0, device="cuda")]:
+        del t
+    o, lse = sta.sta_cache_attention(q, kc, vc, ks, vs, table, n, cu_q=cu + first, **kw)
+    assert sta.sta_operator_status() == sta.STA_ERR_BOUNDS
+    ref.check(o[rows], want, "o")
+    ref.check(lse[:, rows], want, "lse")
+    others = [i for i in range(q.shape[0]) if not rows.start <= i < rows.stop]
+    assert bool((o[others] == (7.0 if given else 0.0)).all())
+    assert bool((lse[:, others] == (7.0 if given else -math.inf)).all())

@@ -525,3 +525,39 @@ def test_many_keys_that_no_query_sees(sta, H, K, d, causal):
             ref.check(t, want, name)
         for t in (dk, dv):
             assert not bool(t[300:].any())
+
+
+@pytest.mark.parametrize("lens_q,lens_k,H,K,d", [
+    ([30, 5], [30, 5], 4, 2, 64), ([300, 100], [300, 100], 4, 2, 128), ([60] * 40, [60] * 40, 4, 2, 64),
+    ([3500], [3500], 12, 12, 64), ([40, 70], [0, 0], 4, 2, 64), ([0, 0], [90, 30], 4, 2, 128), ([20], [500], 6, 2, 128)])
+@pytest.mark.parametrize("first_q,first_k", [(3, 3), (50, 0), (0, 17)])
+def test_rows_before_the_first_sequence_are_no_ones(sta, lens_q, lens_k, H, K, d, first_q, first_k):
+    """A first bound above 0 is reported; the rows before it are zeros in new tensors and left alone in given ones,
+    the sequences' own are those of the same bounds with one more sequence in front."""
+    first_q, first_k = (first_q if sum(lens_q) else 0), (first_k if sum(lens_k) else 0)
+    if not first_q and not first_k:
+        first_q = first_k = 2
+    q, k, v, do = make([first_q] + lens_q, [first_k] + lens_k, H, K, d, seed=51)
+    cq, ck = ref.cu_of([first_q] + lens_q), ref.cu_of([first_k] + lens_k)
+
+    def both(a, b, clear):
+        o, dq, dk, dv = (torch.full_like(t, 7.0) for t in (q, q, k, v))
+        lse = torch.full((H, q.shape[0]), 7.0, device="cuda")
+        if clear:
+            o, lse = sta.sta_packed_attention(q, k, v, a, b)
+            return (o, lse) + sta.sta_packed_attention_backward(q, k, v, o, lse, do, a, b)
+        sta.sta_packed_forward(q, k, v, o, lse, a, b)
+        sta.sta_packed_backward(q, k, v, o, lse, do, dq, dk, dv, a, b)
+        return o, lse, dq, dk, dv
+    for clear in (True, False):
+        want = both(cq, ck, clear)
+        assert sta.sta_operator_status() == 0
+        for t in [torch.full_like(x, 3.0) for x in want]:  # memory that is handed out again holds something
+            del t
+        got = both(cq[1:].contiguous(), ck[1:].contiguous(), clear)
+        assert sta.sta_operator_status() == sta.STA_ERR_BOUNDS
+        for name, a, b, n in zip(("o", "lse", "dq", "dk", "dv"), got, want, (first_q, first_q, first_q, first_k, first_k)):
+            if name == "lse":
+                a, b = a.t(), b.t()
+            assert torch.equal(a[n:], b[n:]), name
+            assert bool((a[:n] == (7.0 if not clear else -math.inf if name == "lse" else 0.0)).all()), name
