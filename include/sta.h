@@ -543,10 +543,12 @@ STA_API sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const i
  * returns TIMEOUT.  Mode 0 (the default): off.  Else INVALID_ARG. */
 STA_API sta_status sta_debug_inject_operator_timeout(int32_t mode, int32_t limit_ms);
 
-/* Synchronise `stream`, then report (and clear) the first asynchronous error of
- * the calls of this part on the current device: CUDA, BOUNDS (bounds, block ids
- * or slots out of range, cut as described) or TIMEOUT.  The device has one
- * status word for these calls, whichever stream they ran on. */
+/* Synchronise `stream`, then report (and clear) an asynchronous error of
+ * the calls of this part on the current device: CUDA, TIMEOUT (outputs are
+ * left partly written) or BOUNDS (bounds, block ids or slots out of range, cut
+ * as described).  Where both of the last two are pending, TIMEOUT comes first and
+ * the next call returns BOUNDS.  The device has one status word for these
+ * calls, whichever stream they ran on. */
 STA_API sta_status sta_operator_status(void* stream);
 
 /* Synchronise `stream`, then report (and clear) the first asynchronous error

@@ -204,7 +204,8 @@ def sta_cache_extend(new_tokens: torch.Tensor, lengths: torch.Tensor, block_tabl
 
 
 def sta_operator_status(device=None, stream=None) -> int:
-    """Synchronise and return (clearing it) the status of the calls of this part on ``device``."""
+    """Synchronise and return (clearing it) the status of the calls of this part on ``device``: 0,
+    ``STA_ERR_TIMEOUT`` or ``STA_ERR_BOUNDS`` (of both, the first; the next call then returns the other)."""
     with torch.cuda.device(device):
         s = torch.cuda.current_stream() if stream is None else stream
         h = s.cuda_stream if isinstance(s, torch.cuda.Stream) else int(s)

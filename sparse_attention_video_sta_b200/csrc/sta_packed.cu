@@ -46,7 +46,8 @@ constexpr float kRescaleRowSum = 65536.0f;
 
 constexpr int kMaxDevices = 64;
 __device__ uint32_t g_op_status;  // one word per device: kDevTimeout | kDevBounds
-std::mutex g_status_mutex;
+__device__ uint32_t g_op_taken;   // the bit that sta_operator_status took last
+std::mutex g_status_mutex, g_taken_mutex;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per device-side wait
 std::atomic<int32_t> g_op_inject_ms{0};
 uint32_t* g_status_ptr[kMaxDevices] = {};
@@ -704,6 +705,13 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     return e;
 }
 
+// Takes one bit from the status word, the timeout's first: what other streams' kernels set meanwhile stays.
+__global__ void take_status_kernel(uint32_t* word, uint32_t* taken) {
+    const uint32_t now = atomicOr(word, 0u), bit = (now & kDevTimeout) != 0u ? uint32_t(kDevTimeout) : now & uint32_t(kDevBounds);
+    atomicAnd(word, ~bit);
+    *taken = bit;
+}
+
 // Does the forward plan this problem in the kernel?
 bool self_planned(const PackedProblem& p, const packed::Layout& w) {
     return p.batch > 0 && p.batch <= kSelfBatch && p.tokens_k > 0 && !w.split_q &&
@@ -847,13 +855,16 @@ sta_status sta_operator_status(void* stream) {
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return op_cuda_status(e);
     uint32_t* p = nullptr;
     if (cudaError_t e = op_status_word(&p); e != cudaSuccess) return op_cuda_status(e);
-    uint32_t word = 0;
-    if (cudaError_t e = cudaMemcpy(&word, p, sizeof word, cudaMemcpyDeviceToHost); e != cudaSuccess)
-        return op_cuda_status(e);
-    if (word != 0)
-        if (cudaError_t e = cudaMemset(p, 0, sizeof word); e != cudaSuccess) return op_cuda_status(e);
-    if (word & kDevBounds) return STA_ERR_BOUNDS;
-    return word & kDevTimeout ? STA_ERR_TIMEOUT : STA_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* taken = nullptr;
+    uint32_t bit = 0;
+    std::lock_guard<std::mutex> lock(g_taken_mutex);  // (one g_op_taken for each device)
+    cudaError_t e = cudaGetSymbolAddress(&taken, g_op_taken);
+    if (e == cudaSuccess) e = packed::launch(take_status_kernel, dim3(1), 1, 0, s, false, p, static_cast<uint32_t*>(taken));
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&bit, taken, sizeof bit, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return op_cuda_status(e);
+    return bit == kDevTimeout ? STA_ERR_TIMEOUT : bit == kDevBounds ? STA_ERR_BOUNDS : STA_OK;
 }
 
 }  // extern "C"

@@ -320,3 +320,31 @@ def test_captured_calls_on_a_stream_that_joined_the_capture(sta):
             assert all(torch.equal(x, y) and torch.equal(z, y) for x, y, z in zip(a, b, c))
     assert sta.sta_operator_status() == 0
     del g
+
+
+def test_a_timeout_and_a_cut_bound_are_both_reported(sta):
+    """Both are pending, of one call or of two: the timeout first, whose outputs are lost, then the bound."""
+    a = packed_args()
+    bad = torch.tensor([0, 7, 4, 9], dtype=torch.int32, device="cuda")
+    a["cu_q"] = bad
+    assert sta.sta_operator_status() == 0
+    for one_call in (True, False):
+        sta.sta_debug_inject_operator_timeout(1, 20)
+        try:
+            sta.sta_packed_attention(a["q"], a["k"], a["v"], bad if one_call else ref.cu_of([5, 4]))
+            torch.cuda.synchronize()
+        finally:
+            sta.sta_debug_inject_operator_timeout(0)
+        if not one_call:
+            sta.sta_packed_attention(a["q"], a["k"], a["v"], bad)
+        assert sta.sta_operator_status() == sta.STA_ERR_TIMEOUT
+        assert sta.sta_operator_status(stream=torch.cuda.Stream()) == sta.STA_ERR_BOUNDS
+        assert sta.sta_operator_status() == 0
+    # each alone, asked from several threads at once: said once
+    from concurrent.futures import ThreadPoolExecutor
+    for _ in range(20):
+        sta.sta_packed_attention(a["q"], a["k"], a["v"], bad)
+        torch.cuda.synchronize()
+        with ThreadPoolExecutor(4) as pool:
+            got = list(pool.map(lambda i: sta.sta_operator_status(device=0, stream=torch.cuda.Stream(device=0)), range(4)))
+        assert sorted(got) == [0, 0, 0, sta.STA_ERR_BOUNDS]
