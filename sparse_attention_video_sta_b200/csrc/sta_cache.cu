@@ -219,6 +219,7 @@ cudaError_t launch_append(const sta_cache& c, const Rows& k, const Rows& v, int6
 constexpr int kExtendThreads = 1024;
 constexpr unsigned kExtendCluster = 16;
 constexpr int kMaxRequests = 8192;
+constexpr int extend_smem(int batch) { return (4 * batch + 3) * int(sizeof(int32_t)); }
 
 struct ExtendParams {
     int32_t batch, bt, bt_log2, width, pool;
@@ -430,6 +431,12 @@ __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const Exte
     }
 }
 
+// The kernel's limit on dynamic shared memory belongs to all threads of the process: always the most
+// that any call needs, so that none lowers it under another's launch.
+cudaError_t extend_most_smem() {
+    return cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, extend_smem(kMaxRequests));
+}
+
 // A cluster of 16 where the device has one (the SMs of a GPC; 500 requests, 121000 new tokens: 11 us, with 8
 // CTAs 14.6); asked once for each device.  (The kernel's attribute belongs to the device as well.)
 cudaError_t extend_cluster(unsigned* ctas) {
@@ -439,7 +446,8 @@ cudaError_t extend_cluster(unsigned* ctas) {
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     unsigned n = dev < kDevices ? known[dev].load() : 0u;
     if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaError_t e = extend_most_smem();
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = *ctas;
@@ -447,6 +455,7 @@ cudaError_t extend_cluster(unsigned* ctas) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(*ctas);
         cfg.blockDim = dim3(kExtendThreads);
+        cfg.dynamicSmemBytes = extend_smem(kMaxRequests);  // what is known then holds for every batch
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int fit = 0;
@@ -515,14 +524,11 @@ sta_status sta_cache_extend(int32_t batch, int32_t block_tokens, const int32_t* 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kExtendThreads);
-    cfg.dynamicSmemBytes = size_t(4 * batch + 3) * sizeof(int32_t);
+    cfg.dynamicSmemBytes = extend_smem(batch);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     if (cfg.dynamicSmemBytes > 48 * 1024)
-        if (cudaError_t e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 int(cfg.dynamicSmemBytes));
-            e != cudaSuccess)
-            return op_cuda_status(e);
+        if (cudaError_t e = extend_most_smem(); e != cudaSuccess) return op_cuda_status(e);
     // a serving step's few slots and tables need no second CTA
     unsigned ctas = 1;
     if (max_slots > 8 * kExtendThreads || batch > 4 * kExtendThreads / 32) {

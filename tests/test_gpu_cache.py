@@ -678,3 +678,27 @@ def test_queries_before_the_first_sequence_are_no_ones(sta, batch, given):
     others = [i for i in range(q.shape[0]) if not rows.start <= i < rows.stop]
     assert bool((o[others] == (7.0 if given else 0.0)).all())
     assert bool((lse[:, others] == (7.0 if given else -math.inf)).all())
+
+
+def test_extend_from_several_threads_at_once(sta):
+    """Steps of different sizes (shared memory from a few bytes to the most) called at the same time, each on its
+    own stream: none changes what another's launch needs."""
+    from concurrent.futures import ThreadPoolExecutor
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    free, count = torch.arange(8192, dtype=torch.int32, device="cuda"), i32([8192])
+
+    def steps(batch):
+        lengths, new = i32([5] * batch), i32([12] * batch)  # 17 tokens: one block more of 16
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(150):
+                t, f = torch.zeros(batch, 2, dtype=torch.int32, device="cuda"), free.clone()
+                s = sta.sta_cache_extend(new, lengths, t, f, count, 16, 12 * batch)
+            torch.cuda.current_stream().synchronize()
+        return int(s.short), int(s.free_count), s.slots[-1].item()
+    torch.cuda.synchronize()
+    sizes = [8192, 3100, 4000, 8192, 6000, 100, 3500, 5000]
+    with ThreadPoolExecutor(len(sizes)) as pool:
+        got = list(pool.map(steps, sizes))
+    for batch, (short, left, slot) in zip(sizes, got):
+        # the last request's last token is the first of its new block, the batch-th from the top
+        assert short == 0 and left == 8192 - batch and slot == (8192 - batch) * 16
