@@ -19,6 +19,7 @@ DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libsta_debug.so")
 
 TORCH_PATH = os.path.join(PKG_DIR, "_sta_torch.so")
 TORCH_SOURCE = os.path.join(CSRC, "sta_torch.cpp")
+TORCH_STAMP = os.path.join(PKG_DIR, "_sta_torch.stamp")  # the torch_key that _sta_torch.so was built for
 
 SOURCES = ["sta_api.cu", "sta_permute.cu", "sta_forward.cu", "sta_backward.cu", "sta_search.cu", "sta_pipe.cu", "sta_noalloc.cu",
            "sta_packed_lists.cu", "sta_packed.cu", "sta_packed_pair.cu",
@@ -58,19 +59,29 @@ def _compile(path: str, extra, verbose: bool):
     os.replace(tmp, path)
 
 
+def torch_key() -> str:
+    """The PyTorch and Python whose ABI _sta_torch.so has to be built for."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def _torch_command(out: str):
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     inc = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-            *[a for i in inc for a in ("-isystem", i)], TORCH_SOURCE, "-o", out, "-L", os.path.join(torch_dir, "lib"),
+            f'-DSTA_TORCH_KEY="{torch_key()}"', *[a for i in inc for a in ("-isystem", i)], TORCH_SOURCE, "-o", out, "-L", os.path.join(torch_dir, "lib"),
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
 def _torch_up_to_date() -> bool:
-    return os.path.exists(TORCH_PATH) and all(os.path.getmtime(f) <= os.path.getmtime(TORCH_PATH)
-                                              for f in (TORCH_SOURCE, os.path.join(INCLUDE, "sta.h")))
+    if not os.path.exists(TORCH_PATH) or not os.path.exists(TORCH_STAMP):
+        return False
+    with open(TORCH_STAMP) as f:
+        if f.read() != torch_key():
+            return False
+    return all(os.path.getmtime(f) <= os.path.getmtime(TORCH_PATH) for f in (TORCH_SOURCE, os.path.join(INCLUDE, "sta.h")))
 
 
 def _build_torch(verbose: bool):
@@ -80,6 +91,8 @@ def _build_torch(verbose: bool):
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, TORCH_PATH)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(torch_key())
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:

@@ -21,10 +21,32 @@ from typing import NamedTuple
 
 import torch
 
-try:
-    from . import _sta_torch as _torch
-except ImportError as e:
-    raise ImportError(f"{e}; build _sta_torch.so with `python sparse_attention_video_sta_b200/_build.py`") from e
+from ._build import torch_key
+
+
+class _Missing:
+    """Stands for a ``_sta_torch.so`` that is not there or is another PyTorch's or Python's: the calls of this part
+    say so, the others need only libsta."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self._why}; build _sta_torch.so with `python sparse_attention_video_sta_b200/_build.py`")
+
+
+def _load():
+    try:
+        from . import _sta_torch
+    except ImportError as e:
+        return _Missing(str(e))
+    built_for = getattr(_sta_torch, "built_for", "another version of this package")
+    if built_for != torch_key():
+        return _Missing(f"_sta_torch.so was built for {built_for}, this is {torch_key()}")
+    return _sta_torch
+
+
+_torch = _load()
 
 __all__ = [
     "sta_packed_forward", "sta_packed_backward", "sta_packed_attention", "sta_packed_attention_backward",
@@ -78,7 +100,8 @@ def bind(lib, check) -> None:
     }.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = args, ctypes.c_int
-    _torch.bind({name: ctypes.cast(getattr(lib, name), vp).value for name in SYMBOLS}, check)
+    if not isinstance(_torch, _Missing):
+        _torch.bind({name: ctypes.cast(getattr(lib, name), vp).value for name in SYMBOLS}, check)
 
 
 def _raw(stream) -> int:

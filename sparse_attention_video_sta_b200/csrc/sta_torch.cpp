@@ -338,6 +338,7 @@ void bind(const py::dict& at, const py::object& check_) {
 }  // namespace
 
 PYBIND11_MODULE(_sta_torch, m) {
+    m.attr("built_for") = STA_TORCH_KEY;
     m.def("bind", &bind);
     m.def("packed_forward", &packed_forward);
     m.def("packed_attention", &packed_attention);

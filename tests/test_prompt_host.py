@@ -143,3 +143,64 @@ def test_cache_attention_without_sequences():
     assert att(0) == OK and att(0, q=None, o=None, lse=None, ws=None) == OK
     for kw in (dict(q=None), dict(o=rows(data=P + 8)), dict(lse=None), dict(lse=P + 2), dict(ws=None), dict(ws=P + 16)):
         assert att(1, **kw) == INV, kw
+
+
+def run(code):
+    import os
+    import subprocess
+    import sys
+    return subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+MISSING = {
+    "not there": 'sys.modules["sparse_attention_video_sta_b200._sta_torch"] = None',
+    "of another torch": """
+import types
+m = types.ModuleType("sparse_attention_video_sta_b200._sta_torch")
+m.built_for, m.bind = "torch 1.0, cpython-30", None
+sys.modules[m.__name__] = m""",
+    "of an older package": """
+import types
+m = types.ModuleType("sparse_attention_video_sta_b200._sta_torch")
+sys.modules[m.__name__] = m""",
+}
+
+
+@pytest.mark.parametrize("how", MISSING)
+def test_without_the_compiled_binding_the_other_calls_work(how):
+    """The package loads and plans; a call that needs _sta_torch.so says that it is missing and how to build it."""
+    r = run(f"""
+import sys
+{MISSING[how]}
+import torch
+import sparse_attention_video_sta_b200 as sta
+with sta.sta_plan_host((12, 16, 16), (6, 8, 8), 1, 2, [(6, 8, 8)] * 2) as plan:
+    assert plan.query(0, 0) == [0]
+assert sta._lib.sta_packed_workspace(None, 0, None) == sta.STA_ERR_INVALID_ARG
+t = torch.zeros(1, 1, 64)
+for call in (lambda: sta.sta_packed_attention(t, t, t, t), lambda: sta.sta_cache_append(t, t, t, t, t, t, t),
+             lambda: sta.StaPackedAttention.apply(t, t, t, t)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_build.py" in str(e) and "_sta_torch" in str(e), e
+    else:
+        raise SystemExit("no error")
+print("fine")
+""")
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-3000:]
+
+
+def test_the_compiled_binding_is_built_again_for_another_torch_or_python(tmp_path, monkeypatch):
+    from sparse_attention_video_sta_b200 import _build, _sta_torch
+    key = _build.torch_key()
+    assert _sta_torch.built_for == key
+    monkeypatch.setattr(_build.os.path, "getmtime", lambda f: 1.0)  # sources and library of the same age
+    monkeypatch.setattr(_build, "TORCH_STAMP", str(tmp_path / "stamp"))
+    assert not _build._torch_up_to_date()
+    (tmp_path / "stamp").write_text(key)
+    assert _build._torch_up_to_date()
+    monkeypatch.setattr(_build, "torch_key", lambda: "torch 99.0, cpython-399")
+    assert not _build._torch_up_to_date()
+    assert any("torch 99.0" in a for a in _build._torch_command("x.so"))
