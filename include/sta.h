@@ -476,8 +476,9 @@ typedef struct {
  * codes no longer count).  NaN stays NaN; an infinity sets e = 120.
  * The tokens of one block stand next to each other in `slots`, in rising order
  * (as sta_cache_extend writes them), and the caller lets no two blocks' runs
- * name the same block.  A slot outside the pool is skipped and reported by
- * sta_operator_status as BOUNDS.  One kernel, no workspace. */
+ * name the same block.  A slot named twice keeps the later token.  A slot outside
+ * the pool is skipped, and so are a run's tokens past the first block_tokens;
+ * both are reported by sta_operator_status as BOUNDS.  One kernel, no workspace. */
 STA_API sta_status sta_cache_append(const sta_cache* c, const sta_rows* k, const sta_rows* v, int64_t tokens,
                                     const int64_t* slots, void* stream);
 

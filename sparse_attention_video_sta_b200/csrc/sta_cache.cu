@@ -109,7 +109,7 @@ cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* 
         const int64_t* mine = sh_slot + (t - t0 + 1);
         const int64_t blk = mine[0] >> kLog2;
         // ---- the run's length and offsets
-        if (tid == 0) sh_n = BT;
+        if (tid == 0) sh_n = BT + 1;
         __syncthreads();
         bool odd = false;
         for (int i = tid; i < BT + 1; i += kAppendThreads) {
@@ -120,7 +120,9 @@ cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* 
             if (in && i > 0 && si != mine[i - 1] + 1) odd = true;  // (past the run's end this may be said in vain)
         }
         const bool in_order = !__syncthreads_or(odd);
-        const int n = sh_n;
+        // (a run longer than a block names slots twice: what is past a block's worth is left out, and reported)
+        const int n = min(sh_n, BT);
+        if (sh_n > BT && tid == 0) atomicOr(status, kDevBounds);
         const int col = (tid % kPer) * 8, j0 = tid / kPer;
         uint4 raw[kPasses];
         const __nv_bfloat16* src = x.p + (t + j0) * x.ts + h * x.hs + col;
@@ -188,7 +190,9 @@ cache_append_kernel(sta_cache c, Rows k, Rows v, int64_t tokens, const int64_t* 
         } else {  // a scale that the caller set, or slots out of order: small code, the values read again
 #pragma unroll 1
             for (int j = j0; j < n; j += kStep) {
-                if (j + 1 < n && sh_off[j + 1] == sh_off[j]) continue;  // a slot named twice in a row keeps the later token
+                bool again = false;  // a slot named twice keeps the later token
+                for (int i = j + 1; i < n; ++i) again |= sh_off[i] == sh_off[j];
+                if (again) continue;
                 const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + (j - j0) * x.ts));
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
                 float y[8];

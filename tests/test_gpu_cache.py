@@ -702,3 +702,36 @@ def test_extend_from_several_threads_at_once(sta):
     for batch, (short, left, slot) in zip(sizes, got):
         # the last request's last token is the first of its new block, the batch-th from the top
         assert short == 0 and left == 8192 - batch and slot == (8192 - batch) * 16
+
+
+@pytest.mark.parametrize("before", [0, 1, 15, 40])
+@pytest.mark.parametrize("bt,d", [(16, 64), (32, 128), (128, 128)])
+def test_append_slots_named_twice(sta, bt, d, before):
+    """Slots of a block named again keep the later token, wherever in the run; a run longer than a block is cut at
+    one block's worth and reported."""
+    K, blocks = 2, 60
+    for extra in (0, 1, 2 * bt):  # tokens past a block's worth
+        names = [3, 3] + list(range(4, bt)) + [3, 7]
+        names = (names + [5] * (bt + extra))[:bt + extra]
+        slots = [(10 + i) * bt for i in range(before)] + names + [5 * bt, 5 * bt + 1]
+        # many tokens of other blocks behind, so that more than one range is taken
+        slots += [6 * bt + i for i in range(bt)] + [-1] * 9
+        g = torch.Generator("cuda").manual_seed(bt + before)
+        x = torch.randn(len(slots), K, d, generator=g, device="cuda").bfloat16()
+        kc, vc, ks, vs = empty_cache(blocks, K, bt, d)
+        sta.sta_cache_append(x, -x, torch.tensor(slots, dtype=torch.int64, device="cuda"), kc, vc, ks, vs)
+        assert sta.sta_operator_status() == (sta.STA_ERR_BOUNDS if extra else 0)
+        taken = {s: i for i, s in list(enumerate(slots))[before:before + bt]}
+        taken.update({s: i for i, s in enumerate(slots) if s >= bt})
+        for codes, scales, sign in ((kc, ks, 1), (vc, vs, -1)):
+            got = values(codes, scales).transpose(1, 2).reshape(blocks * bt, K, d)
+            for b in sorted({s // bt for s in taken}):
+                mine = [s for s in taken if s // bt == b]
+                used = range(before, before + bt) if b == 0 else [taken[s] for s in mine]
+                for h in range(K):
+                    scale = ref.scale_of(max(float(x[i, h].abs().max()) for i in used))
+                    assert float(scales[b, h]) == scale
+                    for s in mine:
+                        assert torch.equal(got[s, h], ref.e4m3(sign * x[taken[s], h].double() / scale) * scale)
+            rest = sorted(set(range(blocks * bt)) - set(taken))
+            assert not bool(got[rest].any())
