@@ -809,6 +809,9 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else {
         // ------------------------------------------------------- elementwise
         const int h = warp >> 2;  // which 32 query columns
+        // Is this part's last column a row that no box fills?  Those are zeros, and so are their products with a
+        // key or value, or NaN where that is not finite: the last column says so for all of them.
+        const bool gap = rows_used < 32 * h + 32;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
         const uint64_t c2 = ptx::f2(p.scale_log2, p.scale_log2);
@@ -896,7 +899,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         pr[4 * i + 3] = ptx::ex2(x3);
                     }
                 }
-                if (masked)
+                if (masked || (gap && __any_sync(~0u, pr[31] != pr[31])))
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (i < from || i >= to) pr[i] = 0.0f;
@@ -939,7 +942,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         pk[2 * i] = ptx::pack_bf16x2(t0, t1);
                         pk[2 * i + 1] = ptx::pack_bf16x2(t2, t3);
                     }
-                    if (masked)  // (selected last: dP and D of a row may be anything)
+                    if (masked || (gap && __any_sync(~0u, (pk[15] & 0x7f800000u) == 0x7f800000u)))  // (selected last: dP and D of a row may be anything)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             if (2 * i < from || 2 * i >= to) pk[i] &= 0xffff0000u;

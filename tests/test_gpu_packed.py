@@ -561,3 +561,26 @@ def test_rows_before_the_first_sequence_are_no_ones(sta, lens_q, lens_k, H, K, d
                 a, b = a.t(), b.t()
             assert torch.equal(a[n:], b[n:]), name
             assert bool((a[:n] == (7.0 if not clear else -math.inf if name == "lse" else 0.0)).all()), name
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,K,d,n", [(24, 8, 128, 300), (10, 2, 64, 300), (100, 1, 64, 9), (2, 2, 128, 300)])
+def test_keys_of_no_weight_have_no_gradient(sta, H, K, d, n, causal, what):
+    """Keys whose scores are -inf (and then their values, zeros or not) leave dK and dV of their own rows zero, also where
+    128 is no multiple of the query heads to a key head."""
+    q, k, v, do = make([n], [n], H, K, d, seed=71)
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    keys = [1, n // 2, n - 1]
+    k[keys, :, 0] = -math.inf
+    if what == "v":
+        v[keys] = 0.0
+    cu = ref.cu_of([n])
+    o, lse = sta.sta_packed_attention(q, k, v, cu, causal=causal, softmax_scale=0.1)
+    _, dk, dv = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cu, causal=causal, softmax_scale=0.1)
+    assert bool(o.isfinite().all()) and not bool(dk[keys].any()) and not bool(dv[keys].any())
+    if not causal:
+        rest = [i for i in range(n) if i not in keys]
+        want = ref.packed(q, k[rest], v[rest], [n], [n - 3], False, 0.1, do)
+        for name, t in (("o", o), ("lse", lse), ("dk", dk[rest]), ("dv", dv[rest])):
+            ref.check(t, want, name)
