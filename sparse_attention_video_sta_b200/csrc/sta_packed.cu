@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -72,8 +73,8 @@ uint32_t* g_status_ptr[kMaxDevices] = {};
 // (warp-uniform test) runs without a mask; in the others scores from the limit
 // on become -inf before any arithmetic, so what they were (NaN, inf) is
 // forgotten.  Every row that sees a key sees key 0, in half A of chunk 0, so the
-// first chunk sets its maximum; a row without keys gets a stand-in of 0 and ends
-// with l = 0.  Rows past the block's tokens hold whatever the box brought: they
+// first chunk sets its maximum; a row without keys, or with scores of -inf alone so far,
+// gets a stand-in below any other score, and one that stays so ends with l = 0.  Rows past the block's tokens hold whatever the box brought: they
 // are never stored, and never start the slow path.
 // Bound like the video forward: MUFU exponentials and the tensor pipe nearly level at d = 128
 // (16384 causal tokens, 24 / 8 heads: 1.65-1.7 ms, 970-1000 TFLOP/s over the visible pairs, tensor pipe
@@ -482,7 +483,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     const float mx = fmaxf(*x_mine, *x_other);
                     float alpha = 1.0f;
                     if (i == 0) {
-                        m_used = mx == -INFINITY ? 0.0f : mx;  // no key yet: a finite stand-in
+                        m_used = mx == -INFINITY ? p.nothing_yet : mx;  // (no key, or scores of -inf alone)
                     } else if ((mx - m_used) * c > 0.0f) {
                         alpha = ptx::ex2((m_used - mx) * c);
                         m_used = mx;
@@ -687,6 +688,7 @@ cudaError_t launch_fwd(const PackedProblem& p, const Rows& q, const Rows& k, con
     if (e == cudaSuccess) e = packed::rows_map(&mv, v, p.tokens_k, p.kv_heads, D, 1, 128);
     if (e != cudaSuccess) return e;
     FwdParams fp{view, p, self ? 1 : 0, p.kv_heads, p.group, p.causal, p.tokens_q, o, v, lse, p.scale, p.scale * 1.4426950408889634f,
+                 -3.0e38f / std::max(p.scale * 1.4426950408889634f, 1.0f),
                  uint32_t(p.group * tpb) * 128u, p.status, p.waits.timeout_ns};
     constexpr int kSmem = Cfg<D>::kSmemBytes;
     const int64_t items = w.max_wq * p.kv_heads;

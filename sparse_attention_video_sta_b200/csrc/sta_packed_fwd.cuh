@@ -32,6 +32,10 @@ struct FwdParams {
     Rows vals;  // V
     float* lse;
     float scale, scale_log2;
+    // The running maximum m of a row that has seen no score above -inf: finite, so that exp2(S c - m c) of such a
+    // score is 0 (c = scale_log2), and m or m c at the end of fp32's range (0 would hide scores below -126 / c
+    // that come later).
+    float nothing_yet;
     uint32_t q_box_bytes;  // bytes of one box of a query block: group * (128 / group) rows of 128 bytes
     uint32_t* status;
     uint64_t timeout_ns;

@@ -436,7 +436,7 @@ packed_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 }
                 float alpha = 1.0f;
                 if (i == 0) {
-                    m = mx == -INFINITY ? 0.0f : mx;  // no key: a finite stand-in
+                    m = mx == -INFINITY ? p.nothing_yet : mx;  // (no key, or scores of -inf alone)
                 } else if (real && (mx - m) * c > kRise) {
                     alpha = ptx::ex2((m - mx) * c);
                     m = mx;

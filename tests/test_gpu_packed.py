@@ -584,3 +584,27 @@ def test_keys_of_no_weight_have_no_gradient(sta, H, K, d, n, causal, what):
         want = ref.packed(q, k[rest], v[rest], [n], [n - 3], False, 0.1, do)
         for name, t in (("o", o), ("lse", lse), ("dk", dk[rest]), ("dv", dv[rest])):
             ref.check(t, want, name)
+
+
+@pytest.mark.parametrize("hidden", [128, 300])
+@pytest.mark.parametrize("n,m,H,K,d,causal", [
+    (400, 400, 4, 2, 64, True), (400, 500, 4, 4, 128, False), (1100, 1100, 24, 8, 128, True), (3500, 3500, 12, 12, 64, True),
+    (5, 9000, 2, 1, 64, True), (40, 9000, 4, 1, 128, False)])
+def test_first_keys_whose_scores_are_minus_infinity(sta, n, m, H, K, d, causal, hidden):
+    """The first chunks' scores are all -inf, the others far below zero: the results are those over the others alone,
+    in both forward kernels and in split walks."""
+    q, k, v, do = make([n], [m], H, K, d, seed=61)
+    q[..., 0] = 1.0
+    q[..., 1], k[..., 1] = 40.0, -100.0  # scores of -400, 2^-577
+    k[..., 0] = 0.0
+    k[:hidden, :, 0] = -math.inf
+    scale, cq, ck = 0.1, ref.cu_of([n]), ref.cu_of([m])
+    want = ref.packed(q, k[hidden:], v[hidden:], [n], [m - hidden], causal, scale, do)
+    o, lse = sta.sta_packed_attention(q, k, v, cq, ck, causal=causal, softmax_scale=scale)
+    ref.check(o, want, "o")
+    ref.check(lse, want, "lse")
+    _, dk, dv = sta.sta_packed_attention_backward(q, k, v, o, lse, do, cq, ck, causal=causal, softmax_scale=scale)
+    ref.check(dk[hidden:], want, "dk")
+    ref.check(dv[hidden:], want, "dv")
+    assert not bool(dk[:hidden].any()) and not bool(dv[:hidden].any())
+    assert sta.sta_operator_status() == 0
