@@ -161,13 +161,12 @@ __device__ __forceinline__ void self_clear(const PackedProblem& p, int head_dim,
     const int32_t none = first + p.tokens_q - last, parts = head_dim / 8;
     for (int64_t i = int64_t(blockIdx.x) * 32 + lane; i < int64_t(none) * p.heads * parts; i += int64_t(gridDim.x) * 32) {
         const int64_t row = i / parts;
-        const int32_t nth = int32_t(row / p.heads), h = int32_t(row % p.heads);
-        const int32_t tok = nth < first ? nth : last + nth - first;
-        *reinterpret_cast<uint4*>(o.p + tok * o.ts + h * o.hs + i % parts * 8) = make_uint4(0u, 0u, 0u, 0u);
-        if (i % parts == 0) lse[int64_t(h) * p.tokens_q + tok] = -INFINITY;
+        const int32_t nth = int32_t(row / p.heads), h = int32_t(row - int64_t(nth) * p.heads);
+        const int32_t tok = nth + (nth < first ? 0 : last - first);
+        *reinterpret_cast<uint4*>(o.p + tok * o.ts + h * o.hs + (i - row * parts) * 8) = make_uint4(0u, 0u, 0u, 0u);
+        if (i == row * parts) lse[int64_t(h) * p.tokens_q + tok] = -INFINITY;
     }
 }
-
 
 // The same pieces for 32 scores, sr[kAt] .. sr[kAt + 31].
 template <int kAt>
