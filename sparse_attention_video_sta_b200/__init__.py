@@ -28,6 +28,8 @@ serving over a paged 8-bit cache.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import math
 import os
 
@@ -180,6 +182,31 @@ def _device(tensors, plan=None) -> torch.device:
     if len(idx) != 1:
         raise ValueError(f"tensors and plan must be on one CUDA device (got devices {sorted(idx)})")
     return torch.device("cuda", idx.pop())
+
+
+def _allocates(call):
+    """For calls that make new tensors: ``stream`` is current meanwhile, so that their memory is from the pool of the
+    stream that uses it (a block that another stream has just given back may still be in use there).  What they
+    return may be used and dropped on the caller's current stream."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        dev = None if stream is None else next((t.device for t in (*args, *kw.values())
+                                                if isinstance(t, torch.Tensor) and t.is_cuda), None)
+        if dev is None:
+            return call(*args, **kw)
+        before, handle = torch.cuda.current_stream(dev), _stream(stream).value or 0
+        if handle == before.cuda_stream:
+            return call(*args, **kw)
+        side = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(side):
+            out = call(*args, **kw)
+        for t in out if isinstance(out, tuple) else ():
+            t.record_stream(before)
+        return out
+    return run
 
 
 def _windows(heads: int, windows) -> ctypes.Array:
@@ -443,6 +470,7 @@ def _backward_call(fn, what: str, plan: Plan, q, k, v, o, lse, dout, softmax_sca
     return dq, dk, dv
 
 
+@_allocates
 def sta_backward(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                  lse: torch.Tensor, dout: torch.Tensor, softmax_scale: float, dq=None, dk=None, dv=None,
                  workspace=None, stream=None):
@@ -453,6 +481,7 @@ def sta_backward(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
                           dq, dk, dv, workspace, stream, raster=False)
 
 
+@_allocates
 def sta_backward_raster(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                         lse: torch.Tensor, dout: torch.Tensor, softmax_scale: float, dq=None, dk=None, dv=None,
                         workspace=None, stream=None):
@@ -517,6 +546,7 @@ def sta_debug_inject_timeout(mode, limit_ms: int = 50) -> None:
     _check(_lib.sta_debug_inject_timeout(int(mode), int(limit_ms)), "sta_debug_inject_timeout")
 
 
+@_allocates
 def sta_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: Plan,
                   softmax_scale: float | None = None, stream=None, fused: bool = True):
     """STA attention on raster-order ``[B, H, N, d]`` bf16 tensors.
@@ -547,6 +577,7 @@ def sta_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: Plan,
     return o, lse
 
 
+@_allocates
 def sta_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                            lse: torch.Tensor, dout: torch.Tensor, plan: Plan,
                            softmax_scale: float | None = None, stream=None, fused: bool = True):
@@ -597,6 +628,7 @@ class StaAttention(torch.autograd.Function):
         return dq, dk, dv, None, None
 
 
+@_allocates
 def sta_window_stats(lse_w: torch.Tensor, lse_full: torch.Tensor, o_w: torch.Tensor, o_full: torch.Tensor,
                      stream=None):
     """Per-(b, h) attention recall (mean of exp(lse_w - lse_full)) and output
@@ -620,6 +652,7 @@ def sta_window_stats(lse_w: torch.Tensor, lse_full: torch.Tensor, o_w: torch.Ten
     return recall, mse
 
 
+@_allocates
 def sta_window_search(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, latent, tile, candidates,
                       softmax_scale: float | None = None, max_mse: float | None = None,
                       min_recall: float | None = None, stream=None) -> dict:

@@ -108,3 +108,58 @@ def test_tensors_on_another_device_than_the_plan_are_rejected(sta):
     finally:
         plan.device = real
     assert sta.sta_last_device_status(plan) == 0
+
+
+def test_new_memory_of_a_call_on_another_stream(sta):
+    """Outputs and scratch of calls with `stream=` (by name or by position) are not blocks that the current stream has
+    just given back with work queued on them; a search with `stream=` reads its statistics behind its kernels."""
+    w = sta_inputs.WORKLOADS[1]
+    wins = sta_inputs.windows(w).tolist()
+    q, k, v, do = _inputs(w, 7)
+    plan = sta.sta_plan(w.latent, w.tile, w.batch, w.heads, wins)
+    o, lse = sta.sta_attention(q, k, v, plan, w.softmax_scale)
+    full = sta.sta_plan(w.latent, w.tile, w.batch, w.heads, [w.latent] * w.heads)
+    o_full, lse_full = sta.sta_attention(q, k, v, full, w.softmax_scale)
+    side = torch.cuda.Stream()
+    scale = w.softmax_scale
+    calls = [
+        lambda s: sta.sta_attention(q, k, v, plan, scale, s),
+        lambda s: sta.sta_attention(q, k=k, v=v, plan=plan, softmax_scale=scale, stream=s, fused=False),
+        lambda s: sta.sta_attention_backward(q, k, v, o, lse, do, plan, scale, stream=s),
+        lambda s: sta.sta_attention_backward(q, k, v, o, lse, do, plan, scale, stream=s, fused=False),
+        lambda s: sta.sta_backward_raster(plan, q, k, v, o, lse, do, scale, stream=s),
+        lambda s: sta.sta_window_stats(lse, lse_full, o, o_full, s),
+    ]
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        call(side)
+        torch.cuda.synchronize()
+        for stream in (side, side.cuda_stream):
+            spots = [torch.empty(n, dtype=torch.uint8, device="cuda")
+                     for n in [t.numel() * t.element_size() for t in want] * 2 + [1 << i for i in range(9, 26)]]
+            used = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in spots]
+            torch.cuda._sleep(400_000_000)
+            for t in spots:
+                t.fill_(0x7f)
+            del spots, t
+            got = call(stream)
+            side.synchronize()
+            assert not torch.cuda.current_stream().query()
+            for t in got:
+                a = t.data_ptr()
+                assert not any(a < hi and lo < a + t.numel() * t.element_size() for lo, hi in used)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        with torch.cuda.stream(side):
+            got = call(0)
+            assert torch.cuda.current_stream() == side
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    cands = [w.latent, wins[0]]
+    want = sta.sta_window_search(q, k, v, w.latent, w.tile, cands)
+    got = sta.sta_window_search(q, k, v, w.latent, w.tile, cands, stream=side)
+    assert got["windows"] == want["windows"] and (got["mse"] == want["mse"]).all() and (got["recall"] == want["recall"]).all()
+    with pytest.raises(ValueError):
+        sta.sta_attention(q.float(), k, v, plan, scale, stream=side)
+    plan.destroy()
+    full.destroy()
