@@ -64,7 +64,7 @@ __device__ uint2 codes8(const float (&x)[8]) {
 // registers between the reduction of their maximum and their rounding, so each
 // is read once: 128 threads hold a block of 128 tokens x 128 in 64 registers.
 // Bound by HBM: 2 bytes read and 1 written for each value.  22600 prompt tokens, 8 key heads, d = 128
-// (139 MB): 29 us, 4.7 TB/s.  Instructions count here: the maximum and the scaling on pairs of bf16, one
+// (139 MB): 27.4 us, 5.1 TB/s.  Instructions count here: the maximum and the scaling on pairs of bf16, one
 // multiplication where the scale is a power of two (a division compiled beside it took 10 us), and
 // addresses without a lookup where a run's slots follow one another: 45 us before these three.
 template <int D, int BT>
@@ -301,7 +301,7 @@ __device__ void each_of(int n, Get get, Put put) {
 // pushes, meet, and share the tables and slots.  The reads of `len` and `count`
 // come before the cluster's meeting and their writes after it, so the outputs
 // may be the inputs.  Latency-bound: one launch in place of a chain of scans (64 requests, one token
-// each: 6.6 us a call, nearly all of it the host's; 500 requests with 121000 new tokens: 11 us).  Its steps
+// each: 6.8 us a call, nearly all of it the host's; 500 requests with 121000 new tokens: 9.7 us).  Its steps
 // are round trips: loads go four at a time, the three sums share their barriers, and a warp
 // finds the requests of its 128 slots by ballots (a binary search in each thread: 20 us).
 __global__ void __launch_bounds__(kExtendThreads) cache_extend_kernel(const ExtendParams p) {
@@ -441,8 +441,8 @@ cudaError_t extend_most_smem() {
     return cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, extend_smem(kMaxRequests));
 }
 
-// A cluster of 16 where the device has one (the SMs of a GPC; 500 requests, 121000 new tokens: 11 us, with 8
-// CTAs 14.6); asked once for each device.  (The kernel's attribute belongs to the device as well.)
+// A cluster of 16 where the device has one (the SMs of a GPC; 500 requests, 121000 new tokens: 11 us when this was
+// chosen, with 8 CTAs 14.6); asked once for each device.  (The kernel's attribute belongs to the device as well.)
 cudaError_t extend_cluster(unsigned* ctas) {
     constexpr int kDevices = 64;
     static std::atomic<unsigned> known[kDevices];

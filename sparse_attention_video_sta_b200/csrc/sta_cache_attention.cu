@@ -238,8 +238,8 @@ __device__ int32_t plan_locate(const CacheArgs& a, const PlanShared& sh, int64_t
 }
 
 // One sequence alone: each of its units goes to a CTA where that leaves a warp at most so many tiles, and the
-// second kernel has nothing to join (24 / 8 heads, d = 128, one query on 1000 tokens: 17.6 us joined, 15.5 so; on 1500:
-// 18.3 / 17.9; with 12 on 2300: 16.3 / 21.4).
+// second kernel has nothing to join (24 / 8 heads, d = 128, one query on 1000 tokens: 16.4 us joined, 14.1 so; on 1500:
+// 17.1 / 16.2; with 12 on 2000: 17.0 / 18.7, on 2300: 15.3 / 19.9).
 constexpr int kAlone = 8;
 // CTAs that take part; the runs of the CTAs, or of a CTA's warps.
 __device__ __forceinline__ int64_t plan_ctas(int64_t total, int64_t most) {
@@ -348,7 +348,7 @@ __device__ __forceinline__ void join_row(int64_t s, int64_t n, int share, const 
 // which fp16 and fp32 bear and which makes rescaling O rare.  Q is scaled by a power of two
 // for each row into fp16's range.
 // HBM-bound: 2 D bytes for each token and key head.  64 requests of 500-8000 tokens, 24 / 8 heads, d = 128
-// (313 MB): 71 us a call, 4.4 TB/s: the plan, the first copies' latency, the joins and 5.4 TB/s of
+// (313 MB): 72 us a call, 4.3 TB/s: the plan, the first copies' latency, the joins and 5.4 TB/s of
 // 2 KB boxes between them (leaving the products out saved 7 of 77 us when it took that).
 template <int D, int NT>
 struct Cfg {
@@ -805,7 +805,7 @@ cache_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     }
     // (one warp for each row of each such unit)
     const float* parts0 = a.warp_parts + int64_t(blockIdx.x) * kWarps * kRows * (D + 4);
-    // lane i < 16: does warp i's run begin inside of a unit, does it leave one unfinished
+    // lane i < warps: does warp i's run begin inside of a unit, does it leave one unfinished
     const int64_t began = lane < warps ? ends[lane][0].unit0 : -1, left = lane < warps ? ends[lane][1].unit0 : -1;
     const uint32_t starts = __ballot_sync(~0u, left >= 0) << 1 | (__shfl_sync(~0u, began, 0) >= 0 ? 1u : 0u);
     int turn = 0;

@@ -77,8 +77,8 @@ uint32_t* g_status_ptr[kMaxDevices] = {};
 // gets a stand-in below any other score, and one that stays so ends with l = 0.  Rows past the block's tokens hold whatever the box brought: they
 // are never stored, and never start the slow path.
 // Bound like the video forward: MUFU exponentials and the tensor pipe nearly level at d = 128
-// (16384 causal tokens, 24 / 8 heads: 1.65-1.7 ms, 970-1000 TFLOP/s over the visible pairs, tensor pipe
-// active 66 %, MUFU 55 %; what is left is the chunk's round trips and the board's power cap);
+// (16384 causal tokens, 24 / 8 heads: 1.63-1.7 ms, 970-1010 TFLOP/s over the visible pairs; tensor pipe and
+// MUFU 56 % each under a profiler's higher clock; what is left is the chunk's round trips and the board's power cap);
 // causal blocks lose the masked part of their last chunks.  Skipping the exponentials of a
 // wholly masked half was tried: the extra path in the loop cost 4-8 % and saved less.
 template <int D>

@@ -79,7 +79,7 @@ inline int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 // Split where every SM would get fewer than two blocks: with more, the longest walks first
 // level the SMs nearly by themselves (a long sequence has many blocks), and the parts' sums
 // cost what they save.  (Six sequences of 342-2047 tokens, 16 / 2 heads, d = 64: dK / dV
-// 227 us whole, 75 split, plus the sums; one of 8192 tokens, 24 / 8 heads, d = 128, 520 blocks:
+// 227 us whole, 66 split, plus 10 for the sums; one of 8192 tokens, 24 / 8 heads, d = 128, 520 blocks:
 // 730 whole, 848 split.)
 inline Layout layout(const PackedProblem& p, bool backward, int head_dim, int sms) {
     Layout w{};

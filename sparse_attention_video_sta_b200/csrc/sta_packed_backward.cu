@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedProblem p,
 }
 
 // ---------------------------------------------------------------- dQ
-// Three products for each chunk (S, dP, dQ).  8192 causal tokens, 24 / 8 heads, d = 128: 535 us,
-// 1.16 PFLOP/s of products, tensor pipe active 70 %; the rest is the chain dP -> dS -> dQ of a chunk,
+// Three products for each chunk (S, dP, dQ).  8192 causal tokens, 24 / 8 heads, d = 128: 563 us under a
+// profiler, 1.10 PFLOP/s of products, tensor pipe active 58 %; the rest is the chain dP -> dS -> dQ of a chunk,
 // since TMEM holds two S but one dP beside dQ.
 template <int D>
 struct DqCfg {
@@ -581,9 +581,9 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
 // ---------------------------------------------------------------- dK / dV
 // Four products for each query block (S^T, dP^T, dV, dK).  8192 causal tokens, 24 / 8 heads, d = 128:
-// 725 us, 1.14 PFLOP/s of products, tensor pipe active 66 %; S^T, dP^T, dV and dK fill TMEM, so a block's
-// exponentials (1650 of a step's 3550 cycles) wait for its scores, which wait for the P of the block before to
-// be read (750).
+// 743 us under a profiler, 1.11 PFLOP/s of products, tensor pipe active 58 %; S^T, dP^T, dV and dK fill TMEM, so a
+// block's exponentials wait for its scores, which wait for the P of the block before to be read (with eight
+// elementwise warps 1650 and 750 of a step's 3550 cycles).
 template <int D>
 struct DkvCfg {
     static constexpr int kBlk = 128 * D * 2;

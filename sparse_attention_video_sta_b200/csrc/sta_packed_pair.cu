@@ -16,7 +16,7 @@
 //
 // Masks and rows that are not there: as in sta_packed.cu; V rows that no row of the block sees are
 // cleared by the softmax warpgroup before it hands over its P.
-// Measured: 20736 queries of two videos on 226 and 100 text keys, 24 heads, d = 128: 103 us (152 one item
+// Measured: 20736 queries of two videos on 226 and 100 text keys, 24 heads, d = 128: 101-106 us (152 one item
 // at a time; 117 with the softmax warps storing O themselves; the tensors alone are 40 us of HBM).  No unit
 // is busy for more than a third of the time: an item's steps follow one another (loads, product, maximum,
 // exponentials, product), and TMEM holds no third S and O.
